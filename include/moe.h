@@ -31,6 +31,13 @@
  * plus the prefill path (whole-layer copy and grouped GEMM; FreeToken summary
  * "method steps", reader "System Architecture" ping-pong buffers).
  *
+ * The attention half of the same layer (no counterpart on the pages), over a
+ * paged key/value cache in the experts' own 4-bit form:
+ *   moe_kv_plan        block tables and slot maps from request lengths
+ *   moe_qkv_store      query/key norms, rotation and the 4-bit store
+ *   moe_kv_load        slots read back
+ *   moe_kv_attention   attention over the cache (decode and prompt chunks)
+ *
  * Conventions shared by every entry point
  *   Memory   Every pointer named *device* must point to device memory that
  *            the caller owns (for instance a torch tensor's data_ptr()).  The
@@ -106,6 +113,13 @@ enum { MOE_FORMAT_INT4 = 0, MOE_FORMAT_MXFP4 = 1, MOE_FORMAT_NVFP4 = 2 };
  * (libmoe_checked.so, compiled with -DMOE_CHECKED): a cache-table entry read
  * on the device lay outside its range and was treated as absent. */
 enum { MOE_DERR_BAD_ID = 1, MOE_DERR_WAIT = 2, MOE_DERR_RANGE = 4 };
+
+/* Device-side error bits of the key/value cache's calls, OR-ed into
+ * moe_kv_batch.err.  MOE_DERR_KV_FULL: a plan was refused (too few free
+ * blocks, a row longer than the block table, more tokens than the batch
+ * holds).  MOE_DERR_KV_INDEX: a slot, position, block id or row bound lay
+ * outside its range; the entry was skipped. */
+enum { MOE_DERR_KV_FULL = 8, MOE_DERR_KV_INDEX = 16 };
 
 /* Model description (Edge0 §3 "MoESpec": expert count, routing family,
  * quantisation, layout). */
@@ -482,6 +496,185 @@ size_t moe_profile_workspace_bytes(const moe_spec* spec);
 int moe_profile_bandwidths(const moe_spec* spec, const moe_cache* cache, int32_t layer,
                            void* workspace, size_t workspace_bytes, int32_t reps,
                            int32_t* bp_mbps, int32_t* bh_mbps, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit key/value cache.  No counterpart on the pages: the attention half
+ * of the decoder layer whose MoE half the calls above run.  Keys and values
+ * live in fixed blocks of one pool per layer, quantised as the int4 experts
+ * are (affine, groups of 64 columns), so that the memory a budget leaves for
+ * expert slots (moe_slots_for_budget) is not spent on the context.
+ *
+ * Blocks, rows, slots: a block holds block_tokens (P) tokens; row b of the
+ * block table lists the blocks of one request, token position p of it lives in
+ * slot block_table[b][p / P] * P + p % P.  The tables (block_table, seq_len,
+ * free_list, free_count) are shared by all layers; a model of several layers
+ * copies the struct once per layer with that layer's `pool`, and plans once
+ * per step.
+ *
+ * Pool layout: block i starts at i * moe_kv_block_bytes; in it come the kv
+ * heads, each as P / 16 tiles of 16 tokens.  A tile (18 * D bytes, D =
+ * head_dim, G = D / 64) is
+ *   K codes [16][D/2] | V codes [16][D/2]                               (u8)
+ *   K scale [16][G] | K bias [16][G] | V scale [G][16] | V bias [G][16] (fp16)
+ * two codes per byte, the low nibble is the even column; the 16-byte chunk j
+ * of code row r is stored at chunk j ^ x, x = r & 7 (D = 256), (r >> 1) & 3
+ * (D = 128), (r >> 2) & 1 (D = 64).  A value is scale * code + bias, code in
+ * 0..15.
+ * ------------------------------------------------------------------------ */
+#define MOE_KV_MAX_HEADS 256 /* query heads, kv heads */
+#define MOE_KV_MAX_GROUP 64  /* query heads per kv head */
+#define MOE_ROPE_MAX_AXES 4
+
+typedef struct moe_kv {
+  int32_t num_blocks;   /* blocks in the pool; num_blocks * block_tokens < 2^31 */
+  int32_t block_tokens; /* P: 16, 32, 64 or 128 */
+  int32_t kv_heads;     /* 1..MOE_KV_MAX_HEADS */
+  int32_t head_dim;     /* D: 64, 128 or 256 */
+  int32_t max_rows;     /* rows of the block table (requests held at once) */
+  int32_t max_blocks;   /* its width; max_blocks * block_tokens < 2^31 */
+  int32_t* block_table; /* device [max_rows][max_blocks]: block id, or -1 */
+  int32_t* seq_len;     /* device [max_rows]: tokens each row holds */
+  int32_t* free_list;   /* device [num_blocks]: free block ids, a stack */
+  int32_t* free_count;  /* device [1]: entries of free_list in use */
+  void* pool;           /* device [num_blocks * moe_kv_block_bytes], 128-byte aligned */
+} moe_kv;
+
+/* A step's buffers (device): moe_kv_plan writes them, the other calls read
+ * them.  One batch serves all layers of a step. */
+typedef struct moe_kv_batch {
+  int32_t max_tokens; /* entries of slot and pos */
+  int32_t max_rows;   /* rows that kv_len and q_start are made for */
+  int32_t* q_start;   /* [max_rows + 1]: row b's new tokens are q_start[b] .. q_start[b+1] - 1 */
+  int32_t* kv_len;    /* [max_rows]: tokens of row b in the cache, the new ones among them */
+  int32_t* slot;      /* [max_tokens]: slot of each new token; -1 behind the last one */
+  int32_t* pos;       /* [max_tokens]: its position in its row; 0 behind the last one */
+  int32_t* err;       /* [1]: MOE_DERR_KV_* bits, OR-ed, never cleared by the library */
+} moe_kv_batch;
+
+/* Bytes of one block (all kv heads): kv_heads * block_tokens * head_dim * 9 / 8;
+ * 0 for an invalid shape. */
+size_t moe_kv_block_bytes(const moe_kv* kv);
+
+/* Empty the cache: block_table = -1, seq_len = 0, every block free, block 0 on
+ * top of the stack.  The pool is not touched. */
+int moe_kv_reset(const moe_kv* kv, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_plan -- one step's lengths in, block tables and slot maps out, all on
+ * the device.
+ *   new_len  device int32 [rows]: n > 0: row b takes n new tokens; n < 0: its
+ *            last -n tokens are dropped (rejected drafts; -n >= seq_len frees
+ *            the row); 0: nothing
+ *   rows     rows 0 .. rows - 1 of the block table take part
+ * First the dropped tokens' blocks go back to the free list, then the new
+ * blocks come off its end; both in (row, block) order, and so that blocks
+ * given back are taken again in that order.  A token's place is reserved, its
+ * key and value are written by moe_qkv_store.  seq_len, block_table,
+ * free_list and free_count are updated; the whole batch is written: q_start,
+ * kv_len (rows 0 .. rows - 1), slot and pos (all max_tokens entries).
+ * All or nothing: when the free blocks, the table's width or max_tokens do
+ * not suffice for every row, no row takes tokens (drops still happen), the
+ * batch is empty (q_start = 0, slot = -1) and MOE_DERR_KV_FULL is set.
+ * ------------------------------------------------------------------------ */
+int moe_kv_plan(const moe_kv* kv, const int32_t* new_len, int32_t rows, const moe_kv_batch* batch,
+                moe_stream_t stream);
+
+/* Rotary positions.  Column pair i of the first rotary_dim columns, (i, i +
+ * rotary_dim/2) or with `adjacent` (2i, 2i + 1), turns by the angle whose
+ * cosine and sine are table[p][i] and table[p][rotary_dim/2 + i]; p is the
+ * token's position on axis pair_axis[i] (one axis for text; time, height and
+ * width for images and video). */
+typedef struct moe_rope {
+  const float* table;     /* device fp32 [max_pos][rotary_dim], 16-byte aligned */
+  int32_t max_pos;        /* positions the table holds */
+  int32_t rotary_dim;     /* multiple of 16, <= head_dim; 0: no rotation */
+  int32_t adjacent;       /* 0: halves, 1: adjacent columns */
+  int32_t axes;           /* 1..MOE_ROPE_MAX_AXES */
+  uint8_t pair_axis[128]; /* axis of each of the rotary_dim/2 pairs */
+} moe_rope;
+
+/* The projections' output, bf16; strides in elements, multiples of 8, pointers
+ * 16-byte aligned; the columns of a head are contiguous (so q, k and v may be
+ * slices of one buffer, and a gate may lie between query heads). */
+typedef struct moe_qkv {
+  const void *q, *k, *v;
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int32_t q_heads;     /* 1..MOE_KV_MAX_HEADS (k and v: the cache's kv_heads) */
+  float eps;           /* of the norms, >= 0 */
+  const float* q_norm; /* device fp32 [D], 16-byte aligned, or NULL: no norm */
+  const float* k_norm; /* the same for the keys */
+} moe_qkv;
+
+/* ------------------------------------------------------------------------
+ * moe_qkv_store -- norms of queries and keys per head, rotation, and the
+ * quantised store of keys and values, in one kernel.
+ *   y = x * rsqrt(mean(x^2) + eps) * w   (q and k, where a norm is given)
+ *   then the rotation (q and k); v is stored as it is.  All in fp32.
+ *   q_out      device bf16 [T][q_heads][D], contiguous
+ *   cache      k and v of token t at batch->slot[t], straight from fp32: per
+ *              64 columns scale = fp16((max - min) / 15), bias = fp16(min),
+ *              code = round((y - bias) / scale), half to even, in 0..15 (scale
+ *              0: code 0).  Values are clamped to +-32768 first; a NaN makes
+ *              its group of 64 NaN.
+ *   positions  device int32 [axes][T], or NULL: batch->pos (one axis)
+ *   rope       NULL: no rotation
+ * Tokens with slot -1 are skipped (their q_out rows stay as they were); so are
+ * tokens whose slot or position lies outside the pool or the table, with
+ * MOE_DERR_KV_INDEX set.  Two tokens with one slot: one of them wins, which is
+ * not defined.
+ * ------------------------------------------------------------------------ */
+int moe_qkv_store(const moe_kv* kv, const moe_kv_batch* batch, const moe_rope* rope,
+                  const moe_qkv* proj, int32_t T, const int32_t* positions, void* q_out,
+                  moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_load -- slots read back: k, v bf16 [T][kv_heads][D] = scale * code +
+ * bias in fp32, rounded once (to inspect a cache, or to hand a context to a
+ * program that keeps it in another form).
+ *   slots  device int32 [T]; -1: the row is left as it was.  The same slot may
+ *          stand there more than once.
+ *   err    device int32 [1] or NULL: MOE_DERR_KV_INDEX is OR-ed in for a slot
+ *          outside the pool (its row is left as it was)
+ * ------------------------------------------------------------------------ */
+int moe_kv_load(const moe_kv* kv, const int32_t* slots, int32_t T, void* k, void* v, int32_t* err,
+                moe_stream_t stream);
+
+/* Scratch bytes moe_kv_attention needs; 0 for invalid arguments. */
+size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t T, int32_t heads,
+                                        int32_t max_new);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_attention -- causal attention of a step's new tokens over the cache.
+ * Token i of row b's n = q_start[b+1] - q_start[b] new tokens sits at position
+ * p = kv_len[b] - n + i and sees the keys 0 .. p of its row (the step's own
+ * keys among them: moe_qkv_store comes first):
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j
+ * with query head h reading kv head h / (heads / kv_heads).  Rows may mix
+ * single tokens, drafts to check and prompt chunks in one call.
+ *   q, out     device bf16 [T][heads][D], contiguous, 16-byte aligned; `out`
+ *              must not overlap `q`
+ *   T          rows of q and out (T >= q_start[rows]); rows of `out` behind
+ *              q_start[rows] stay as they were
+ *   heads      query heads, a multiple of kv_heads, at most
+ *              MOE_KV_MAX_GROUP per kv head
+ *   max_new    upper bound of n over the rows (1: a decode step)
+ *   workspace  device, >= moe_kv_attention_workspace_bytes for the same
+ *              arguments, 256-byte aligned, any contents; calls whose
+ *              execution overlaps need one each
+ * Scores, maxima, sums and accumulators are fp32; the weights enter the second
+ * product in fp16.  Results do not depend on the order in which the GPU runs
+ * its blocks.  Cache entries that no token sees (the rest of a last block,
+ * free blocks) may hold anything, NaN included.
+ * A row whose bounds are not consistent (n < 0, n > max_new, n > kv_len,
+ * kv_len beyond the block table, q_start outside 0..T) is skipped, and keys in
+ * a block whose id lies outside the pool are left out, with MOE_DERR_KV_INDEX
+ * set; an output row that is left without a single key is 0.
+ * ------------------------------------------------------------------------ */
+int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, const void* q,
+                     int32_t T, int32_t heads, int32_t max_new, float scale, void* workspace,
+                     size_t workspace_bytes, void* out, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,8 @@ MOE_ROUTER_SIGMOID_GROUP = 1
 MOE_DERR_BAD_ID = 1
 MOE_DERR_WAIT = 2
 MOE_DERR_RANGE = 4  # checked builds only (libmoe_checked.so)
+MOE_DERR_KV_FULL = 8
+MOE_DERR_KV_INDEX = 16
 
 EXPORTED = (
     "moe_last_error", "moe_version", "moe_expert_bytes", "moe_route", "moe_cache_reset",
@@ -35,6 +37,8 @@ EXPORTED = (
     "moe_layer_forward", "moe_expert_ffn_noalloc", "moe_prefill_workspace_bytes",
     "moe_layer_prefetch", "moe_expert_ffn_prefill", "moe_layer_forward_prefill",
     "moe_slots_for_budget", "moe_cache_resize_workspace_bytes", "moe_cache_resize",
+    "moe_kv_block_bytes", "moe_kv_reset", "moe_kv_plan", "moe_qkv_store", "moe_kv_load",
+    "moe_kv_attention_workspace_bytes", "moe_kv_attention",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -77,6 +81,33 @@ class MoePlan(C.Structure):
                 ("hit_slots", C.c_void_p), ("fill_ids", C.c_void_p), ("fill_slots", C.c_void_p),
                 ("evicted_ids", C.c_void_p), ("direct_ids", C.c_void_p), ("victims", C.c_void_p),
                 ("counts", C.c_void_p), ("err", C.c_void_p)]
+
+
+class MoeKv(C.Structure):
+    _fields_ = [("num_blocks", C.c_int32), ("block_tokens", C.c_int32), ("kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("max_rows", C.c_int32), ("max_blocks", C.c_int32),
+                ("block_table", C.c_void_p), ("seq_len", C.c_void_p), ("free_list", C.c_void_p),
+                ("free_count", C.c_void_p), ("pool", C.c_void_p)]
+
+
+class MoeKvBatch(C.Structure):
+    _fields_ = [("max_tokens", C.c_int32), ("max_rows", C.c_int32), ("q_start", C.c_void_p),
+                ("kv_len", C.c_void_p), ("slot", C.c_void_p), ("pos", C.c_void_p),
+                ("err", C.c_void_p)]
+
+
+class MoeRope(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("max_pos", C.c_int32), ("rotary_dim", C.c_int32),
+                ("adjacent", C.c_int32), ("axes", C.c_int32), ("pair_axis", C.c_uint8 * 128)]
+
+
+class MoeQkv(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("q_token_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("k_token_stride", C.c_int64), ("k_head_stride", C.c_int64),
+                ("v_token_stride", C.c_int64), ("v_head_stride", C.c_int64),
+                ("q_heads", C.c_int32), ("eps", C.c_float), ("q_norm", C.c_void_p),
+                ("k_norm", C.c_void_p)]
 
 
 _lib = None
@@ -146,6 +177,22 @@ def lib():
         L.moe_profile_bandwidths.restype = C.c_int
         L.moe_profile_bandwidths.argtypes = [sp, cp, i32, vp, sz, i32, C.POINTER(i32),
                                              C.POINTER(i32), vp]
+        kp, bp = C.POINTER(MoeKv), C.POINTER(MoeKvBatch)
+        L.moe_kv_block_bytes.restype = sz
+        L.moe_kv_block_bytes.argtypes = [kp]
+        L.moe_kv_reset.restype = C.c_int
+        L.moe_kv_reset.argtypes = [kp, vp]
+        L.moe_kv_plan.restype = C.c_int
+        L.moe_kv_plan.argtypes = [kp, vp, i32, bp, vp]
+        L.moe_qkv_store.restype = C.c_int
+        L.moe_qkv_store.argtypes = [kp, bp, C.POINTER(MoeRope), C.POINTER(MoeQkv), i32, vp, vp,
+                                    vp]
+        L.moe_kv_load.restype = C.c_int
+        L.moe_kv_load.argtypes = [kp, vp, i32, vp, vp, vp, vp]
+        L.moe_kv_attention_workspace_bytes.restype = sz
+        L.moe_kv_attention_workspace_bytes.argtypes = [kp, i32, i32, i32, i32]
+        L.moe_kv_attention.restype = C.c_int
+        L.moe_kv_attention.argtypes = [kp, bp, i32, vp, i32, i32, i32, C.c_float, vp, sz, vp, vp]
         _lib = L
     return _lib
 
@@ -310,6 +357,44 @@ def moe_layer_forward_prefill(spec, layer_experts, x, T, w_router, bias, shared,
                                                   _stream(stream)))
 
 
+def _ref(s):
+    return None if s is None else C.byref(s)
+
+
+def moe_kv_block_bytes(kv) -> int:
+    return int(lib().moe_kv_block_bytes(C.byref(kv)))
+
+
+def moe_kv_reset(kv, stream=None):
+    return _check(lib().moe_kv_reset(C.byref(kv), _stream(stream)))
+
+
+def moe_kv_plan(kv, new_len, rows, batch, stream=None):
+    return _check(lib().moe_kv_plan(C.byref(kv), _ptr(new_len), rows, C.byref(batch),
+                                    _stream(stream)))
+
+
+def moe_qkv_store(kv, batch, rope, proj, T, positions, q_out, stream=None):
+    return _check(lib().moe_qkv_store(C.byref(kv), C.byref(batch), _ref(rope), C.byref(proj), T,
+                                      _ptr(positions), _ptr(q_out), _stream(stream)))
+
+
+def moe_kv_load(kv, slots, T, k, v, err=None, stream=None):
+    return _check(lib().moe_kv_load(C.byref(kv), _ptr(slots), T, _ptr(k), _ptr(v), _ptr(err),
+                                    _stream(stream)))
+
+
+def moe_kv_attention_workspace_bytes(kv, rows, T, heads, max_new) -> int:
+    return int(lib().moe_kv_attention_workspace_bytes(C.byref(kv), rows, T, heads, max_new))
+
+
+def moe_kv_attention(kv, batch, rows, q, T, heads, max_new, scale, workspace, workspace_bytes,
+                     out, stream=None):
+    return _check(lib().moe_kv_attention(C.byref(kv), C.byref(batch), rows, _ptr(q), T, heads,
+                                         max_new, scale, _ptr(workspace), workspace_bytes,
+                                         _ptr(out), _stream(stream)))
+
+
 # ------------------------------------------------- device memory (plumbing)
 def make_spec(num_layers, hidden, inter, num_experts, top_k, router="softmax", n_groups=1,
               topk_groups=1, routed_scale=1.0, has_shared=False, shared_inter=None,
@@ -393,3 +478,83 @@ class DevicePlan:
             "n_direct": n_direct, "n_victims": n_vict, "now": now,
             "err": int(self.err.cpu()[0]),
         }
+
+
+class DeviceKv:
+    """The 4-bit key/value cache in device memory (torch tensors) + the C struct of each
+    layer: `layers[l]` for layer l, `c` the first one's.  All layers share the tables."""
+
+    def __init__(self, max_rows, max_blocks, num_blocks, block_tokens, kv_heads, head_dim,
+                 device="cuda", layers=1, with_pool=True):
+        import torch
+
+        def ints(*n):
+            return torch.zeros(n, dtype=torch.int32, device=device)
+
+        self.block_table, self.seq_len = ints(max_rows, max_blocks), ints(max_rows)
+        self.free_list, self.free_count = ints(num_blocks), ints(1)
+        self.block_table.fill_(-1)
+        self.free_list.copy_(torch.arange(num_blocks - 1, -1, -1, device=device))
+        self.free_count.fill_(num_blocks)
+
+        def struct(pool):
+            return MoeKv(num_blocks, block_tokens, kv_heads, head_dim, max_rows, max_blocks,
+                         _ptr(self.block_table), _ptr(self.seq_len), _ptr(self.free_list),
+                         _ptr(self.free_count), _ptr(pool))
+
+        n = moe_kv_block_bytes(struct(None))
+        if n == 0:
+            raise MoeError(MOE_EINVAL, moe_last_error())
+        self.pools = [torch.zeros((num_blocks, n), dtype=torch.uint8, device=device)
+                      if with_pool else None for _ in range(layers)]
+        self.pool = self.pools[0]
+        self.layers = [struct(p) for p in self.pools]
+        self.c = self.layers[0]
+
+
+class DeviceKvBatch:
+    """A step's slot map in device memory + the C struct (written by moe_kv_plan)."""
+
+    def __init__(self, max_tokens, max_rows, device="cuda"):
+        import torch
+
+        def ints(n, value=0):
+            return torch.full((n,), value, dtype=torch.int32, device=device)
+
+        self.q_start, self.kv_len = ints(max_rows + 1), ints(max_rows)
+        self.slot, self.pos, self.err = ints(max_tokens, -1), ints(max_tokens), ints(1)
+        self.c = MoeKvBatch(max_tokens, max_rows, _ptr(self.q_start), _ptr(self.kv_len),
+                            _ptr(self.slot), _ptr(self.pos), _ptr(self.err))
+
+
+def rope_table(max_pos, rotary_dim, base=10000.0, device="cuda"):
+    """Cosines and sines for make_rope: fp32 [max_pos][rotary_dim], pair i turning by
+    p * base^(-2 i / rotary_dim); the angles are formed in fp64, so far positions keep
+    their accuracy."""
+    import torch
+
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64, device=device)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * base ** (
+        -2.0 * i / rotary_dim)
+    return torch.cat((a.cos(), a.sin()), 1).float().contiguous()
+
+
+def make_rope(table, rotary_dim, adjacent=False, axes=1, pair_axis=None) -> MoeRope:
+    """table: device fp32 [max_pos][rotary_dim], cosines then sines of each pair."""
+    r = MoeRope(_ptr(table), table.shape[0], rotary_dim, 1 if adjacent else 0, axes)
+    for i, a in enumerate(pair_axis or []):
+        r.pair_axis[i] = a
+    r.table_tensor = table
+    return r
+
+
+def make_qkv(q, k, v, q_norm=None, k_norm=None, eps=1e-6) -> MoeQkv:
+    """q [T, heads, D], k and v [T, kv_heads, D]: bf16 device tensors whose columns are
+    contiguous (slices of one projection buffer are fine)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or t.element_size() != 2:
+            raise MoeError(MOE_EINVAL, f"{name} must be bf16 [T, heads, D] with contiguous columns")
+    p = MoeQkv(_ptr(q), _ptr(k), _ptr(v), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
+               v.stride(0), v.stride(1), q.shape[1], eps, _ptr(q_norm), _ptr(k_norm))
+    p.tensors = (q, k, v, q_norm, k_norm)
+    return p

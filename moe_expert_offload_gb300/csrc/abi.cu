@@ -287,6 +287,17 @@ size_t align256(size_t b) { return (b + 255) / 256 * 256; }
 
 }  // namespace
 
+namespace moe {
+int set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof(g_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+int set_ok() { return ok(); }
+}  // namespace moe
+
 extern "C" {
 
 const char* moe_last_error(void) { return g_err; }

@@ -1,0 +1,243 @@
+// Query/key norms, rotation and the 4-bit store in one pass over the
+// projections' output; and its reverse, reading slots back as bf16.
+//
+// Per token and head: y = x * rsqrt(mean(x^2) + eps) * w (q and k), then every
+// rotated pair (a, b) -> (a cos - b sin, b cos + a sin) at the pair's own axis'
+// position, all in fp32.  q goes out in bf16.  k and v are quantised straight
+// from fp32, per 64 columns: scale = fp16((max - min) / 15), bias = fp16(min),
+// code = round((y - bias) / scale) clamped to 0..15.
+//
+// A row of D columns is held by D / 8 lanes, 8 columns each (one 16-byte
+// load); 8 lanes are one quantisation group, whose minimum and maximum take
+// three shuffles, and a lane's eight codes are one 32-bit word.  One CTA per
+// token: a lane keeps its norm weights, cosines and sines over the heads.
+// Bound by memory.
+#include "kv_common.cuh"
+
+namespace moe {
+namespace kv {
+namespace {
+
+constexpr float kMaxValue = 32768.0f;  // what an fp16 scale and bias can hold with room to spare
+
+__device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t bf2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(bf2(x[0], x[1]), bf2(x[2], x[3]), bf2(x[4], x[5]), bf2(x[6], x[7]));
+}
+
+// The tile of (block, head, token) and the token's row in it.
+template <int D>
+__device__ __forceinline__ uint8_t* tile_of(const moe_kv& kv, int slot, int head, int& key) {
+  const int P = kv.block_tokens, at = slot % P;
+  key = at % kTile;
+  const int64_t tile = ((int64_t)(slot / P) * kv.kv_heads + head) * (P / kTile) + at / kTile;
+  return static_cast<uint8_t*>(kv.pool) + tile * tile_bytes(D);
+}
+
+// One row's 8 columns of this lane into the cache (which: 0 = K, 1 = V).  The
+// whole warp calls it (shuffles); lanes with `store` unset write nothing.
+template <int D>
+__device__ __forceinline__ void quantise_store(const float (&x)[8], uint8_t* tile, int key,
+                                               int which, int sub, bool store) {
+  float lo = kMaxValue, hi = -kMaxValue, v[8];
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    nan |= x[i] != x[i];
+    v[i] = fminf(fmaxf(x[i], -kMaxValue), kMaxValue);
+    lo = fminf(lo, v[i]);
+    hi = fmaxf(hi, v[i]);
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    lo = fminf(lo, __shfl_xor_sync(~0u, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, o));
+  }
+  const unsigned nans = __ballot_sync(~0u, nan);
+  if (!store) return;
+  __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.0f)), bh = __float2half_rn(lo);
+  const float s = __half2float(sh), b = __half2float(bh);
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float c = s > 0.0f ? rintf(__fdiv_rn(v[i] - b, s)) : 0.0f;
+    word |= (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f) << (4 * i);
+  }
+  // a NaN makes its whole group NaN
+  if (nans & (0xFFu << (threadIdx.x & 24))) sh = bh = __ushort_as_half(0x7FFFu);
+  const int chunk = (sub >> 2) ^ swizzle<D>(key);
+  *reinterpret_cast<uint32_t*>(tile + which * 8 * D + key * (D / 2) + chunk * 16 + (sub & 3) * 4) =
+      word;
+  if ((sub & 7) == 0) {
+    __half* meta = reinterpret_cast<__half*>(tile + 16 * D);
+    const int g = sub >> 3;
+    meta[which ? Meta<D>::v_scale(key, g) : Meta<D>::k_scale(key, g)] = sh;
+    meta[which ? Meta<D>::v_bias(key, g) : Meta<D>::k_bias(key, g)] = bh;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) store_kernel(StoreArgs a) {
+  constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+  const int t = blockIdx.x, sub = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+  const int slot = a.slot[t];
+  if (slot < 0) return;  // padding
+  if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
+    if (threadIdx.x == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
+    return;
+  }
+  const int H = a.proj.q_heads, K = a.kv.kv_heads, rot = a.rope.rotary_dim, half = rot / 2;
+  // this lane's cosines and (signed) sines; the partner of column c is c + half
+  // (halves) or c ^ 1 (adjacent)
+  float cs[8], sn[8];
+  const bool turns = sub * 8 < rot;
+  bool bad = false;
+  if (rot) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = sub * 8 + i;
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
+      if (turns) {
+        const int pair = a.rope.adjacent ? c >> 1 : (c < half ? c : c - half);
+        const int p = a.positions[(int64_t)a.rope.pair_axis[pair] * a.T + t];
+        if (p < 0 || p >= a.rope.max_pos) {
+          bad = true;
+        } else {
+          const float* e = a.rope.table + (int64_t)p * rot;
+          const bool second = a.rope.adjacent ? (c & 1) : c >= half;
+          cs[i] = e[pair];
+          sn[i] = second ? e[pair + half] : -e[pair + half];
+        }
+      }
+    }
+  }
+  if (__syncthreads_or(bad)) {  // a position outside the table: the token is skipped
+    if (threadIdx.x == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
+    return;
+  }
+  const int partner = (threadIdx.x & 31) - sub + (sub * 8 < half ? sub + half / 8 : sub - half / 8);
+  // rows: q heads, k heads, v heads; all lanes run the same number of rounds
+  const int total = H + 2 * K;
+  for (int h0 = 0; h0 < total; h0 += kRows) {
+    const int h = h0 + part;
+    const bool live = h < total;
+    const int which = h < H ? 0 : h < H + K ? 1 : 2;
+    const int hh = which == 0 ? h : which == 1 ? h - H : h - H - K;
+    float x[8] = {};
+    if (live) {
+      const void* base = which == 0 ? a.proj.q : which == 1 ? a.proj.k : a.proj.v;
+      const int64_t ts = which == 0 ? a.proj.q_token_stride
+                                    : which == 1 ? a.proj.k_token_stride : a.proj.v_token_stride;
+      const int64_t hs = which == 0 ? a.proj.q_head_stride
+                                    : which == 1 ? a.proj.k_head_stride : a.proj.v_head_stride;
+      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + t * ts +
+                                              hh * hs + sub * 8),
+              x);
+    }
+    const float* w = which == 0 ? a.proj.q_norm : which == 1 ? a.proj.k_norm : nullptr;
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+    if (w) {
+      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.proj.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[sub * 8 + i];
+    }
+    if (rot) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float u = x[i + 1], v = x[i];
+        if (!a.rope.adjacent) {
+          u = __shfl_sync(~0u, x[i], partner & 31);
+          v = __shfl_sync(~0u, x[i + 1], partner & 31);
+        }
+        if (which < 2 && turns) {
+          x[i] = fmaf(u, sn[i], x[i] * cs[i]);
+          x[i + 1] = fmaf(v, sn[i + 1], x[i + 1] * cs[i + 1]);
+        }
+      }
+    }
+    if (which == 0) {
+      if (live)
+        *reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * H + hh) * D + sub * 8) = pack8(x);
+    }
+    const bool store = live && which > 0;
+    if (__any_sync(~0u, store)) {
+      int key;
+      uint8_t* tile = tile_of<D>(a.kv, slot, store ? hh : 0, key);
+      quantise_store<D>(x, tile, key, which == 2, sub, store);
+    }
+  }
+}
+
+// Slots read back: scale * code + bias in fp32, rounded once to bf16.
+template <int D>
+__global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
+  constexpr int kLanes = D / 8, kRows = 256 / kLanes;
+  const int K = a.kv.kv_heads, sub = threadIdx.x % kLanes;
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;  // [T][2][K]
+  if (row >= (int64_t)a.T * 2 * K) return;
+  const int t = (int)(row / (2 * K)), which = (int)(row / K) & 1, h = (int)(row % K);
+  const int slot = a.slot[t];
+  if (slot < 0) return;
+  if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
+    if (sub == 0 && a.err) atomicOr(a.err, MOE_DERR_KV_INDEX);
+    return;
+  }
+  int key;
+  const uint8_t* tile = tile_of<D>(a.kv, slot, h, key);
+  const __half* meta = reinterpret_cast<const __half*>(tile + 16 * D);
+  const int g = sub >> 3, chunk = (sub >> 2) ^ swizzle<D>(key);
+  const float s = __half2float(meta[which ? Meta<D>::v_scale(key, g) : Meta<D>::k_scale(key, g)]);
+  const float b = __half2float(meta[which ? Meta<D>::v_bias(key, g) : Meta<D>::k_bias(key, g)]);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + which * 8 * D + key * (D / 2) +
+                                                        chunk * 16 + (sub & 3) * 4);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), b);
+  *reinterpret_cast<uint4*>((which ? a.v : a.k) + ((int64_t)t * K + h) * D + sub * 8) = pack8(x);
+}
+
+template <int D>
+cudaError_t store_d(const StoreArgs& a, cudaStream_t st) {
+  store_kernel<D><<<a.T, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t load_d(const LoadArgs& a, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.T * 2 * a.kv.kv_heads, per = 256 / (D / 8);
+  load_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_store(const StoreArgs& a, cudaStream_t st) {
+  return a.kv.head_dim == 256 ? store_d<256>(a, st)
+         : a.kv.head_dim == 128 ? store_d<128>(a, st) : store_d<64>(a, st);
+}
+
+cudaError_t launch_load(const LoadArgs& a, cudaStream_t st) {
+  return a.kv.head_dim == 256 ? load_d<256>(a, st)
+         : a.kv.head_dim == 128 ? load_d<128>(a, st) : load_d<64>(a, st);
+}
+
+}  // namespace kv
+}  // namespace moe

@@ -9,6 +9,10 @@
 
 namespace moe {
 
+// The thread's error message (moe_last_error) for entry points outside abi.cu.
+int set_error(int code, const char* fmt, ...);
+int set_ok();
+
 constexpr int kGroup = 64;
 constexpr int kMaxRouted = 1024;  // T*k limit of the single-CTA control step
 constexpr int kMaxVictims = 32;

@@ -1,0 +1,605 @@
+"""GPU tests of the 4-bit key/value cache: block plans, the rotated quantised store, slots read
+back, attention, and a decode loop of all of them, against plain 64-bit restatements
+(kv_reference.py)."""
+import numpy as np
+import pytest
+
+import kv_reference as ref
+import moe_expert_offload_gb300 as m
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DEV = "cuda"
+
+
+def _np(t):
+    return t.detach().cpu().numpy()
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _ints(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ plans
+def _check_plan(kv, batch, tab, new, max_tokens):
+    refused, start, length, slot, pos = tab.plan(new, max_tokens)
+    B = len(new)
+    m.moe_kv_plan(kv.c, _ints(new), B, batch.c)
+    err = int(batch.err[0])
+    assert err == (m.MOE_DERR_KV_FULL if refused else 0)
+    batch.err.zero_()
+    assert np.array_equal(_np(batch.q_start)[: B + 1], start)
+    assert np.array_equal(_np(batch.kv_len)[:B], length)
+    assert np.array_equal(_np(batch.slot), slot)
+    assert np.array_equal(_np(batch.pos), pos)
+    assert np.array_equal(_np(kv.block_table), tab.table)
+    assert np.array_equal(_np(kv.seq_len), tab.len)
+    n = int(kv.free_count[0])
+    assert _np(kv.free_list)[:n].tolist() == tab.free
+    return refused
+
+
+@pytest.mark.parametrize("P,rows,width,blocks,max_tokens,longest,seed", [
+    (16, 1, 3, 3, 40, 30, 0), (64, 7, 5, 20, 200, 90, 1), (128, 33, 4, 60, 5000, 300, 2),
+    (32, 1500, 4, 3000, 9000, 12, 3), (16, 300, 40, 5000, 20011, 200, 4),
+    (16, 1025, 2, 2050, 30000, 32, 5),
+])
+def test_plans_match_the_bookkeeping(P, rows, width, blocks, max_tokens, longest, seed):
+    rng = np.random.default_rng(seed)
+    kv = m.DeviceKv(rows, width, blocks, P, 1, 64, with_pool=False)
+    batch = m.DeviceKvBatch(max_tokens, rows)
+    tab = ref.Tables(rows, width, blocks, P)
+    m.moe_kv_reset(kv.c)
+    refusals = 0
+    for step in range(8):
+        kind = rng.integers(0, 6, rows)
+        new = np.where(kind < 2, 1, np.where(kind == 2, rng.integers(0, longest + 1, rows),
+                       np.where(kind == 3, -rng.integers(1, 5, rows),
+                                np.where(kind == 4, 0, -(2 ** 31 - 1)))))
+        if step == 5:
+            new[rng.integers(0, rows)] = width * P + 1  # longer than its row
+        if step == 6:
+            new = np.full(rows, width * P // 2)  # more than there is room for, mostly
+        if step == 7:
+            new = -tab.len  # every row given up
+        refusals += _check_plan(kv, batch, tab, new, max_tokens)
+    assert refusals >= 1
+    assert int(kv.free_count[0]) == blocks
+
+
+def test_plan_of_fewer_rows_and_edges():
+    """Rows behind `rows` keep what they hold; a batch filled to the last token and the last
+    block; one token too many is refused whole."""
+    kv = m.DeviceKv(4, 2, 6, 16, 1, 64, with_pool=False)
+    batch = m.DeviceKvBatch(64, 5)
+    tab = ref.Tables(4, 2, 6, 16)
+    assert not _check_plan(kv, batch, tab, [16, 0, 17, 31], 64)
+    kv3, len3 = _np(kv.block_table)[3].copy(), int(kv.seq_len[3])
+    assert not _check_plan(kv, batch, tab, [16, 0], 64)
+    assert np.array_equal(_np(kv.block_table)[3], kv3) and int(kv.seq_len[3]) == len3
+    assert _check_plan(kv, batch, tab, [0, 1], 64)  # no block left
+    assert not _check_plan(kv, batch, tab, [-32, 32, -17, 1], 64)
+    assert not _check_plan(kv, batch, tab, [0, -32, 32, -32], 64)
+    assert _check_plan(kv, batch, tab, [32, 32, 1, 0], 64)
+
+
+def test_plan_refuses_tables_that_are_not_its_own():
+    """A free count and row lengths that together pass the pool's blocks: flagged, nothing moves."""
+    kv = m.DeviceKv(2, 4, 5, 16, 1, 64, with_pool=False)
+    batch = m.DeviceKvBatch(8, 2)
+    kv.seq_len.fill_(64)  # claims 8 blocks of a pool of 5, with 5 free
+    before = _np(kv.block_table).copy(), _np(kv.free_list).copy()
+    m.moe_kv_plan(kv.c, _ints([-64, 1]), 2, batch.c)
+    assert int(batch.err[0]) == m.MOE_DERR_KV_FULL | m.MOE_DERR_KV_INDEX
+    assert np.array_equal(_np(kv.block_table), before[0])
+    assert np.array_equal(_np(kv.free_list), before[1])
+    assert int(kv.free_count[0]) == 5 and _np(batch.q_start).tolist() == [0, 0, 0]
+
+
+# ------------------------------------------------------------------ store and load
+def _slots(rng, T, blocks, P):
+    return _ints(rng.permutation(blocks * P)[:T])
+
+
+def _store_case(T, H, K, D, P, rot, adjacent, axes, norms, seed, gap=0):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    blocks = -(-T // P) + 2
+    kv = m.DeviceKv(1, blocks, blocks, P, K, D)
+    batch = m.DeviceKvBatch(T, 1)
+    batch.slot.copy_(_slots(rng, T, blocks, P))
+    max_pos = 5000
+    pos = _ints(rng.integers(0, max_pos, (axes, T)))
+    if axes == 1:
+        batch.pos.copy_(pos[0])
+    # q, k, v slices of one buffer; `gap` columns lie between query heads
+    wide = H * (D + gap) + 2 * K * D
+    buf = (torch.randn(T, wide, generator=g, device=DEV) * 1.5).bfloat16()
+    q = buf[:, : H * (D + gap)].unflatten(1, (H, D + gap))[..., :D]
+    k = buf[:, H * (D + gap): H * (D + gap) + K * D].unflatten(1, (K, D))
+    v = buf[:, H * (D + gap) + K * D:].unflatten(1, (K, D))
+    w = [1 + 0.2 * torch.randn(D, generator=g, device=DEV) if n else None for n in norms]
+    table = m.rope_table(max_pos, rot, 1e6) if rot else None
+    axis = [i % axes for i in range(rot // 2)]
+    rope = m.make_rope(table, rot, adjacent, axes, axis) if rot else None
+    return dict(kv=kv, batch=batch, pos=pos, q=q, k=k, v=v, w=w, table=table, axis=axis, rope=rope,
+                eps=1e-5, rot=rot, adjacent=adjacent, T=T, H=H, K=K, D=D, P=P, axes=axes)
+
+
+def _run_store(c, T=None):
+    q_out = torch.full((c["T"], c["H"], c["D"]), 7.0, dtype=torch.bfloat16, device=DEV)
+    proj = m.make_qkv(c["q"], c["k"], c["v"], c["w"][0], c["w"][1], c["eps"])
+    m.moe_qkv_store(c["kv"].c, c["batch"].c, c["rope"], proj, c["T"] if T is None else T,
+                    c["pos"] if c["axes"] > 1 else None, q_out)
+    return q_out
+
+
+def _expected(c):
+    angles = _np(c["table"]) if c["rot"] else None
+    pos = _np(c["pos"])
+    return [ref.norm_rotate(_f64(x), None if w is None else _np(w), c["eps"], angles, pos, c["rot"],
+                            c["adjacent"], c["axis"])
+            for x, w in ((c["q"], c["w"][0]), (c["k"], c["w"][1]))] + [_f64(c["v"])]
+
+
+def _check_quantised(got, y, what):
+    """got: the values that the cache stands for.  A code is off by at most half a step of the
+    group's scale; scale and bias are rounded to fp16 (2^-11 of themselves: 15 steps of the
+    scale, and the bias), and y comes from fp32 (2^-20 of the group's largest covers its sums)."""
+    n = y.shape[-1] // 64
+    yg = y.reshape(*y.shape[:-1], n, 64)
+    lo, hi = yg.min(-1, keepdims=True), yg.max(-1, keepdims=True)
+    step, big = (hi - lo) / 15, np.maximum(np.abs(lo), np.abs(hi))
+    tol = 0.5 * step * (1 + 2.0 ** -11) + 2.0 ** -11 * (15 * step + np.abs(lo)) + big * 2.0 ** -20
+    tol = tol + 2.0 ** -24  # an fp16 scale or bias in the subnormal range
+    off = np.abs(got.reshape(yg.shape) - yg)
+    assert np.all(off <= tol + 15 * 2.0 ** -25), (what, float((off - tol).max()))
+
+
+@pytest.mark.parametrize("T,H,K,D,P,rot,adjacent,axes,norms,gap", [
+    (1, 16, 2, 256, 64, 64, False, 1, (1, 1), 0),
+    (5, 8, 8, 64, 16, 64, True, 1, (1, 1), 0),
+    (33, 32, 4, 128, 32, 128, False, 1, (1, 1), 0),
+    (70, 6, 1, 256, 128, 256, True, 3, (1, 0), 256),
+    (17, 5, 5, 128, 16, 96, False, 3, (0, 1), 8),
+    (9, 1, 1, 64, 64, 16, False, 1, (0, 0), 0),
+    (300, 7, 1, 64, 128, 48, True, 4, (1, 1), 64),
+    (6, 256, 1, 64, 16, 0, False, 1, (1, 1), 0),
+    (40, 3, 3, 256, 16, 80, False, 1, (1, 1), 0),
+    (2049, 4, 2, 128, 64, 32, False, 1, (1, 1), 0),
+])
+def test_store_and_load(T, H, K, D, P, rot, adjacent, axes, norms, gap):
+    c = _store_case(T, H, K, D, P, rot, adjacent, axes, norms, T + D, gap)
+    q_out = _run_store(c)
+    yq, yk, yv = _expected(c)
+    # bf16: half a step, 2^-8 of itself; the fp32 norm and rotation add 2^-20 of the pair
+    pair = np.abs(yq).max(-1, keepdims=True) * 2.0 ** -20
+    assert np.all(np.abs(_f64(q_out) - yq) <= np.abs(yq) * 2.0 ** -8 + pair)
+    slots = _np(c["batch"].slot)
+    kk, vv = ref.read_slots(_np(c["kv"].pool), slots, K, P, D)
+    _check_quantised(kk, yk, "k")
+    _check_quantised(vv, yv, "v")
+    assert int(c["batch"].err[0]) == 0
+    # read back: scale * code + bias rounded once
+    k2 = torch.empty(T, K, D, dtype=torch.bfloat16, device=DEV)
+    v2 = torch.empty_like(k2)
+    m.moe_kv_load(c["kv"].c, c["batch"].slot, T, k2, v2)
+    for got, want in ((k2, kk), (v2, vv)):
+        assert np.all(np.abs(_f64(got) - want) <= np.abs(want) * 2.0 ** -8 + 2.0 ** -24 * 16)
+    # nothing outside the slots was written
+    free = np.setdiff1d(np.arange(c["kv"].pool.shape[0] * P), slots)
+    if len(free):
+        k0, v0 = ref.read_slots(_np(c["kv"].pool), free, K, P, D)
+        assert not k0.any() and not v0.any()
+
+
+def test_store_skips_padding_and_flags_bad_tokens():
+    c = _store_case(12, 4, 2, 128, 16, 64, False, 1, (1, 1), 3)
+    slots = c["batch"].slot.clone()
+    c["batch"].slot[4:6] = -1
+    c["batch"].slot[9] = c["kv"].pool.shape[0] * 16  # one behind the last
+    c["batch"].pos[10] = 5000
+    c["batch"].pos[11] = -3
+    q_out = _run_store(c)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    skipped = [4, 5, 9, 10, 11]
+    kept = [i for i in range(12) if i not in skipped]
+    assert torch.all(q_out[skipped] == 7.0) and not torch.any(q_out[kept] == 7.0)
+    kk, _ = ref.read_slots(_np(c["kv"].pool), _np(slots), 2, 16, 128)
+    assert not kk[skipped].any() and np.all(np.abs(kk[kept]).sum((1, 2)) > 0)
+    # fewer tokens than the batch holds: the rest is left alone
+    c = _store_case(12, 4, 2, 128, 16, 64, False, 1, (1, 1), 4)
+    q_out = _run_store(c, T=7)
+    assert torch.all(q_out[7:] == 7.0)
+    kk, _ = ref.read_slots(_np(c["kv"].pool), _np(c["batch"].slot), 2, 16, 128)
+    assert not kk[7:].any()
+    # load: -1 and out of range leave their rows, the same slot may come twice
+    s = c["batch"].slot[:7].clone()
+    s[1], s[2], s[3] = -1, c["kv"].pool.shape[0] * 16, s[0]
+    k2 = torch.full((7, 2, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    v2 = k2.clone()
+    c["batch"].err.zero_()
+    m.moe_kv_load(c["kv"].c, s, 7, k2, v2, c["batch"].err)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    assert torch.all(k2[1:3] == 9.0) and torch.equal(k2[3], k2[0]) and not torch.any(k2[4:] == 9.0)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_store_of_unusual_values(D):
+    """Constant groups, zeros, subnormals, infinities, NaN, and values past the clamp."""
+    c = _store_case(8, 2, 1, D, 16, 0, False, 1, (0, 0), 5)
+    k = torch.zeros(8, 1, D, device=DEV)
+    k[1] = 2.5
+    k[2] = 1e-30
+    k[3] = 3.0
+    k[3, 0, 5] = float("nan")
+    k[4, 0, 0], k[4, 0, 1] = float("inf"), float("-inf")
+    k[5] = torch.linspace(-3e38, 3e38, D, device=DEV)
+    k[6] = torch.linspace(0, 1, D, device=DEV)
+    k[7] = -65504.0
+    c["k"] = k.bfloat16()
+    c["v"] = c["k"].flip(0).contiguous()
+    _run_store(c)
+    kk, vv = ref.read_slots(_np(c["kv"].pool), _np(c["batch"].slot), 1, 16, D)
+    for got, x in ((kk, _f64(c["k"])), (vv, _f64(c["v"]))):
+        nan = np.isnan(x).reshape(8, 1, -1, 64).any(-1, keepdims=True)
+        nan = np.broadcast_to(nan, (8, 1, D // 64, 64)).reshape(8, 1, D)
+        assert np.array_equal(np.isnan(got), nan)
+        x = np.where(nan, 0.0, np.clip(np.where(np.isnan(x), 0.0, x), -32768, 32768))
+        _check_quantised(np.where(nan, 0.0, got), x, "unusual")
+    assert np.array_equal(kk[1], np.full((1, D), 2.5)) and not kk[0].any()
+
+
+# ------------------------------------------------------------------ attention
+def _fill(kv, D, gen, poison):
+    """Random codes, scales and biases in every tile of the pool."""
+    tiles = kv.pool.view(-1, 18 * D)
+    n, G = tiles.shape[0], D // 64
+    tiles[:, : 16 * D] = torch.randint(0, 256, (n, 16 * D), generator=gen, device=DEV,
+                                       dtype=torch.uint8)
+    s = 0.1 + 0.3 * torch.rand(2, n, 16 * G, generator=gen, device=DEV)
+    b = -7.5 * s + 0.3 * torch.randn(2, n, 16 * G, generator=gen, device=DEV)
+    if poison is not None:
+        s[:], b[:] = poison, poison
+    meta = torch.cat((s[0], b[0], s[1], b[1]), 1).half()
+    tiles[:, 16 * D:] = meta.view(torch.uint8)
+
+
+def _attend_case(P, K, D, r, lens, news, seed, poison=False, spare=3):
+    """A cache of random tokens; with `poison` every slot that no token may see is NaN."""
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    B, width = len(lens), max(1, -(-max(lens) // P)) + 1
+    blocks = sum(-(-n // P) for n in lens) + spare
+    kv = m.DeviceKv(B, width, blocks, P, K, D)
+    T = sum(news) + 2
+    batch = m.DeviceKvBatch(T, B)
+    order = rng.permutation(blocks)
+    table = np.full((B, width), -1)
+    used = 0
+    for b, n in enumerate(lens):
+        k = -(-n // P)
+        table[b, :k] = order[used:used + k]
+        used += k
+    kv.block_table.copy_(_ints(table))
+    batch.kv_len.copy_(_ints(lens))
+    batch.q_start.copy_(_ints(np.concatenate([[0], np.cumsum(news)])))
+    _fill(kv, D, gen, None)
+    if poison:
+        live = np.concatenate([table[b, np.arange(n) // P] * P + np.arange(n) % P
+                               for b, n in enumerate(lens)] + [np.zeros(0, np.int64)]).astype(np.int64)
+        mask = np.ones(blocks * P, bool)
+        mask[live] = False
+        # scales and biases of the dead slots: [tile][part][...]
+        G = D // 64
+        meta = kv.pool.view(-1, 18 * D)[:, 16 * D:].contiguous().view(torch.float16)
+        dead = torch.tensor(mask, device=DEV).view(blocks, 1, P // 16, 16).expand(-1, K, -1, -1)
+        dead = dead.reshape(-1, 16)
+        parts = meta.view(-1, 4, 16 * G)
+        by_key = dead[:, :, None].expand(-1, 16, G).reshape(-1, 16 * G)
+        by_group = dead[:, None, :].expand(-1, G, 16).reshape(-1, 16 * G)
+        for i in range(4):
+            parts[:, i].masked_fill_(by_key if i < 2 else by_group, float("nan"))
+        kv.pool.view(-1, 18 * D)[:, 16 * D:] = meta.view(torch.uint8)
+    q = (torch.randn(T, K * r, D, generator=gen, device=DEV) * 1.5).bfloat16()
+    return dict(kv=kv, batch=batch, q=q, T=T, H=K * r, K=K, D=D, P=P, B=B, lens=lens, news=news,
+                table=table, scale=D ** -0.5, max_new=max(1, max(news)))
+
+
+def _run_attend(c, q=None, ws=None, stream=None, out=None, max_new=None):
+    max_new = max_new or c["max_new"]
+    if out is None:
+        out = torch.full_like(c["q"], 5.0)
+    n = m.moe_kv_attention_workspace_bytes(c["kv"].c, c["B"], c["T"], c["H"], max_new)
+    if ws is None:
+        ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)  # NaN in every float
+    m.moe_kv_attention(c["kv"].c, c["batch"].c, c["B"], c["q"] if q is None else q, c["T"], c["H"],
+                       max_new, c["scale"], ws, n, out, stream)
+    return out
+
+
+def _check_attend(c, out, rows=None, q=None):
+    pool, got = _np(c["kv"].pool), _f64(out)
+    q = _f64(c["q"] if q is None else q)
+    start, want_all, got_all = 0, [], []
+    for b, (L, n) in enumerate(zip(c["lens"], c["news"])):
+        if n and (rows is None or b in rows):
+            j = np.arange(L)
+            k, v = ref.read_slots(pool, c["table"][b, j // c["P"]] * c["P"] + j % c["P"], c["K"],
+                                  c["P"], c["D"])
+            qq = q[start:start + n]
+            want = ref.attention(qq, k, v, c["scale"], L - n)
+            tol = ref.attention_bound(qq, k, v, c["scale"], want)
+            g = got[start:start + n]
+            assert np.all(np.isfinite(g)), f"row {b}: not finite"
+            off = np.abs(g - want)
+            assert np.all(off <= tol), (b, L, n, float((off - tol).max()), float(off.max()))
+            want_all.append(want.ravel())
+            got_all.append(g.ravel())
+        start += n
+    if want_all:
+        w, g = np.concatenate(want_all), np.concatenate(got_all)
+        rel = np.linalg.norm(g - w) / np.linalg.norm(w)
+        assert rel <= ref.ATTENTION_REL, rel
+    assert torch.all(out[sum(c["news"]):] == 5.0), "rows behind the last token changed"
+
+
+CASES = [
+    # P, kv heads, D, group, lengths, new tokens
+    (64, 2, 256, 8, [1000], [1]),
+    (16, 1, 64, 1, [1], [1]),
+    (16, 2, 128, 8, [1, 15, 16, 17, 31, 32, 33, 63, 64, 65], [1] * 10),
+    (128, 1, 256, 4, [127, 128, 129, 5, 700], [1] * 5),
+    (32, 8, 64, 4, [3, 0, 257, 0, 40], [1, 0, 1, 0, 1]),
+    (64, 4, 128, 6, [513, 100], [1, 1]),
+    (32, 2, 128, 16, [300, 33, 90], [1, 1, 1]),
+    (16, 1, 256, 16, [77, 500], [1, 1]),
+    (16, 1, 64, 64, [200, 9], [1, 1]),
+    (64, 1, 128, 33, [130], [2]),
+    (32, 4, 128, 8, [400, 4, 129, 64, 9], [4, 4, 2, 1, 3]),
+    (64, 2, 256, 8, [100, 2000], [3, 8]),
+    (64, 2, 256, 8, [257], [257]),
+    (16, 2, 128, 8, [130], [130]),
+    (64, 2, 128, 8, [640, 128], [128, 100]),
+    (128, 2, 64, 1, [300, 17, 129], [300, 17, 100]),
+    (16, 1, 256, 6, [333], [200]),
+    (64, 1, 128, 5, [1500, 64], [70, 64]),
+    (64, 2, 256, 16, [200, 900, 0, 50], [200, 1, 0, 33]),
+    (32, 2, 128, 4, [3000, 40, 2100, 1], [5, 40, 300, 1]),
+    (64, 8, 64, 2, [256], [256]),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+@pytest.mark.parametrize("poison", [False, True])
+def test_attention(i, poison):
+    P, K, D, r, lens, news = CASES[i]
+    c = _attend_case(P, K, D, r, lens, news, 100 + i, poison)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_attend(c, out)
+
+
+def test_attention_is_repeatable_and_ignores_its_workspace():
+    c = _attend_case(64, 2, 128, 8, [3000, 5, 777, 1200], [1, 2, 200, 1], 7)
+    first = _run_attend(c)
+    for fill in (0, 1, 255):
+        n = m.moe_kv_attention_workspace_bytes(c["kv"].c, c["B"], c["T"], c["H"], c["max_new"])
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        assert torch.equal(_run_attend(c, ws=ws).view(torch.int16), first.view(torch.int16))
+    # a larger bound on the new tokens changes nothing but roundings
+    wider = _run_attend(c, max_new=1000)
+    _check_attend(c, wider)
+
+
+@pytest.mark.parametrize("D,news", [(128, [1, 1, 1]), (256, [1, 1, 1]), (64, [40, 200, 3]),
+                                    (256, [130, 1, 3])])
+def test_attention_of_extreme_scores(D, news):
+    """Queries so large that one key takes all the weight, zero queries (plain means), and
+    scores that all lie far below zero."""
+    c = _attend_case(32, 1, D, 8, [500, 260, 33], news, 11)
+    big = c["q"].float() * 200
+    big[0] = 0
+    big[:, 1::3] = 0
+    big[:, 2::3] = -big[:, 2::3].abs()
+    q = big.bfloat16()
+    out = _run_attend(c, q=q)
+    # the bound's score term assumes scores of ordinary size: with weights that jump between
+    # keys only finiteness, zero queries and the hull of the values are checked here
+    got = _f64(out)[: sum(news)]
+    assert np.all(np.isfinite(got))
+    pool, start = _np(c["kv"].pool), 0
+    for b, (L, n) in enumerate(zip(c["lens"], news)):
+        j = np.arange(L)
+        k, v = ref.read_slots(pool, c["table"][b, j // 32] * 32 + j % 32, 1, 32, D)
+        lo, hi = v.min(0), v.max(0)
+        slack = np.abs(v).max() * 2.0 ** -7
+        g = got[start:start + n]
+        assert np.all(g >= lo - slack) and np.all(g <= hi + slack)
+        qz = np.zeros((n, 8, D))
+        want = ref.attention(qz, k, v, 1.0, L - n)
+        tol = ref.attention_bound(qz, k, v, 1.0, want)
+        zero = ~_f64(q)[start:start + n].any(-1)
+        assert zero.any()
+        assert np.all(np.abs(g - want)[zero] <= tol[zero])
+        start += n
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("news", [[1, 1], [1, 150]])
+def test_attention_of_values_of_all_sizes(D, news):
+    """Scales from 2^-9 to 2^9 within a row, tiny and large queries: the fp16 products keep
+    their range."""
+    c = _attend_case(16, 2, D, 4, [300, 200], news, 13)
+    G = D // 64
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].contiguous().view(torch.float16).view(-1, 4, 16 * G)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    f = torch.exp2(torch.randint(-9, 10, (meta.shape[0], 16 * G), generator=g, device=DEV).float())
+    meta[:, 2] = (meta[:, 2].float() * f).half()
+    meta[:, 3] = (meta[:, 3].float() * f).half()
+    c["kv"].pool.view(-1, 18 * D)[:, 16 * D:] = meta.reshape(-1, 64 * G).view(torch.uint8)
+    size = torch.exp2(torch.randint(-40, 2, (c["T"], 1, 1), generator=g, device=DEV).float())
+    c["q"] = (c["q"].float() * size).bfloat16()
+    _check_attend(c, _run_attend(c))
+
+
+@pytest.mark.parametrize("lens,news", [([300, 70, 200], [1, 1, 1]), ([300, 260, 200], [150, 9, 130])])
+def test_attention_leaves_out_bad_blocks_and_rows(lens, news):
+    """Block ids outside the pool and rows whose bounds do not fit are flagged; the others'
+    results stay."""
+    c = _attend_case(16, 2, 128, 4, lens, news, 17)
+    good = _run_attend(c)
+    bad = c["kv"].block_table.clone()
+    bad[1, 2] = c["kv"].pool.shape[0]
+    bad[1, 0] = -1
+    c["kv"].block_table.copy_(bad)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    _check_attend(c, out, rows=(0, 2))
+    assert torch.all(torch.isfinite(out.float()))
+    first = news[0]
+    assert torch.equal(out[:first], good[:first])
+    # a row without a single good block is 0
+    c["kv"].block_table[1].fill_(-1)
+    out = _run_attend(c)
+    assert not torch.any(out[first:first + news[1]])
+    # bounds: longer than the block table, more new tokens than the cache holds
+    c["kv"].block_table.copy_(bad)
+    for value in (c["kv"].c.max_blocks * 16 + 1, -1, news[1] - 1):
+        c["batch"].err.zero_()
+        c["batch"].kv_len[1] = value
+        out = _run_attend(c)
+        assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+        assert torch.all(out[first:first + news[1]] == 5.0)
+        _check_attend(c, out, rows=(0, 2))
+    c["batch"].kv_len[1] = lens[1]
+    c["batch"].q_start[3] = c["T"] + 1  # past the queries
+    c["batch"].err.zero_()
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) & m.MOE_DERR_KV_INDEX
+    assert torch.all(out[sum(news[:2]):] == 5.0)
+
+
+def test_attention_on_two_streams_at_once():
+    a = _attend_case(64, 2, 256, 8, [4000, 900], [1, 1], 19)
+    b = _attend_case(32, 4, 128, 8, [600, 700], [300, 2], 20)
+    want = [_run_attend(x).clone() for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for _ in range(5):
+        for x, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(_run_attend(x, stream=s))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+
+
+# ------------------------------------------------------------------ all of them, as they are used
+@pytest.mark.parametrize("P,H,K,D,rot,prompts,steps", [
+    (16, 8, 2, 128, 128, [37, 5, 0, 130], 20),
+    (64, 16, 2, 256, 64, [200, 64], 6),
+    (32, 4, 4, 64, 32, [1, 31, 33], 35),
+])
+def test_decode_loop(P, H, K, D, rot, prompts, steps):
+    """Two layers: the prompts' chunk, then decode steps captured once as a graph and replayed
+    while the cache grows, with rows that finish, restart and take back drafts."""
+    B, layers = len(prompts), 2
+    g = torch.Generator(device=DEV).manual_seed(P + D)
+    width = -(-(max(prompts) + 2 * steps + 8) // P)
+    kv = m.DeviceKv(B, width, B * width, P, K, D, layers=layers)
+    rope = m.make_rope(m.rope_table(width * P, rot), rot)
+    wq, wk = (1 + 0.1 * torch.randn(D, generator=g, device=DEV) for _ in range(2))
+    scale = D ** -0.5
+    hist = [[[] for _ in range(B)] for _ in range(layers)]  # slots are read back each step
+
+    def layer_calls(l, batch, T, max_new, buf, q, out, ws):
+        c = kv.layers[l]
+        x = buf[l]
+        proj = m.make_qkv(x[:, :H], x[:, H:H + K], x[:, H + K:], wq, wk)
+        m.moe_qkv_store(c, batch.c, rope, proj, T, None, q[l])
+        m.moe_kv_attention(c, batch.c, B, q[l], T, H, max_new, scale, ws, ws.numel(), out[l])
+
+    def check(batch, T, q, out):
+        assert int(batch.err[0]) == 0
+        start, length, table = _np(batch.q_start), _np(batch.kv_len), _np(kv.block_table)
+        for l in range(layers):
+            pool = _np(kv.pools[l])
+            for b in range(B):
+                n, L = start[b + 1] - start[b], int(length[b])
+                if n == 0:
+                    continue
+                j = np.arange(L)
+                k, v = ref.read_slots(pool, table[b, j // P] * P + j % P, K, P, D)
+                qq = _f64(q[l][start[b]:start[b + 1]])
+                want = ref.attention(qq, k, v, scale, L - n)
+                off = np.abs(_f64(out[l][start[b]:start[b + 1]]) - want)
+                assert np.all(off <= ref.attention_bound(qq, k, v, scale, want)), (l, b, L)
+                # the last token's key is this step's own
+                x = _f64(buf_now[l][start[b + 1] - 1:start[b + 1], H:H + K])
+                y = ref.norm_rotate(x, _np(wk), 1e-6, _np(rope.table_tensor), np.array([[L - 1]]),
+                                    rot, False, None)
+                _check_quantised(k[-1:], y, "k in the loop")
+
+    def buffers(T):
+        buf = torch.randn(layers, T, H + 2 * K, D, generator=g, device=DEV).bfloat16()
+        q = torch.zeros(layers, T, H, D, dtype=torch.bfloat16, device=DEV)
+        return buf, q, torch.zeros_like(q)
+
+    T = sum(prompts)
+    batch = m.DeviceKvBatch(T, B)
+    buf_now, q, out = buffers(T)
+    ws = torch.empty(m.moe_kv_attention_workspace_bytes(kv.c, B, T, H, max(prompts)),
+                     dtype=torch.uint8, device=DEV)
+    m.moe_kv_plan(kv.c, _ints(prompts), B, batch.c)
+    for l in range(layers):
+        layer_calls(l, batch, T, max(prompts), buf_now, q, out, ws)
+    check(batch, T, q, out)
+
+    # decode: at most 2 tokens a row (a draft), everything captured once
+    T = 2 * B
+    batch = m.DeviceKvBatch(T, B)
+    buf_now, q, out = buffers(T)
+    new = _ints([1] * B)
+    ws = torch.empty(m.moe_kv_attention_workspace_bytes(kv.c, B, T, H, 2), dtype=torch.uint8,
+                     device=DEV)
+    tab = ref.Tables(B, width, B * width, P)
+    tab.plan(prompts, sum(prompts))
+
+    def step():
+        m.moe_kv_plan(kv.c, new, B, batch.c)
+        for l in range(layers):
+            layer_calls(l, batch, T, 2, buf_now, q, out, ws)
+
+    state = [t.clone() for t in (kv.block_table, kv.seq_len, kv.free_list, kv.free_count)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for t, s in zip((kv.block_table, kv.seq_len, kv.free_list, kv.free_count), state):
+        t.copy_(s)
+    rng = np.random.default_rng(steps)
+    for i in range(steps):
+        n = rng.choice([1, 1, 1, 2, 0], B)
+        if i == steps // 2:
+            n[0] = -(1 << 30)  # this row finishes
+        elif i % 5 == 4:
+            n[B - 1] = -1  # a rejected draft
+        new.copy_(_ints(n))
+        buf_now.copy_(torch.randn(buf_now.shape, generator=g, device=DEV))
+        graph.replay()
+        tab.plan(n, T)
+        assert np.array_equal(_np(kv.seq_len), tab.len)
+        assert np.array_equal(_np(kv.block_table), tab.table)
+        if i % 4 == 0 or i == steps - 1:
+            check(batch, T, q, out)
