@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(256) attn_simple_kernel(AttnArgs a) {
     if (lane == 0) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
     return;
   }
+  if (n * (a.heads / K) <= kDecodeCols) return;
   const int last = len - n + (t - a.batch.q_start[lo]);
   const int64_t at = ((int64_t)t * a.heads + h) * D + lane * N;
   float q[N], o[N] = {}, m = -INFINITY, l = 0.0f;
@@ -67,9 +68,13 @@ __global__ void __launch_bounds__(256) attn_simple_kernel(AttnArgs a) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(const moe_kv&, int, int, int, int) { return 256; }
+size_t attn_workspace_bytes(const moe_kv& kv, int, int, int, int) {
+  return decode_workspace_bytes(kv.head_dim);
+}
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_decode(a, st);
+  if (e != cudaSuccess || (int64_t)a.max_new * (a.heads / a.kv.kv_heads) <= kDecodeCols) return e;
   const unsigned grid = (unsigned)(((int64_t)a.T * a.heads + 7) / 8);
   if (a.kv.head_dim == 256) attn_simple_kernel<256><<<grid, 256, 0, st>>>(a);
   else if (a.kv.head_dim == 128) attn_simple_kernel<128><<<grid, 256, 0, st>>>(a);

@@ -21,6 +21,10 @@ namespace moe {
 namespace kv {
 
 constexpr int kTile = 16;  // tokens of a tile
+constexpr int kGrid = 152; // CTAs of the attention kernels: one per SM
+// rows of up to this many queries per kv head (new tokens x query heads on it)
+// go through the decode kernel, longer ones through the prompt kernel
+constexpr int kDecodeCols = 64;
 
 __host__ __device__ constexpr int tile_bytes(int D) { return 18 * D; }
 
@@ -80,6 +84,8 @@ struct AttnArgs {
 };
 size_t attn_workspace_bytes(const moe_kv& kv, int rows, int T, int heads, int max_new);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
+size_t decode_workspace_bytes(int D);
+cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace moe
