@@ -86,6 +86,8 @@ size_t attn_workspace_bytes(const moe_kv& kv, int rows, int T, int heads, int ma
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
 size_t decode_workspace_bytes(int D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st);
+size_t prompt_workspace_bytes(int D);
+cudaError_t launch_prompt(const AttnArgs& a, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace moe

@@ -799,85 +799,85 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
   // ------------------------------------------------ parts merged over the CTA
   // In order: each warp's head part (it ends a unit) and its last part (it does
   // not).  A run of parts of one unit is closed by a head or by the CTA's end;
-  // run i takes the last parts of the warps from the i-th head's on and then the
-  // next head.  One warp per run and column.
+  // it takes the last parts of the warps from the previous head's on and then
+  // the next head.  One warp per column of a run.
   const uint32_t heads = __ballot_sync(~0u, lane < W && s_part[lane < W ? lane : 0][0].unit >= 0);
   const uint32_t lasts = __ballot_sync(~0u, lane < W && s_part[lane < W ? lane : 0][1].unit >= 0);
-  const int n_heads = __popc(heads);
-  const int after = n_heads ? 31 - __clz(heads) : 0;  // the last head's warp
-  const bool open_run = (lasts >> after) != 0;
-  bool cut = false;
-  Part cut_part = {};
-  for (int task = wid; task < (n_heads + open_run) * C::kCols; task += W) {
-    const int run = task / C::kCols, cc = task % C::kCols;
-    const bool closed = run < n_heads;
-    const int to = closed ? (int)__fns(heads, 0, run + 1) : W;
-    const int from = run == 0 ? 0 : (int)__fns(heads, 0, run);
-    // member k: the last part of warp from + k, and at the end the head of `to`
-    uint32_t members = lasts & (to == 32 ? ~0u : (1u << to) - 1u) & ~((1u << from) - 1u);
-    if (closed) members |= 1u << to;
-    const Part pt = closed ? s_part[to][0] : s_part[31 - __clz(members)][1];
-    const int head_w = __ffs(members) - 1;
-    const bool begun = !(closed && head_w == to) && s_part[head_w][1].first;
-    auto source = [&](int w) {
-      return closed && w == to ? warp_part + ((size_t)blockIdx.x * W + w) * C::kPartial
-                               : reinterpret_cast<const float*>(rings + w * C::kWarpBytes);
-    };
-    // lane w: warp w's maximum, weight and sum
-    float mk = kNone, lk = 0.0f;
-    if ((members >> lane) & 1u) {
-      const float* src = source(lane);
-      mk = src[C::kCols * D + cc];
-      lk = src[C::kCols * (D + 1) + cc];
+  int from = 0, task = wid;
+  for (uint32_t left = heads;; left &= left - 1) {
+    const bool closed = left != 0;
+    const int to = closed ? __ffs(left) - 1 : W;  // members: lasts of [from, to), head of `to`
+    const uint32_t mine = lasts & (uint32_t)((1ull << to) - 1ull) & ~((1u << from) - 1u);
+    if (!closed && mine == 0) {
+      if (tid == 0) static_cast<Cut*>(a.ws)[blockIdx.x].last = -1;
+      break;
     }
-    float mm = mk;
+    const int w0 = mine ? __ffs(mine) - 1 : to, w1 = closed ? to : 31 - __clz(mine);
+    const Part pt = closed ? s_part[to][0] : s_part[w1][1];
+    const bool begun = mine != 0 && s_part[w0][1].first;
+    const float* head_part = warp_part + ((size_t)blockIdx.x * W + to) * C::kPartial;
+    float* dst = cta_part + ((size_t)blockIdx.x * 2 + (closed || !begun ? 0 : 1)) * C::kPartial;
+    for (; task < C::kCols; task += W) {
+      const int cc = task;
+      // lane w: warp w's maximum, weight and sum
+      float mk = kNone, lk = 0.0f;
+      if (lane >= w0 && lane <= w1) {
+        const float* src = closed && lane == to
+                               ? head_part
+                               : reinterpret_cast<const float*>(rings + lane * C::kWarpBytes);
+        mk = src[C::kCols * D + cc];
+        lk = src[C::kCols * (D + 1) + cc];
+      }
+      float mm = mk;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    const float fk = exp2f(mk - mm);
-    lk *= fk;
+      for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+      const float fk = exp2_fast(mk - mm);
+      lk *= fk;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
-    float y[D / 32] = {};
-    for (uint32_t rest = members; rest; rest &= rest - 1) {
-      const int w = __ffs(rest) - 1;
-      const float f = __shfl_sync(~0u, fk, w);
-      const float* src = source(w) + cc * D + lane * 2;
+      for (int o = 8; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
+      mm = __shfl_sync(~0u, mm, 0);
+      lk = __shfl_sync(~0u, lk, 0);
+      float y[D / 32] = {};
+      auto add = [&](const float* src, float f) {
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const float2 v = *reinterpret_cast<const float2*>(src + i * 64);
-        y[2 * i] = fmaf(f, v.x, y[2 * i]);
-        y[2 * i + 1] = fmaf(f, v.y, y[2 * i + 1]);
+        for (int i = 0; i < D / 64; ++i) {
+          const float2 v = *reinterpret_cast<const float2*>(src + cc * D + lane * 2 + i * 64);
+          y[2 * i] = fmaf(f, v.x, y[2 * i]);
+          y[2 * i + 1] = fmaf(f, v.y, y[2 * i + 1]);
+        }
+      };
+#pragma unroll 4
+      for (int w = w0; w < w1 + (closed ? 0 : 1); ++w)
+        add(reinterpret_cast<const float*>(rings + w * C::kWarpBytes), __shfl_sync(~0u, fk, w));
+      if (closed) add(head_part, __shfl_sync(~0u, fk, to));
+      if (closed && begun) {
+        const int c = (pt.unit % pt.ntb) * C::kCols + cc;
+        if (c < pt.n * r)
+          store_row<D>(a.out + ((int64_t)(pt.start + c / r) * a.heads + pt.unit / pt.ntb * r + c % r) * D,
+                       y, lk, lane);
+      } else {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          *reinterpret_cast<float2*>(dst + cc * D + lane * 2 + i * 64) =
+              make_float2(y[2 * i], y[2 * i + 1]);
+        if (lane == 0) {
+          dst[C::kCols * D + cc] = mm;
+          dst[C::kCols * (D + 1) + cc] = lk;
+        }
       }
     }
-    if (closed && begun) {
-      const int c = (pt.unit % pt.ntb) * C::kCols + cc;
-      if (c < pt.n * r)
-        store_row<D>(a.out + ((int64_t)(pt.start + c / r) * a.heads + pt.unit / pt.ntb * r + c % r) * D,
-                     y, lk, lane);
-    } else {
-      float* dst = cta_part + ((size_t)blockIdx.x * 2 + (closed || !begun ? 0 : 1)) * C::kPartial;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        *reinterpret_cast<float2*>(dst + cc * D + lane * 2 + i * 64) = make_float2(y[2 * i], y[2 * i + 1]);
-      if (lane == 0) {
-        dst[C::kCols * D + cc] = mm;
-        dst[C::kCols * (D + 1) + cc] = lk;
-      }
-      if (!closed && begun && cc == 0) {
-        cut = true;
-        cut_part = pt;
-      }
+    task -= C::kCols;
+    if (!closed) {
+      // a unit begun here that goes on behind this CTA: its tiles go on from the share's end
+      const long long per = share * W;
+      if (tid == 0)
+        static_cast<Cut*>(a.ws)[blockIdx.x] =
+            Cut{begun ? (int)(blockIdx.x + (pt.left + per - 1) / per) : -1, pt.unit, pt.start, pt.n,
+                pt.ntb, {}};
+      break;
     }
+    from = to;
   }
-  // the unit that goes on behind this CTA: its tiles go on from the share's end
-  const int any_cut = open_run && s_part[__ffs(lasts >> after) - 1 + after][1].first;
-  if (cut && lane == 0) {
-    const long long per = share * W;
-    static_cast<Cut*>(a.ws)[blockIdx.x] = Cut{(int)(blockIdx.x + (cut_part.left + per - 1) / per),
-                                              cut_part.unit, cut_part.start, cut_part.n,
-                                              cut_part.ntb, {}};
-  }
-  if (!any_cut && tid == 0) static_cast<Cut*>(a.ws)[blockIdx.x].last = -1;
 }
 
 // Units that were cut between CTAs, each found at the CTA that began it: their
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
     float mm = fmaxf(mk, m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    const float fk = exp2f(mk - mm), f0 = exp2f(m - mm);
+    const float fk = exp2_fast(mk - mm), f0 = exp2_fast(m - mm);
     lk *= fk;
 #pragma unroll
     for (int o = 16; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
@@ -978,7 +978,7 @@ template <int D>
 size_t bytes_for() {
   const size_t one = (2 + Cfg<D, 1>::kWarps) * (size_t)Cfg<D, 1>::kPartial;
   const size_t two = (2 + Cfg<D, 2>::kWarps) * (size_t)Cfg<D, 2>::kPartial;
-  return kCutBytes + kGrid * 4 * (one > two ? one : two);
+  return (kCutBytes + kGrid * 4 * (one > two ? one : two) + 255) / 256 * 256;
 }
 
 }  // namespace

@@ -1,0 +1,862 @@
+// Attention over the 4-bit cache for rows of many new tokens (prompt chunks),
+// on the 5th-generation tensor cores.
+//
+// A unit is a tile of 128 (head_dim 256) or 2 x 128 queries of one row and kv
+// head: tok tokens x the r query heads that share the head, row i * r + h.  It
+// walks the keys that its last token sees in blocks of 128.  The blocks of all
+// units form one line of work that is cut into equal shares, one per CTA, so a
+// long row, a causal triangle and ragged batches keep all SMs equally busy;
+// units cut by a share's end are merged afterwards in a fixed order.
+//
+// One CTA per SM, warp-specialised, blocks handed over with mbarriers:
+//   warps 0-7   softmax: thread = query row.  Scores come from TMEM, weights go
+//               back to TMEM in fp16 over the scores they came from, as the A
+//               operand of the second product.  head_dim 256: the two warp
+//               groups share a row's columns and swap maxima through shared
+//               memory; else each has its own tile of 128 queries.
+//   warps 8-15  dequantise keys and values to fp16, scale * code + bias, rounded
+//               once: codes by 16-byte loads one block ahead, one LOP3 per pair
+//               (1024 + c or 64 + c), the offset taken off exactly, one fma.
+//               Both land in the 128-byte swizzled layout, the keys read K-major
+//               and the values MN-major by the MMAs.
+//   warp 16     issues the MMAs (M = 128, fp32 accumulators in TMEM): the next
+//               block's scores run while the softmax works on this one's.
+// The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
+// order in which one LOP3 yields pairs): the queries are laid out alike, and the
+// result is put in order when it is stored.
+// fp16 roundings: keys and values 2^-11 once, weights 2^-11 once (their largest
+// near 2^15, so that small ones keep their bits); queries are scaled by a power
+// of two per row.  The maximum that weights refer to follows the scores only
+// when they pass it by 2^8, so the accumulator in TMEM is rarely rescaled.
+#include <type_traits>
+
+#include "kv_common.cuh"
+#include "stream_common.cuh"
+
+namespace moe {
+namespace kv {
+namespace {
+
+using sc::bar_init;
+using sc::bar_wait;
+using sc::su32;
+
+constexpr int kKeys = 128;  // keys of a block
+constexpr int kSoftWarps = 8, kDequantWarps = 8, kMmaWarp = 16;
+constexpr int kThreads = 17 * 32;
+constexpr int kUnitKeys = 384;  // a unit's fixed cost, in keys
+constexpr float kNone = -1e30f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTiles = D == 256 ? 1 : 2;   // query tiles of a unit
+  static constexpr int kStages = D == 256 ? 1 : 2;  // key and value blocks held
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kBlockBytes = kKeys * D * 2;  // one block of keys (or values, or queries)
+  static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes;
+  static constexpr int kPartial = kRows * (D + 2);  // floats: o [row][D], m [row], l [row]
+  static constexpr uint32_t kIdescS = (1u << 4) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
+  static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+                                      ((128u >> 4) << 24);  // bit 16: B is MN-major
+  static constexpr int kO = D == 256 ? 256 : 128;   // TMEM columns between the tiles' results
+  static constexpr int kS = 256;                    // scores: two slots of 128 columns
+};
+
+// The unit that a CTA began and did not end: the last CTA with a part of it (-1: there is none).
+struct Cut {
+  int last, start, n, tok0, kvh, pad[3];
+};
+constexpr size_t kCutBytes = (kGrid * sizeof(Cut) + 255) / 256 * 256;
+
+struct Row {
+  int start, n, len, tiles;  // tiles 0: nothing here
+};
+
+__device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok) {
+  Row i;
+  i.start = a.batch.q_start[b];
+  i.n = a.batch.q_start[b + 1] - i.start;
+  i.len = a.batch.kv_len[b];
+  i.tiles = 0;
+  // (the decode kernel, which sees every row, reports what does not fit)
+  if (i.n <= 0 || i.start < 0 || i.n > a.max_new || i.n > i.len ||
+      (long long)i.len > (long long)a.kv.max_blocks * a.kv.block_tokens ||
+      (long long)i.start + i.n > a.T || (long long)i.n * r <= kDecodeCols)
+    return i;
+  i.tiles = (i.n + tok - 1) / tok;
+  return i;
+}
+
+// Cost of the first j units of a head of the row: each its keys (taking every
+// tile for a full one) and a fixed part.
+__device__ __forceinline__ long long cost_before(const Row& i, int tok, long long j) {
+  return j * (i.len - i.n + kUnitKeys) + (long long)tok * (j * (j + 1) / 2);
+}
+
+struct Unit {
+  int kvh, tok0;     // kv head, first token
+  int blk0, blk1;    // key blocks of this share
+  int blocks;        // key blocks of the unit
+  long long rest;    // cost behind this share's end that still holds blocks
+};
+
+// The walk over a CTA's share; every role runs it for itself.
+struct Walk {
+  int b, kvh, j;
+  long long at, left;  // offset in unit (kvh, j) where the share goes on; what is left of it
+  Row row;
+};
+
+__device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int tok, Unit& u) {
+  while (w.left > 0) {
+    if (w.row.tiles == 0 || w.kvh >= a.kv.kv_heads) {
+      do {
+        if (++w.b >= a.rows) return false;
+        w.row = row_info(a, w.b, r, tok);
+      } while (w.row.tiles == 0);
+      w.kvh = w.j = 0;
+      w.at = 0;
+    }
+    const int seen = w.row.len - w.row.n + min(w.row.n, (w.j + 1) * tok);
+    const long long cost = w.row.len - w.row.n + kUnitKeys + (long long)(w.j + 1) * tok;
+    u.kvh = w.kvh;
+    u.tok0 = w.j * tok;
+    u.blocks = (seen + kKeys - 1) / kKeys;
+    // both ends of a share fall on the same block for the CTAs on either side
+    auto block_at = [&](long long x) {
+      const long long k = (x - kUnitKeys + kKeys / 2) / kKeys;
+      return x <= kUnitKeys ? 0 : (int)min(k, (long long)u.blocks);
+    };
+    u.blk0 = block_at(w.at);
+    const bool whole = w.left >= cost - w.at;
+    u.blk1 = whole ? u.blocks : block_at(w.at + w.left);
+    u.rest = min(cost, kUnitKeys + (long long)u.blocks * kKeys - kKeys / 2) - (w.at + w.left);
+    if (whole) {
+      w.left -= cost - w.at;
+      w.at = 0;
+      if (++w.j >= w.row.tiles) {
+        w.j = 0;
+        ++w.kvh;
+      }
+    } else {
+      w.left = 0;
+    }
+    if (u.blk0 < u.blk1) return true;
+  }
+  return false;
+}
+
+// ------------------------------------------------------------- PTX wrappers
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+// 128-byte swizzled operand, groups of 8 rows 1024 bytes apart; lead: bytes from one
+// 64-column stripe to the next (read MN-major only)
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lead >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+// 32 lanes x 32 columns of 32 bits; the values are there after tm_wait_ld
+__device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+  // the registers pass through, so that nothing reads them before the wait
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// All lanes of a warp wait.  A wait that runs out sets `stop`, and from then on nothing waits:
+// every role runs through (or leaves) its loop and the CTA ends.
+__device__ __forceinline__ void wait_all(uint64_t* bar, uint32_t parity, volatile int& stop) {
+  if (__any_sync(~0u, stop)) return;
+  if (!__all_sync(~0u, bar_wait(su32(bar), parity & 1u))) stop = 1;
+}
+
+// eight codes as fp16 pairs (0,4) (1,5) (2,6) (3,7), scaled
+__device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t s, uint32_t b) {
+  const uint32_t v = w >> 8;
+  uint4 r;
+  r.x = hfma2(hadd2((w & 0x000F000Fu) | 0x64006400u, 0xE400E400u), s, b);  // 1024 + c, - 1024
+  r.y = hfma2(hadd2((w & 0x00F000F0u) | 0x54005400u, 0xD400D400u), s, b);  // 64 + c, - 64
+  r.z = hfma2(hadd2((v & 0x000F000Fu) | 0x64006400u, 0xE400E400u), s, b);
+  r.w = hfma2(hadd2((v & 0x00F000F0u) | 0x54005400u, 0xD400D400u), s, b);
+  return r;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
+  using C = Cfg<D>;
+  constexpr int NT = C::kTiles, S = C::kStages;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, drained;
+  __shared__ uint32_t tmem_slot;
+  __shared__ long long s_scan[17], s_at, s_share;
+  __shared__ int s_row;
+  __shared__ volatile int s_stop;
+  __shared__ float s_fac[C::kRows], s_max[2][2][128], s_sum[2][128];
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int K = a.kv.kv_heads, r = a.heads / K, P = a.kv.block_tokens;
+  const int p_shift = 31 - __clz(P);
+  const int per_tile = 128 / r, tok = per_tile * NT;  // tokens of a tile, of a unit
+  const uint32_t base = (su32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t q_at = base, k_at = q_at + NT * C::kBlockBytes, v_at = k_at + S * C::kBlockBytes;
+
+  if (wid == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(su32(&k_full[i]), kDequantWarps);
+      bar_init(su32(&v_full[i]), kDequantWarps);
+      bar_init(su32(&k_empty[i]), 1);
+      bar_init(su32(&v_empty[i]), 1);
+      bar_init(su32(&s_full[i]), 1);
+      bar_init(su32(&p_full[i]), NT == 1 ? kSoftWarps : kSoftWarps / 2);
+      bar_init(su32(&o_done[i]), 1);
+    }
+    bar_init(su32(&q_full), kSoftWarps);
+    bar_init(su32(&drained), 1);
+    s_row = -1;
+    s_stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  griddep_wait();
+
+  // ------------------------------------------------------- this CTA's share
+  long long total = 0;
+  const int chunks = (a.rows + kThreads - 1) / kThreads;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long carry = 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c * kThreads + tid;
+      long long cost = 0;
+      if (b < a.rows) {
+        const Row i = row_info(a, b, r, tok);
+        if (i.tiles) cost = K * cost_before(i, tok, i.tiles);
+      }
+      long long v = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+      }
+      __syncthreads();
+      if (lane == 31) s_scan[wid] = v;
+      __syncthreads();
+      long long before = carry, sum = 0;
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < wid) before += s_scan[i];
+        sum += s_scan[i];
+      }
+      if (pass == 0) {
+        total = carry + sum;
+      } else {
+        const long long share = max((total + kGrid - 1) / kGrid, 2ll * kKeys);
+        const long long pre = before + v - cost, x0 = blockIdx.x * share;
+        if (x0 < total && x0 >= pre && x0 < pre + cost) {
+          s_row = b;
+          s_at = x0 - pre;
+        }
+        if (tid == 0) s_share = share;
+      }
+      carry += sum;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = tmem_slot;
+  Cut* cuts = static_cast<Cut*>(a.ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kCutBytes);
+  if (tid == 0) cuts[blockIdx.x].last = -1;
+
+  Walk walk;
+  walk.left = 0;
+  if (s_row >= 0) {
+    walk.b = s_row;
+    walk.row = row_info(a, walk.b, r, tok);
+    walk.left = min(s_share, total - blockIdx.x * s_share);
+    const long long per_head = cost_before(walk.row, tok, walk.row.tiles);
+    long long x = s_at;
+    walk.kvh = (int)(x / per_head);
+    x -= walk.kvh * per_head;
+    int lo = 0, hi = walk.row.tiles;  // the last unit whose cost_before is <= x
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost_before(walk.row, tok, mid) <= x) lo = mid;
+      else hi = mid;
+    }
+    walk.j = lo;
+    walk.at = x - cost_before(walk.row, tok, lo);
+  }
+  Unit u;
+
+  if (wid < kSoftWarps) {
+    // ---------------------------------------------------------------- softmax
+    const int wg = wid >> 2, row = (wid & 3) * 32 + lane;  // TMEM lane
+    const int tile = NT == 1 ? 0 : wg;
+    const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
+    const uint32_t o_tm = tmem + lanes + tile * C::kO;
+    uint32_t n_s = 0, n_o = 0;  // blocks of scores seen, products seen
+    while (next_unit(walk, a, r, tok, u)) {
+      const Row ri = walk.row;
+      const int b = walk.b;
+      // ---- queries: a warp's rows in turn, 8 columns a lane, largest first
+      for (int i = 0; i < C::kRows / kSoftWarps; ++i) {
+        const int qr = wid * (C::kRows / kSoftWarps) + i, in = qr & 127;
+        const int t = u.tok0 + (qr >> 7) * per_tile + in / r;
+        constexpr int kLanes = D / 8;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (lane < kLanes && in < per_tile * r && t < ri.n)
+          raw = *reinterpret_cast<const uint4*>(
+              a.q + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + in % r) * D + lane * 8);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
+        big = __reduce_max_sync(~0u, max(big & 0xFFFFu, big >> 16));
+        const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
+        const float up = pow2(14 - e);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[2 * k] = __uint_as_float(w[k] << 16) * up;
+          x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+        }
+        if (lane < kLanes)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           q_at + (qr >> 7) * C::kBlockBytes + (lane >> 3) * (kKeys * 128) + in * 128 +
+                           (((lane & 7) ^ (in & 7)) << 4)),
+                       "r"(pack_h2(x[0], x[4])), "r"(pack_h2(x[1], x[5])),
+                       "r"(pack_h2(x[2], x[6])), "r"(pack_h2(x[3], x[7]))
+                       : "memory");
+        // score = fac * accumulated, in units of log2
+        if (lane == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) sc::bar_arrive(su32(&q_full));
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // s_fac of all rows
+      const float fac = s_fac[tile * 128 + row];
+      const int t = u.tok0 + tile * per_tile + row / r;
+      const bool live = row < per_tile * r && t < ri.n;
+      const int lim = ri.len - ri.n + min(t, ri.n - 1);             // last key that the row sees
+      const int open = ri.len - ri.n + u.tok0 + tile * per_tile;   // all rows see the keys up to it
+      float m = kNone, l = 0.0f;
+      for (int i = u.blk0; i < u.blk1; ++i) {
+        const int slot = NT == 1 ? (int)(n_s & 1u) : tile;
+        // tiles of the block that are missing (a block id outside the pool)
+        uint32_t miss = 0;
+        {
+          const int at = i * (kKeys / kTile) + lane;
+          int block = 0;
+          if (lane < kKeys / kTile && at * kTile < ri.len)
+            block = a.kv.block_table[(int64_t)b * a.kv.max_blocks + ((at * kTile) >> p_shift)];
+          miss = __ballot_sync(~0u, (unsigned)block >= (unsigned)a.kv.num_blocks);
+        }
+        wait_all(&s_full[slot], NT == 1 ? n_s >> 1 : n_s, s_stop);
+        tc_after();
+        ++n_s;
+        const uint32_t s_tm = tmem + lanes + C::kS + slot * 128;
+        const int key0 = i * kKeys;
+        const bool edge = key0 + kKeys > open + 1 || miss != 0;
+        constexpr int kChunks = NT == 1 ? 2 : 4;  // of 32 columns
+        const int c_first = NT == 1 ? wg * 2 : 0;
+        auto hide = [&](uint32_t (&v)[32], int c) {
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (key0 + c * 32 + k > lim || ((miss >> (c * 2 + k / 16)) & 1u)) v[k] = 0xFF800000u;
+          }
+        };
+        // the row's maximum; accumulators follow when it passes the reference by 2^8
+        auto refer = [&](float top) {
+          float f = 1.0f;
+          if (top > m + 8.0f) {
+            f = ex2(m - top);
+            m = top;
+          }
+          l *= f;
+          if (i > u.blk0 && __any_sync(~0u, f != 1.0f)) {
+            wait_all(&o_done[tile], n_o - 1, s_stop);
+            tc_after();
+            constexpr int kCols = NT == 1 ? D / 2 : D;
+#pragma unroll 1
+            for (int c = 0; c < kCols; c += 32) {
+              uint32_t v[32];
+              const uint32_t at = o_tm + (NT == 1 ? wg * (D / 2) : 0) + c;
+              tm_ld32(at, v);
+              tm_wait_ld(v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+              tm_st16(at, v);
+              tm_st16(at + 16, v + 16);
+            }
+            tm_wait_st();
+          }
+        };
+        auto weights = [&](uint32_t (&v)[32], int c) {
+          uint32_t p[16];
+          const float off = 7.0f - m;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = ex2(fmaf(__uint_as_float(v[2 * k]), fac, off));
+            const float y = ex2(fmaf(__uint_as_float(v[2 * k + 1]), fac, off));
+            l += x + y;
+            p[k] = pack_h2(x, y);
+          }
+          tm_st16(s_tm + c * 16, p);
+        };
+        if constexpr (NT == 1) {
+          uint32_t v0[32], v1[32];
+          tm_ld32(s_tm + c_first * 32, v0);
+          tm_ld32(s_tm + c_first * 32 + 32, v1);
+          tm_wait_ld(v0);
+          tm_wait_ld(v1);
+          hide(v0, c_first);
+          hide(v1, c_first + 1);
+          float top = kNone;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            top = fmaxf(top, fmaxf(__uint_as_float(v0[k]), __uint_as_float(v1[k])));
+          // both halves of the row, and (every score being in registers by then) the weights
+          // may go over the scores
+          s_max[n_s & 1u][wg][row] = top;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          top = fmaxf(top, s_max[n_s & 1u][wg ^ 1][row]);
+          refer(top * fac);
+          weights(v0, c_first);
+          weights(v1, c_first + 1);
+        } else {
+          float top = kNone;
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t v[32];
+            tm_ld32(s_tm + c * 32, v);
+            tm_wait_ld(v);
+            hide(v, c);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(v[k]));
+          }
+          refer(top * fac);
+#pragma unroll 1
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t v[32];
+            tm_ld32(s_tm + c * 32, v);
+            tm_wait_ld(v);
+            hide(v, c);
+            weights(v, c);
+          }
+        }
+        ++n_o;
+        tm_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) sc::bar_arrive(su32(&p_full[slot]));
+      }
+      // ---- the unit's end (here): a result, or a part of one
+      wait_all(&o_done[tile], n_o - 1, s_stop);
+      tc_after();
+      if constexpr (NT == 1) {
+        s_sum[wg][row] = l;
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        l += s_sum[wg ^ 1][row];
+      }
+      const bool whole = u.blk0 == 0 && u.blk1 == u.blocks;
+      const float inv = l > 0.0f ? 1.0f / l : l;
+      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + row % r) * D;
+      float* part = parts + ((size_t)blockIdx.x * 2 + (u.blk0 == 0 ? 1 : 0)) * C::kPartial;
+      const int pr = tile * 128 + row;
+      constexpr int kCols = NT == 1 ? D / 2 : D;
+      const int c_at = NT == 1 ? wg * (D / 2) : 0;
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 32) {
+        uint32_t v[32];
+        tm_ld32(o_tm + c_at + c, v);
+        tm_wait_ld(v);
+        if (live) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          // columns in order: 0,4,1,5,2,6,3,7 -> 0..7
+          const float y[8] = {__uint_as_float(v[k]),     __uint_as_float(v[k + 2]),
+                              __uint_as_float(v[k + 4]), __uint_as_float(v[k + 6]),
+                              __uint_as_float(v[k + 1]), __uint_as_float(v[k + 3]),
+                              __uint_as_float(v[k + 5]), __uint_as_float(v[k + 7])};
+          if (whole) {
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(y[2 * q] * inv, y[2 * q + 1] * inv);
+              h[q] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(dst + c_at + c + k) = make_uint4(h[0], h[1], h[2], h[3]);
+          } else {
+            float* at = part + (size_t)pr * D + c_at + c + k;
+            *reinterpret_cast<float4*>(at) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4*>(at + 4) = make_float4(y[4], y[5], y[6], y[7]);
+          }
+        }
+        }
+        __syncwarp();
+      }
+      if (!whole && (NT == 2 || wg == 0)) {
+        part[(size_t)C::kRows * D + pr] = m;
+        part[(size_t)C::kRows * (D + 1) + pr] = l;
+      }
+      if (u.blk0 == 0 && !whole && tid == 0)  // begun here; it goes on at the next share's start
+        cuts[blockIdx.x] = Cut{(int)(blockIdx.x + (u.rest + s_share - 1) / s_share), ri.start, ri.n,
+                               u.tok0, u.kvh, {}};
+      tc_before();
+      __syncwarp();
+    }
+  } else if (wid < kSoftWarps + kDequantWarps) {
+    // ------------------------------------------------------------- dequantise
+    constexpr int kChunks = D / 64;               // 16-byte chunks of codes per thread
+    constexpr int kGroups = D == 256 ? 2 : 1;     // and quantisation groups
+    const int dt = tid - kSoftWarps * 32, key = dt & 127, half = dt >> 7;
+    const int in_tile = key & 15, sw = swizzle<D>(in_tile);
+    struct Piece {
+      uint4 code[kChunks];
+      uint16_t s[kGroups], b[kGroups];
+    };
+    uint32_t n_k = 0, n_v = 0;
+    while (next_unit(walk, a, r, tok, u)) {
+      const int len = walk.row.len;
+      const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
+      auto block_of = [&](int i) {
+        const int j = i * kKeys + key;
+        int block = -1;
+        if (i < u.blk1 && j < len) block = table[j >> p_shift];
+        return block;
+      };
+      // which: 0 keys, 1 values; a key that is not there reads as zeros
+      auto load = [&](Piece& pc, int i, int block, int which) {
+        const int j = i * kKeys + key;
+        const bool ok = (unsigned)block < (unsigned)a.kv.num_blocks;
+        const uint8_t* tile =
+            static_cast<const uint8_t*>(a.kv.pool) +
+            (((int64_t)(ok ? block : 0) * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
+        const uint8_t* row = tile + which * 8 * D + in_tile * (D / 2);
+        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + 16 * D);
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          pc.code[c] = ok ? *reinterpret_cast<const uint4*>(row + (((half * kChunks + c) ^ sw) << 4))
+                          : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) {
+          const int g = half * kChunks / 2 + c;
+          const int s = which ? Meta<D>::v_scale(in_tile, g) : Meta<D>::k_scale(in_tile, g);
+          const int b = which ? Meta<D>::v_bias(in_tile, g) : Meta<D>::k_bias(in_tile, g);
+          pc.s[c] = ok ? meta[s] : (uint16_t)0;
+          pc.b[c] = ok ? meta[b] : (uint16_t)0;
+        }
+      };
+      auto store = [&](const Piece& pc, uint32_t at) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const int chunk = half * kChunks + c, g = D == 256 ? c / 2 : 0;
+          const uint32_t s = pc.s[g] * 0x10001u, b = pc.b[g] * 0x10001u;
+          const uint32_t w[4] = {pc.code[c].x, pc.code[c].y, pc.code[c].z, pc.code[c].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = dequant8(w[i], s, b);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             at + (chunk >> 1) * (kKeys * 128) + key * 128 +
+                             ((((chunk & 1) * 4 + i) ^ (key & 7)) << 4)),
+                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                         : "memory");
+          }
+        }
+        fence_async();
+        __syncwarp();
+      };
+      Piece pk, pv;
+      int block = block_of(u.blk0), ahead = block_of(u.blk0 + 1);
+      load(pk, u.blk0, block, 0);
+      for (int i = u.blk0; i < u.blk1; ++i) {
+        load(pv, i, block, 1);
+        int st = n_k % S;
+        if (n_k >= S) wait_all(&k_empty[st], n_k / S - 1, s_stop);
+        store(pk, k_at + st * C::kBlockBytes);
+        if (lane == 0) sc::bar_arrive(su32(&k_full[st]));
+        ++n_k;
+        block = ahead;
+        ahead = block_of(i + 2);
+        load(pk, i + 1, block, 0);
+        st = n_v % S;
+        if (n_v >= S) wait_all(&v_empty[st], n_v / S - 1, s_stop);
+        store(pv, v_at + st * C::kBlockBytes);
+        if (lane == 0) sc::bar_arrive(su32(&v_full[st]));
+        ++n_v;
+      }
+    }
+  } else {
+    // -------------------------------------------------------------------- MMAs
+    uint32_t n_u = 0, n_k = 0, n_v = 0, n_s = 0, n_p = 0;
+    auto scores = [&](int tile, uint32_t st, int slot) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+          mma_ss(tmem + C::kS + slot * 128, smem_desc(q_at + tile * C::kBlockBytes + off, 16),
+                 smem_desc(k_at + st * C::kBlockBytes + off, 16), C::kIdescS, k > 0);
+        }
+        commit(su32(&s_full[slot]));
+      }
+    };
+    auto product = [&](int tile, uint32_t st, int slot, bool more) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8,
+                 smem_desc(v_at + st * C::kBlockBytes + k * 2048, kKeys * 128), C::kIdescO,
+                 more || k > 0);
+        commit(su32(&o_done[tile]));
+      }
+    };
+    auto freed = [&](uint64_t* bar) {
+      if (lane == 0) commit(su32(bar));
+      __syncwarp();
+    };
+    while (next_unit(walk, a, r, tok, u)) {
+      wait_all(&q_full, n_u++, s_stop);
+      const int nb = u.blk1 - u.blk0;
+      if constexpr (NT == 1) {
+        for (int i = 0; i <= nb; ++i) {
+          if (i < nb) {
+            const uint32_t st = n_k % S;
+            wait_all(&k_full[st], n_k / S, s_stop);
+            if (__any_sync(~0u, s_stop)) break;
+            tc_after();
+            scores(0, st, n_s & 1u);
+            freed(&k_empty[st]);
+            ++n_k;
+            ++n_s;
+          }
+          if (i > 0) {
+            const uint32_t st = n_v % S, slot = n_p & 1u;
+            wait_all(&v_full[st], n_v / S, s_stop);
+            wait_all(&p_full[slot], n_p >> 1, s_stop);
+            if (__any_sync(~0u, s_stop)) break;
+            tc_after();
+            product(0, st, slot, i > 1);
+            freed(&v_empty[st]);
+            ++n_v;
+            ++n_p;
+          }
+        }
+      } else {
+        wait_all(&k_full[n_k % S], n_k / S, s_stop);
+        if (__any_sync(~0u, s_stop)) break;
+        tc_after();
+        scores(0, n_k % S, 0);
+        scores(1, n_k % S, 1);
+        freed(&k_empty[n_k % S]);
+        ++n_k;
+        for (int i = 0; i < nb; ++i) {
+          const bool on = i + 1 < nb;
+          const uint32_t sv = n_v % S, sk = n_k % S;
+          wait_all(&v_full[sv], n_v / S, s_stop);
+          wait_all(&p_full[0], n_p, s_stop);
+          if (__any_sync(~0u, s_stop)) break;
+          tc_after();
+          product(0, sv, 0, i > 0);
+          if (on) {
+            wait_all(&k_full[sk], n_k / S, s_stop);
+            if (__any_sync(~0u, s_stop)) break;
+            tc_after();
+            scores(0, sk, 0);
+          }
+          wait_all(&p_full[1], n_p, s_stop);
+          if (__any_sync(~0u, s_stop)) break;
+          tc_after();
+          product(1, sv, 1, i > 0);
+          freed(&v_empty[sv]);
+          if (on) {
+            scores(1, sk, 1);
+            freed(&k_empty[sk]);
+            ++n_k;
+          }
+          ++n_v;
+          ++n_p;
+        }
+      }
+      if (__any_sync(~0u, s_stop)) break;
+    }
+    if (lane == 0) commit(su32(&drained));  // nothing is under way when TMEM goes back
+    __syncwarp();
+    if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  griddep_launch();
+  if (tid == 0 && s_stop) {
+    atomicOr(a.batch.err, MOE_DERR_WAIT);
+    cuts[blockIdx.x].last = -1;
+  }
+  if (wid == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+// Units that were cut between CTAs, each found at the CTA that began it: a warp
+// per query row, its parts in order.
+template <int D>
+__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
+  using C = Cfg<D>;
+  griddep_wait();
+  const int first = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Cut cut = static_cast<const Cut*>(a.ws)[first];
+  if (cut.last <= first) return;
+  const int r = a.heads / a.kv.kv_heads, per_tile = 128 / r, in = row & 127;
+  const int t = cut.tok0 + (row >> 7) * per_tile + in / r;
+  if (in >= per_tile * r || t >= cut.n) return;
+  const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kCutBytes);
+  float m = kNone, l = 0.0f, y[D / 32] = {};
+  for (int k0 = first; k0 <= cut.last; k0 += 32) {
+    const int mine = k0 + lane;  // lane i: part k0 + i
+    float mk = kNone, lk = 0.0f;
+    if (mine <= cut.last) {
+      const float* src = parts + ((size_t)mine * 2 + (mine == first)) * C::kPartial;
+      mk = src[(size_t)C::kRows * D + row];
+      lk = src[(size_t)C::kRows * (D + 1) + row];
+    }
+    float mm = fmaxf(mk, m);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+    const float fk = ex2(mk - mm), f0 = ex2(m - mm);
+    lk *= fk;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
+    l = fmaf(l, f0, lk);
+    m = mm;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) y[i] *= f0;
+    const int n = min(32, cut.last - k0 + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int k = k0 + i;
+      const float f = __shfl_sync(~0u, fk, i);
+      const float* src =
+          parts + ((size_t)k * 2 + (k == first)) * C::kPartial + (size_t)row * D + lane * 2;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const float2 v = *reinterpret_cast<const float2*>(src + j * 64);
+        y[2 * j] = fmaf(f, v.x, y[2 * j]);
+        y[2 * j + 1] = fmaf(f, v.y, y[2 * j + 1]);
+      }
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : l;
+  uint16_t* dst = a.out + ((int64_t)(cut.start + t) * a.heads + cut.kvh * r + in % r) * D;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(y[2 * i] * inv, y[2 * i + 1] * inv);
+    *reinterpret_cast<uint32_t*>(dst + lane * 2 + i * 64) = *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+template <int D>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  using C = Cfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(prompt_kernel<D>, dim3(kGrid), dim3(kThreads), C::kSmem, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(combine_kernel<D>, dim3(kGrid, C::kRows / 8), dim3(256), 0, st, a);
+}
+
+template <int D>
+size_t bytes_for() {
+  return kCutBytes + (size_t)kGrid * 2 * Cfg<D>::kPartial * 4;
+}
+
+}  // namespace
+
+size_t prompt_workspace_bytes(int D) {
+  return D == 256 ? bytes_for<256>() : D == 128 ? bytes_for<128>() : bytes_for<64>();
+}
+
+cudaError_t launch_prompt(const AttnArgs& a, cudaStream_t st) {
+  const int D = a.kv.head_dim;
+  return D == 256 ? launch<256>(a, st) : D == 128 ? launch<128>(a, st) : launch<64>(a, st);
+}
+
+}  // namespace kv
+}  // namespace moe
