@@ -14,13 +14,16 @@
 //               operand of the second product.  head_dim 256: the two warp
 //               groups share a row's columns and swap maxima through shared
 //               memory; else each has its own tile of 128 queries.
-//   warps 8-15  dequantise keys and values to fp16, scale * code + bias, rounded
-//               once: codes by 16-byte loads one block ahead, one LOP3 per pair
-//               (1024 + c or 64 + c), the offset taken off exactly, one fma.
-//               Both land in the 128-byte swizzled layout, the keys read K-major
-//               and the values MN-major by the MMAs.
-//   warp 16     issues the MMAs (M = 128, fp32 accumulators in TMEM): the next
+//   warps 8-15  dequantise keys to fp16, scale * code + bias, rounded once;
+//   warps 16-23 values alike.  Codes come by 16-byte loads one block ahead, one
+//               LOP3 per pair (1024 + c or 64 + c), the offset taken off exactly,
+//               one fma.  Both land in the 128-byte swizzled layout, the keys read
+//               K-major and the values MN-major by the MMAs.
+//   warp 24     issues the MMAs (M = 128, fp32 accumulators in TMEM): the next
 //               block's scores run while the softmax works on this one's.
+// Registers move from the dequantising warps and the MMA warp's group to the
+// softmax (the block starts with 72 a thread, and 112 / 56 / 48 of them add up to
+// less than that).
 // The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
 // order in which one LOP3 yields pairs): the queries are laid out alike, and the
 // result is put in order when it is stored.
@@ -42,8 +45,11 @@ using sc::bar_wait;
 using sc::su32;
 
 constexpr int kKeys = 128;  // keys of a block
-constexpr int kSoftWarps = 8, kDequantWarps = 8, kMmaWarp = 16;
-constexpr int kThreads = 17 * 32;
+constexpr int kSoftWarps = 8, kSideWarps = 8, kMmaWarp = 24;
+constexpr int kThreads = 28 * 32;  // seven warp groups; three warps of the last one idle
+constexpr int kSoftRegs = 112, kSideRegs = 56, kMmaRegs = 48, kStartRegs = 72;
+static_assert(kSoftRegs * 256 + kSideRegs * 512 + kMmaRegs * 128 <= kStartRegs * kThreads,
+              "the registers given out are there");
 constexpr int kUnitKeys = 384;  // a unit's fixed cost, in keys
 constexpr float kNone = -1e30f;
 
@@ -234,11 +240,37 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t y, uint32_t z) {
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
-// All lanes of a warp wait.  A wait that runs out sets `stop`, and from then on nothing waits:
-// every role runs through (or leaves) its loop and the CTA ends.
+// All lanes of a warp wait, bounded as every wait is (stream_common.cuh).  A wait that runs out
+// sets `stop`, and from then on nothing waits: every role runs through (or leaves) its loop and
+// the CTA ends.
 __device__ __forceinline__ void wait_all(uint64_t* bar, uint32_t parity, volatile int& stop) {
-  if (__any_sync(~0u, stop)) return;
-  if (!__all_sync(~0u, bar_wait(su32(bar), parity & 1u))) stop = 1;
+  long long t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(su32(bar)), "r"(parity & 1u)
+        : "memory");
+    if (done) break;
+    if ((i & 15u) == 15u) {
+      if (stop) break;
+      const long long t = clock64();
+      if (t0 == 0) t0 = t;
+      else if (t - t0 > sc::kWaitCycles || i > sc::kSpin) {
+        stop = 1;
+        break;
+      }
+    }
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // eight codes as fp16 pairs (0,4) (1,5) (2,6) (3,7), scaled
@@ -252,15 +284,25 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w, uint32_t s, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   using C = Cfg<D>;
   constexpr int NT = C::kTiles, S = C::kStages;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, drained;
+  constexpr int KC = D / 64, VC = 4;  // chunks of a block: 64 columns of keys, 32 values
+  // A block of keys or values is there; a tile's scores, weights, product are.  The last two by
+  // the block's parity: a buffer's next block waits for the scores (products) of the block that
+  // it replaces, which are never more than one phase of that barrier ago.
+  __shared__ __align__(8) uint64_t k_full[S], v_full[S], p_full[NT][2];
+  __shared__ __align__(8) uint64_t s_full[NT][2], o_done[NT][2], q_full, drained;
   __shared__ uint32_t tmem_slot;
-  __shared__ long long s_scan[17], s_at, s_share;
+  __shared__ long long s_scan[kThreads / 32], s_at, s_share;
   __shared__ int s_row;
   __shared__ volatile int s_stop;
   __shared__ float s_fac[C::kRows], s_max[2][2][128], s_sum[2][128];
@@ -268,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   const int K = a.kv.kv_heads, r = a.heads / K, P = a.kv.block_tokens;
   const int p_shift = 31 - __clz(P);
   const int per_tile = 128 / r, tok = per_tile * NT;  // tokens of a tile, of a unit
+  const uint32_t r_inv = (65536 + r - 1) / r;         // x * r_inv >> 16 = x / r for x < 128
   const uint32_t base = (su32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + NT * C::kBlockBytes, v_at = k_at + S * C::kBlockBytes;
 
@@ -279,14 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      bar_init(su32(&k_full[i]), kDequantWarps);
-      bar_init(su32(&v_full[i]), kDequantWarps);
-      bar_init(su32(&k_empty[i]), 1);
-      bar_init(su32(&v_empty[i]), 1);
-      bar_init(su32(&s_full[i]), 1);
-      bar_init(su32(&p_full[i]), NT == 1 ? kSoftWarps : kSoftWarps / 2);
-      bar_init(su32(&o_done[i]), 1);
+    for (int i = 0; i < S; ++i) {
+      bar_init(su32(&k_full[i]), kSideWarps);
+      bar_init(su32(&v_full[i]), kSideWarps);
+    }
+    for (int i = 0; i < 2 * NT; ++i) {
+      bar_init(su32(&s_full[0][0] + i), 1);
+      bar_init(su32(&o_done[0][0] + i), 1);
+      bar_init(su32(&p_full[0][0] + i), kSoftWarps / NT);
     }
     bar_init(su32(&q_full), kSoftWarps);
     bar_init(su32(&drained), 1);
@@ -367,70 +410,81 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
 
   if (wid < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int wg = wid >> 2, row = (wid & 3) * 32 + lane;  // TMEM lane
     const int tile = NT == 1 ? 0 : wg;
     const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lanes + tile * C::kO;
-    uint32_t n_s = 0, n_o = 0;  // blocks of scores seen, products seen
+    uint32_t n = 0;  // blocks seen
     while (next_unit(walk, a, r, tok, u)) {
       const Row ri = walk.row;
       const int b = walk.b;
-      // ---- queries: a warp's rows in turn, 8 columns a lane, largest first
-      for (int i = 0; i < C::kRows / kSoftWarps; ++i) {
-        const int qr = wid * (C::kRows / kSoftWarps) + i, in = qr & 127;
-        const int t = u.tok0 + (qr >> 7) * per_tile + in / r;
-        constexpr int kLanes = D / 8;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (lane < kLanes && in < per_tile * r && t < ri.n)
-          raw = *reinterpret_cast<const uint4*>(
-              a.q + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + in % r) * D + lane * 8);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t big = 0;
+      // ---- queries: a warp's rows, 8 columns a lane, a few loads under way at a time
+      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = C::kRows / kSoftWarps / kAtOnce;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kRounds; i0 += 8) {
+        uint4 raw[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
-        big = __reduce_max_sync(~0u, max(big & 0xFFFFu, big >> 16));
-        const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
-        const float up = pow2(14 - e);
-        float x[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          x[2 * k] = __uint_as_float(w[k] << 16) * up;
-          x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+        for (int i = 0; i < 8; ++i) {
+          const int qr = (wid * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
+          const int i_tok = (int)(in * r_inv >> 16), t = u.tok0 + (qr >> 7) * per_tile + i_tok;
+          raw[i] = make_uint4(0, 0, 0, 0);
+          if (in < per_tile * r && t < ri.n)
+            raw[i] = *reinterpret_cast<const uint4*>(
+                a.q + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
+                lane % kLanes * 8);
         }
-        if (lane < kLanes)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           q_at + (qr >> 7) * C::kBlockBytes + (lane >> 3) * (kKeys * 128) + in * 128 +
-                           (((lane & 7) ^ (in & 7)) << 4)),
-                       "r"(pack_h2(x[0], x[4])), "r"(pack_h2(x[1], x[5])),
-                       "r"(pack_h2(x[2], x[6])), "r"(pack_h2(x[3], x[7]))
-                       : "memory");
-        // score = fac * accumulated, in units of log2
-        if (lane == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int qr = (wid * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
+          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+          uint32_t big = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
+          big = max(big & 0xFFFFu, big >> 16);
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(~0u, big, o));
+          const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
+          const float up = pow2(14 - e);
+          float x[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16) * up;
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
+          }
+          const int col8 = lane % kLanes;
+          sts128(q_at + (qr >> 7) * C::kBlockBytes + (col8 >> 3) * (kKeys * 128) + in * 128 +
+                     (((col8 & 7) ^ (in & 7)) << 4),
+                 make_uint4(pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]),
+                            pack_h2(x[3], x[7])));
+          // score = fac * accumulated, in units of log2
+          if (col8 == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
+        }
       }
       fence_async();
       __syncwarp();
       if (lane == 0) sc::bar_arrive(su32(&q_full));
       asm volatile("bar.sync 1, 256;" ::: "memory");  // s_fac of all rows
       const float fac = s_fac[tile * 128 + row];
-      const int t = u.tok0 + tile * per_tile + row / r;
+      const int row_tok = (int)(row * r_inv >> 16), row_h = row - row_tok * r;
+      const int t = u.tok0 + tile * per_tile + row_tok;
       const bool live = row < per_tile * r && t < ri.n;
       const int lim = ri.len - ri.n + min(t, ri.n - 1);             // last key that the row sees
       const int open = ri.len - ri.n + u.tok0 + tile * per_tile;   // all rows see the keys up to it
       float m = kNone, l = 0.0f;
+      // the tiles of a block that are missing (a block id outside the pool), looked up a block ahead
+      auto block_of = [&](int i) {
+        const int at = i * (kKeys / kTile) + lane;
+        return lane < kKeys / kTile && at * kTile < ri.len
+                   ? a.kv.block_table[(int64_t)b * a.kv.max_blocks + ((at * kTile) >> p_shift)] : 0;
+      };
+      int block = block_of(u.blk0);
       for (int i = u.blk0; i < u.blk1; ++i) {
-        const int slot = NT == 1 ? (int)(n_s & 1u) : tile;
-        // tiles of the block that are missing (a block id outside the pool)
-        uint32_t miss = 0;
-        {
-          const int at = i * (kKeys / kTile) + lane;
-          int block = 0;
-          if (lane < kKeys / kTile && at * kTile < ri.len)
-            block = a.kv.block_table[(int64_t)b * a.kv.max_blocks + ((at * kTile) >> p_shift)];
-          miss = __ballot_sync(~0u, (unsigned)block >= (unsigned)a.kv.num_blocks);
-        }
-        wait_all(&s_full[slot], NT == 1 ? n_s >> 1 : n_s, s_stop);
+        const int slot = NT == 1 ? (int)(n & 1u) : tile;
+        const uint32_t miss = __ballot_sync(~0u, (unsigned)block >= (unsigned)a.kv.num_blocks);
+        block = block_of(i + 1);
+        wait_all(&s_full[tile][n & 1u], n >> 1, s_stop);
         tc_after();
-        ++n_s;
         const uint32_t s_tm = tmem + lanes + C::kS + slot * 128;
         const int key0 = i * kKeys;
         const bool edge = key0 + kKeys > open + 1 || miss != 0;
@@ -452,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           }
           l *= f;
           if (i > u.blk0 && __any_sync(~0u, f != 1.0f)) {
-            wait_all(&o_done[tile], n_o - 1, s_stop);
+            wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
             tc_after();
             constexpr int kCols = NT == 1 ? D / 2 : D;
 #pragma unroll 1
@@ -495,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             top = fmaxf(top, fmaxf(__uint_as_float(v0[k]), __uint_as_float(v1[k])));
           // both halves of the row, and (every score being in registers by then) the weights
           // may go over the scores
-          s_max[n_s & 1u][wg][row] = top;
+          s_max[n & 1u][wg][row] = top;
           asm volatile("bar.sync 1, 256;" ::: "memory");
-          top = fmaxf(top, s_max[n_s & 1u][wg ^ 1][row]);
+          top = fmaxf(top, s_max[n & 1u][wg ^ 1][row]);
           refer(top * fac);
           weights(v0, c_first);
           weights(v1, c_first + 1);
@@ -522,14 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             weights(v, c);
           }
         }
-        ++n_o;
         tm_wait_st();
         tc_before();
         __syncwarp();
-        if (lane == 0) sc::bar_arrive(su32(&p_full[slot]));
+        if (lane == 0) sc::bar_arrive(su32(&p_full[tile][n & 1u]));
+        ++n;
       }
       // ---- the unit's end (here): a result, or a part of one
-      wait_all(&o_done[tile], n_o - 1, s_stop);
+      wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
       tc_after();
       if constexpr (NT == 1) {
         s_sum[wg][row] = l;
@@ -538,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       }
       const bool whole = u.blk0 == 0 && u.blk1 == u.blocks;
       const float inv = l > 0.0f ? 1.0f / l : l;
-      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + row % r) * D;
+      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + row_h) * D;
       float* part = parts + ((size_t)blockIdx.x * 2 + (u.blk0 == 0 ? 1 : 0)) * C::kPartial;
       const int pr = tile * 128 + row;
       constexpr int kCols = NT == 1 ? D / 2 : D;
@@ -583,183 +637,207 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       tc_before();
       __syncwarp();
     }
-  } else if (wid < kSoftWarps + kDequantWarps) {
-    // ------------------------------------------------------------- dequantise
-    constexpr int kChunks = D / 64;               // 16-byte chunks of codes per thread
-    constexpr int kGroups = D == 256 ? 2 : 1;     // and quantisation groups
-    const int dt = tid - kSoftWarps * 32, key = dt & 127, half = dt >> 7;
+  } else if (wid < kSoftWarps + kSideWarps) {
+    // ------------- keys: a thread per key and half of a chunk's 64 columns
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+    const int key = (tid - kSoftWarps * 32) & 127, half = (tid - kSoftWarps * 32) >> 7;
     const int in_tile = key & 15, sw = swizzle<D>(in_tile);
-    struct Piece {
-      uint4 code[kChunks];
-      uint16_t s[kGroups], b[kGroups];
-    };
-    uint32_t n_k = 0, n_v = 0;
+    uint4 code[KC];
+    uint32_t meta[KC];  // scale | bias << 16
+    uint32_t n = 0;     // blocks written
     while (next_unit(walk, a, r, tok, u)) {
       const int len = walk.row.len;
       const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
-      auto block_of = [&](int i) {
+      auto tile_at = [&](int i) -> const uint8_t* {  // the key's tile; null: it is not there
         const int j = i * kKeys + key;
-        int block = -1;
-        if (i < u.blk1 && j < len) block = table[j >> p_shift];
-        return block;
+        if (i >= u.blk1 || j >= len) return nullptr;
+        const int block = table[j >> p_shift];
+        if ((unsigned)block >= (unsigned)a.kv.num_blocks) return nullptr;
+        return static_cast<const uint8_t*>(a.kv.pool) +
+               (((int64_t)block * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
       };
-      // which: 0 keys, 1 values; a key that is not there reads as zeros
-      auto load = [&](Piece& pc, int i, int block, int which) {
-        const int j = i * kKeys + key;
-        const bool ok = (unsigned)block < (unsigned)a.kv.num_blocks;
-        const uint8_t* tile =
-            static_cast<const uint8_t*>(a.kv.pool) +
-            (((int64_t)(ok ? block : 0) * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
-        const uint8_t* row = tile + which * 8 * D + in_tile * (D / 2);
-        const uint16_t* meta = reinterpret_cast<const uint16_t*>(tile + 16 * D);
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          pc.code[c] = ok ? *reinterpret_cast<const uint4*>(row + (((half * kChunks + c) ^ sw) << 4))
-                          : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c) {
-          const int g = half * kChunks / 2 + c;
-          const int s = which ? Meta<D>::v_scale(in_tile, g) : Meta<D>::k_scale(in_tile, g);
-          const int b = which ? Meta<D>::v_bias(in_tile, g) : Meta<D>::k_bias(in_tile, g);
-          pc.s[c] = ok ? meta[s] : (uint16_t)0;
-          pc.b[c] = ok ? meta[b] : (uint16_t)0;
+      auto load = [&](int c, const uint8_t* tile) {  // zeros for a key that is not there
+        code[c] = make_uint4(0, 0, 0, 0);
+        meta[c] = 0;
+        if (tile) {
+          code[c] = *reinterpret_cast<const uint4*>(tile + in_tile * (D / 2) +
+                                                    (((2 * c + half) ^ sw) << 4));
+          const uint16_t* x = reinterpret_cast<const uint16_t*>(tile + 16 * D);
+          meta[c] = x[Meta<D>::k_scale(in_tile, c)] |
+                    (uint32_t)x[Meta<D>::k_bias(in_tile, c)] << 16;
         }
       };
-      auto store = [&](const Piece& pc, uint32_t at) {
+      const uint8_t *tile = tile_at(u.blk0), *ahead = tile_at(u.blk0 + 1);
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          const int chunk = half * kChunks + c, g = D == 256 ? c / 2 : 0;
-          const uint32_t s = pc.s[g] * 0x10001u, b = pc.b[g] * 0x10001u;
-          const uint32_t w[4] = {pc.code[c].x, pc.code[c].y, pc.code[c].z, pc.code[c].w};
+      for (int c = 0; c < KC; ++c) load(c, tile);
+      for (int i = u.blk0; i < u.blk1; ++i) {
+        tile = ahead;
+        ahead = tile_at(i + 2);
+        if (n >= S) wait_all(&s_full[NT - 1][(n - S) & 1u], (n - S) >> 1, s_stop);
+        const uint32_t to = k_at + n % S * C::kBlockBytes + key * 128;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = dequant8(w[i], s, b);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             at + (chunk >> 1) * (kKeys * 128) + key * 128 +
-                             ((((chunk & 1) * 4 + i) ^ (key & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
+        for (int c = 0; c < KC; ++c) {
+          const uint32_t w[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
+          const uint32_t sc = __byte_perm(meta[c], 0, 0x1010), bi = __byte_perm(meta[c], 0, 0x3232);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sts128(to + c * (kKeys * 128) + (((half * 4 + k) ^ (key & 7)) << 4),
+                   dequant8(w[k], sc, bi));
+          load(c, tile);
         }
         fence_async();
         __syncwarp();
+        if (lane == 0) sc::bar_arrive(su32(&k_full[n % S]));
+        ++n;
+      }
+    }
+  } else if (wid < kMmaWarp) {
+    // ----------------- values: a thread per key of a chunk of 32 and D / 8 columns
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
+    constexpr int kWords = D / 64;  // of eight codes
+    const int part = wid - kSoftWarps - kSideWarps;
+    const int in_tile = lane & 15, g = part * D / 512;  // the columns' quantisation group
+    const int code_at = 8 * D + in_tile * (D / 2) +
+                        (((part * kWords / 4) ^ swizzle<D>(in_tile)) << 4) + part * kWords % 4 * 4;
+    uint32_t code[VC][kWords], meta[VC];
+    uint32_t n = 0;
+    while (next_unit(walk, a, r, tok, u)) {
+      const int len = walk.row.len;
+      const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
+      auto block_of = [&](int i, int c) {
+        const int j = i * kKeys + c * 32 + lane;
+        return i < u.blk1 && j < len ? table[j >> p_shift] : -1;
       };
-      Piece pk, pv;
-      int block = block_of(u.blk0), ahead = block_of(u.blk0 + 1);
-      load(pk, u.blk0, block, 0);
+      auto load = [&](int i, int block, int c) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) code[c][k] = 0;
+        meta[c] = 0;
+        if ((unsigned)block < (unsigned)a.kv.num_blocks) {
+          const int j = i * kKeys + c * 32 + lane;
+          const uint8_t* tile =
+              static_cast<const uint8_t*>(a.kv.pool) +
+              (((int64_t)block * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
+          if constexpr (kWords == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + code_at);
+            code[c][0] = v.x;
+            code[c][1] = v.y;
+            code[c][2] = v.z;
+            code[c][3] = v.w;
+          } else if constexpr (kWords == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(tile + code_at);
+            code[c][0] = v.x;
+            code[c][1] = v.y;
+          } else {
+            code[c][0] = *reinterpret_cast<const uint32_t*>(tile + code_at);
+          }
+          const uint16_t* x = reinterpret_cast<const uint16_t*>(tile + 16 * D);
+          meta[c] = x[Meta<D>::v_scale(in_tile, g)] |
+                    (uint32_t)x[Meta<D>::v_bias(in_tile, g)] << 16;
+        }
+      };
+      int block[VC];
+#pragma unroll
+      for (int c = 0; c < VC; ++c) {
+        load(u.blk0, block_of(u.blk0, c), c);
+        block[c] = block_of(u.blk0 + 1, c);
+      }
       for (int i = u.blk0; i < u.blk1; ++i) {
-        load(pv, i, block, 1);
-        int st = n_k % S;
-        if (n_k >= S) wait_all(&k_empty[st], n_k / S - 1, s_stop);
-        store(pk, k_at + st * C::kBlockBytes);
-        if (lane == 0) sc::bar_arrive(su32(&k_full[st]));
-        ++n_k;
-        block = ahead;
-        ahead = block_of(i + 2);
-        load(pk, i + 1, block, 0);
-        st = n_v % S;
-        if (n_v >= S) wait_all(&v_empty[st], n_v / S - 1, s_stop);
-        store(pv, v_at + st * C::kBlockBytes);
-        if (lane == 0) sc::bar_arrive(su32(&v_full[st]));
-        ++n_v;
+        if (n >= S) wait_all(&o_done[NT - 1][(n - S) & 1u], (n - S) >> 1, s_stop);
+#pragma unroll
+        for (int c = 0; c < VC; ++c) {
+          const int key = c * 32 + lane;
+          const uint32_t to = v_at + n % S * C::kBlockBytes + key * 128;
+          const uint32_t sc = __byte_perm(meta[c], 0, 0x1010), bi = __byte_perm(meta[c], 0, 0x3232);
+#pragma unroll
+          for (int k = 0; k < kWords; ++k) {
+            const int col8 = part * kWords + k;  // eight columns
+            sts128(to + (col8 >> 3) * (kKeys * 128) + (((col8 & 7) ^ (key & 7)) << 4),
+                   dequant8(code[c][k], sc, bi));
+          }
+          load(i + 1, block[c], c);
+          block[c] = block_of(i + 2, c);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) sc::bar_arrive(su32(&v_full[n % S]));
+        ++n;
       }
     }
   } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    if (wid == kMmaWarp) {
     // -------------------------------------------------------------------- MMAs
-    uint32_t n_u = 0, n_k = 0, n_v = 0, n_s = 0, n_p = 0;
-    auto scores = [&](int tile, uint32_t st, int slot) {
-      if (lane == 0) {
+    uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
+    // descriptors: a byte offset moves them by a sixteenth
+    const uint64_t dq = smem_desc(q_at, 16), dk = smem_desc(k_at, 16);
+    const uint64_t dv = smem_desc(v_at, kKeys * 128);
+    // A tile's scores of block n_k go where the weights of the block before (two blocks before,
+    // with one tile) were: their product has to be over, as MMAs of other accumulators are not
+    // ordered by themselves.
+    auto scores = [&](int tile) {
+      const int slot = NT == 1 ? (int)(n_k & 1u) : tile, st = n_k % S;
+      if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
+      if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
+      tc_after();
+      const uint64_t da = dq + tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-          mma_ss(tmem + C::kS + slot * 128, smem_desc(q_at + tile * C::kBlockBytes + off, 16),
-                 smem_desc(k_at + st * C::kBlockBytes + off, 16), C::kIdescS, k > 0);
+          const int off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16;
+          mma_ss(tmem + C::kS + slot * 128, da + off, db + off, C::kIdescS, k > 0);
         }
-        commit(su32(&s_full[slot]));
+        commit(su32(&s_full[tile][n_k & 1u]));
       }
-    };
-    auto product = [&](int tile, uint32_t st, int slot, bool more) {
-      if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8,
-                 smem_desc(v_at + st * C::kBlockBytes + k * 2048, kKeys * 128), C::kIdescO,
-                 more || k > 0);
-        commit(su32(&o_done[tile]));
-      }
-    };
-    auto freed = [&](uint64_t* bar) {
-      if (lane == 0) commit(su32(bar));
       __syncwarp();
     };
+    auto product = [&](int tile, uint32_t n, bool more) {
+      const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n % S;
+      wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
+      if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
+      tc_after();
+      const uint64_t db = dv + st * (C::kBlockBytes / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8, db + k * (2048 / 16),
+                 C::kIdescO, more || k > 0);
+        commit(su32(&o_done[tile][n & 1u]));
+      }
+      __syncwarp();
+    };
+    auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
     while (next_unit(walk, a, r, tok, u)) {
       wait_all(&q_full, n_u++, s_stop);
       const int nb = u.blk1 - u.blk0;
       if constexpr (NT == 1) {
-        for (int i = 0; i <= nb; ++i) {
+        for (int i = 0; i <= nb && !stopped(); ++i) {
           if (i < nb) {
-            const uint32_t st = n_k % S;
-            wait_all(&k_full[st], n_k / S, s_stop);
-            if (__any_sync(~0u, s_stop)) break;
-            tc_after();
-            scores(0, st, n_s & 1u);
-            freed(&k_empty[st]);
+            scores(0);
             ++n_k;
-            ++n_s;
           }
-          if (i > 0) {
-            const uint32_t st = n_v % S, slot = n_p & 1u;
-            wait_all(&v_full[st], n_v / S, s_stop);
-            wait_all(&p_full[slot], n_p >> 1, s_stop);
-            if (__any_sync(~0u, s_stop)) break;
-            tc_after();
-            product(0, st, slot, i > 1);
-            freed(&v_empty[st]);
-            ++n_v;
-            ++n_p;
-          }
+          if (i > 0) product(0, n_p++, i > 1);
         }
       } else {
-        wait_all(&k_full[n_k % S], n_k / S, s_stop);
-        if (__any_sync(~0u, s_stop)) break;
-        tc_after();
-        scores(0, n_k % S, 0);
-        scores(1, n_k % S, 1);
-        freed(&k_empty[n_k % S]);
+        scores(0);
+        scores(1);
         ++n_k;
-        for (int i = 0; i < nb; ++i) {
-          const bool on = i + 1 < nb;
-          const uint32_t sv = n_v % S, sk = n_k % S;
-          wait_all(&v_full[sv], n_v / S, s_stop);
-          wait_all(&p_full[0], n_p, s_stop);
-          if (__any_sync(~0u, s_stop)) break;
-          tc_after();
-          product(0, sv, 0, i > 0);
-          if (on) {
-            wait_all(&k_full[sk], n_k / S, s_stop);
-            if (__any_sync(~0u, s_stop)) break;
-            tc_after();
-            scores(0, sk, 0);
-          }
-          wait_all(&p_full[1], n_p, s_stop);
-          if (__any_sync(~0u, s_stop)) break;
-          tc_after();
-          product(1, sv, 1, i > 0);
-          freed(&v_empty[sv]);
-          if (on) {
-            scores(1, sk, 1);
-            freed(&k_empty[sk]);
+        for (int i = 0; i < nb && !stopped(); ++i) {
+          product(0, n_p, i > 0);
+          ++n_p;
+          if (i + 1 < nb) scores(0);
+          product(1, n_p - 1, i > 0);
+          if (i + 1 < nb) {
+            scores(1);
             ++n_k;
           }
-          ++n_v;
-          ++n_p;
         }
       }
-      if (__any_sync(~0u, s_stop)) break;
+      if (stopped()) break;
     }
-    if (lane == 0) commit(su32(&drained));  // nothing is under way when TMEM goes back
+    if (elect_one()) commit(su32(&drained));  // nothing is under way when TMEM goes back
     __syncwarp();
     if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
+    }
   }
   tc_before();
   __syncthreads();
