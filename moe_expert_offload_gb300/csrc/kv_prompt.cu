@@ -22,8 +22,7 @@
 //   warp 24     issues the MMAs (M = 128, fp32 accumulators in TMEM): the next
 //               block's scores run while the softmax works on this one's.
 // Registers move from the dequantising warps and the MMA warp's group to the
-// softmax (the block starts with 72 a thread, and 112 / 56 / 48 of them add up to
-// less than that).
+// softmax (the CTA starts with 72 a thread; what they add up to is checked below).
 // The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
 // order in which one LOP3 yields pairs): the queries are laid out alike, and the
 // result is put in order when it is stored.
@@ -47,9 +46,7 @@ using sc::su32;
 constexpr int kKeys = 128;  // keys of a block
 constexpr int kSoftWarps = 8, kSideWarps = 8, kMmaWarp = 24;
 constexpr int kThreads = 28 * 32;  // seven warp groups; three warps of the last one idle
-constexpr int kSoftRegs = 112, kSideRegs = 56, kMmaRegs = 48, kStartRegs = 72;
-static_assert(kSoftRegs * 256 + kSideRegs * 512 + kMmaRegs * 128 <= kStartRegs * kThreads,
-              "the registers given out are there");
+constexpr int kStartRegs = 72;
 constexpr int kUnitKeys = 384;  // a unit's fixed cost, in keys
 constexpr float kNone = -1e30f;
 
@@ -66,6 +63,10 @@ struct Cfg {
                                       ((128u >> 4) << 24);  // bit 16: B is MN-major
   static constexpr int kO = D == 256 ? 256 : 128;   // TMEM columns between the tiles' results
   static constexpr int kS = 256;                    // scores: two slots of 128 columns
+  static constexpr int kSoftRegs = D == 256 ? 112 : 128, kSideRegs = D == 256 ? 56 : 48;
+  static constexpr int kMmaRegs = D == 256 ? 48 : 40;
+  static_assert(kSoftRegs * 256 + kSideRegs * 512 + kMmaRegs * 128 <= kStartRegs * kThreads,
+                "the registers given out are there");
 };
 
 // The unit that a CTA began and did not end: the last CTA with a part of it (-1: there is none).
@@ -201,11 +202,33 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, uint32_t* r) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
-  // the registers pass through, so that nothing reads them before the wait
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+// The loads issued so far are over; their registers pass through, so that nothing reads them
+// before.
+template <int N>
+__device__ __forceinline__ void tm_wait_regs(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// whether any thread of the softmax warps says so
+__device__ __forceinline__ bool any_of_256(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -236,6 +259,23 @@ __device__ __forceinline__ uint32_t hadd2(uint32_t x, uint32_t y) {
 __device__ __forceinline__ uint32_t hfma2(uint32_t x, uint32_t y, uint32_t z) {
   uint32_t r;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+// {x, y} * f + g, and a + b, two at a time
+__device__ __forceinline__ float2 fma2(float x, float y, float f, float g) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+      " mov.b64 c, {%5, %5};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x), "f"(y), "f"(f), "f"(g));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
@@ -295,7 +335,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   using C = Cfg<D>;
   constexpr int NT = C::kTiles, S = C::kStages;
   extern __shared__ unsigned char smem_raw[];
-  constexpr int KC = D / 64, VC = 4;  // chunks of a block: 64 columns of keys, 32 values
   // A block of keys or values is there; a tile's scores, weights, product are.  The last two by
   // the block's parity: a buffer's next block waits for the scores (products) of the block that
   // it replaces, which are never more than one phase of that barrier ago.
@@ -305,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   __shared__ long long s_scan[kThreads / 32], s_at, s_share;
   __shared__ int s_row;
   __shared__ volatile int s_stop;
-  __shared__ float s_fac[C::kRows], s_max[2][2][128], s_sum[2][128];
+  __shared__ float s_fac[C::kRows], s_max[2][128], s_sum[2][128];
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int K = a.kv.kv_heads, r = a.heads / K, P = a.kv.block_tokens;
   const int p_shift = 31 - __clz(P);
@@ -410,16 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
 
   if (wid < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int wg = wid >> 2, row = (wid & 3) * 32 + lane;  // TMEM lane
     const int tile = NT == 1 ? 0 : wg;
     const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lanes + tile * C::kO;
     uint32_t n = 0;  // blocks seen
-    while (next_unit(walk, a, r, tok, u)) {
-      const Row ri = walk.row;
-      const int b = walk.b;
-      // ---- queries: a warp's rows, 8 columns a lane, a few loads under way at a time
+    // A unit's queries: a warp's rows, 8 columns a lane, a few loads under way at a time.  The
+    // buffer is free once the last block's scores of the unit before are there.
+    auto load_queries = [&](const Row& w_row, const Unit& u) {
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = C::kRows / kSoftWarps / kAtOnce;
 #pragma unroll 1
       for (int i0 = 0; i0 < kRounds; i0 += 8) {
@@ -429,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           const int qr = (wid * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
           const int i_tok = (int)(in * r_inv >> 16), t = u.tok0 + (qr >> 7) * per_tile + i_tok;
           raw[i] = make_uint4(0, 0, 0, 0);
-          if (in < per_tile * r && t < ri.n)
+          if (in < per_tile * r && t < w_row.n)
             raw[i] = *reinterpret_cast<const uint4*>(
-                a.q + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
+                a.q + ((int64_t)(w_row.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
                 lane % kLanes * 8);
         }
 #pragma unroll
@@ -464,6 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       fence_async();
       __syncwarp();
       if (lane == 0) sc::bar_arrive(su32(&q_full));
+    };
+    bool have = next_unit(walk, a, r, tok, u);
+    if (have) load_queries(walk.row, u);
+    while (have) {
+      const Row ri = walk.row;
+      const int b = walk.b;
       asm volatile("bar.sync 1, 256;" ::: "memory");  // s_fac of all rows
       const float fac = s_fac[tile * 128 + row];
       const int row_tok = (int)(row * r_inv >> 16), row_h = row - row_tok * r;
@@ -488,92 +532,115 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         const uint32_t s_tm = tmem + lanes + C::kS + slot * 128;
         const int key0 = i * kKeys;
         const bool edge = key0 + kKeys > open + 1 || miss != 0;
-        constexpr int kChunks = NT == 1 ? 2 : 4;  // of 32 columns
-        const int c_first = NT == 1 ? wg * 2 : 0;
-        auto hide = [&](uint32_t (&v)[32], int c) {
+        // 16 columns (a key tile) from column c * 16 on: what the row does not see
+        auto hide = [&](uint32_t* v, int c) {
           if (edge) {
+            const int last = (miss >> c) & 1u ? -1 : lim - key0 - c * 16;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (key0 + c * 32 + k > lim || ((miss >> (c * 2 + k / 16)) & 1u)) v[k] = 0xFF800000u;
+            for (int k = 0; k < 16; ++k)
+              if (k > last) v[k] = 0xFF800000u;
           }
         };
-        // the row's maximum; accumulators follow when it passes the reference by 2^8
-        auto refer = [&](float top) {
-          float f = 1.0f;
-          if (top > m + 8.0f) {
-            f = ex2(m - top);
-            m = top;
+        // The weights relative to the maximum so far, 2^7 above it.  While a part's sum is below
+        // 2^16 each of them fits fp16; where it is not, some score passes the maximum by 2^4 or
+        // more: the maximum follows, what there is is scaled and the weights are formed again.
+        float2 sum;
+        auto weights = [&](const uint32_t* v, uint32_t* p) {
+          const float off = 7.0f - m;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float2 x = fma2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), fac, off);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            sum = add2(sum, x);
+            p[k] = pack_h2(x.x, x.y);
           }
+        };
+        constexpr float kMost = 65504.0f;
+        auto refer = [&](float top) {
+          const float f = ex2(m - fmaxf(m, top));
+          m = fmaxf(m, top);
           l *= f;
           if (i > u.blk0 && __any_sync(~0u, f != 1.0f)) {
             wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
             tc_after();
             constexpr int kCols = NT == 1 ? D / 2 : D;
 #pragma unroll 1
-            for (int c = 0; c < kCols; c += 32) {
-              uint32_t v[32];
+            for (int c = 0; c < kCols; c += 16) {
+              uint32_t v[16];
               const uint32_t at = o_tm + (NT == 1 ? wg * (D / 2) : 0) + c;
-              tm_ld32(at, v);
-              tm_wait_ld(v);
+              tm_ld16(at, v);
+              tm_wait_regs(v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f);
               tm_st16(at, v);
-              tm_st16(at + 16, v + 16);
             }
             tm_wait_st();
           }
         };
-        auto weights = [&](uint32_t (&v)[32], int c) {
-          uint32_t p[16];
-          const float off = 7.0f - m;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float x = ex2(fmaf(__uint_as_float(v[2 * k]), fac, off));
-            const float y = ex2(fmaf(__uint_as_float(v[2 * k + 1]), fac, off));
-            l += x + y;
-            p[k] = pack_h2(x, y);
-          }
-          tm_st16(s_tm + c * 16, p);
-        };
         if constexpr (NT == 1) {
-          uint32_t v0[32], v1[32];
-          tm_ld32(s_tm + c_first * 32, v0);
-          tm_ld32(s_tm + c_first * 32 + 32, v1);
-          tm_wait_ld(v0);
-          tm_wait_ld(v1);
-          hide(v0, c_first);
-          hide(v1, c_first + 1);
-          float top = kNone;
+          uint32_t p[32];
+          auto attempt = [&](bool follow) {
+            uint32_t v[64];
+            tm_ld32(s_tm + wg * 64, v);
+            tm_ld32(s_tm + wg * 64 + 32, v + 32);
+            tm_wait_regs(v);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            top = fmaxf(top, fmaxf(__uint_as_float(v0[k]), __uint_as_float(v1[k])));
-          // both halves of the row, and (every score being in registers by then) the weights
-          // may go over the scores
-          s_max[n & 1u][wg][row] = top;
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-          top = fmaxf(top, s_max[n & 1u][wg ^ 1][row]);
-          refer(top * fac);
-          weights(v0, c_first);
-          weights(v1, c_first + 1);
+            for (int c = 0; c < 4; ++c) hide(v + 16 * c, wg * 4 + c);
+            if (follow) {
+              float top = kNone;
+#pragma unroll
+              for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(v[k]));
+              s_max[wg][row] = top;
+              asm volatile("bar.sync 1, 256;" ::: "memory");
+              refer(fmaxf(top, s_max[wg ^ 1][row]) * fac);
+            }
+            sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) weights(v + 16 * c, p + 8 * c);
+          };
+          attempt(i == u.blk0);
+          // both halves of the rows agree (and every score has been read by then: the weights
+          // may go over the scores)
+          while (any_of_256(sum.x + sum.y > kMost)) attempt(true);
+          l += sum.x + sum.y;
+          tm_st16(s_tm + wg * 32, p);
+          tm_st16(s_tm + wg * 32 + 16, p + 16);
         } else {
-          float top = kNone;
-#pragma unroll 1
-          for (int c = 0; c < kChunks; ++c) {
-            uint32_t v[32];
-            tm_ld32(s_tm + c * 32, v);
-            tm_wait_ld(v);
-            hide(v, c);
+#pragma unroll 2
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], p[16];
+            tm_ld32(s_tm + c * 32, x);
+            tm_wait_regs(x);
+            hide(x, 2 * c);
+            hide(x + 16, 2 * c + 1);
+            sum = make_float2(0.0f, 0.0f);
+            weights(x, p);
+            weights(x + 16, p + 8);
+            if (__any_sync(~0u, sum.x + sum.y > kMost)) {
+              // (the block's earlier weights are in TMEM by now, and scaled there)
+              const float before = m;
+              float top = kNone;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(v[k]));
-          }
-          refer(top * fac);
-#pragma unroll 1
-          for (int c = 0; c < kChunks; ++c) {
-            uint32_t v[32];
-            tm_ld32(s_tm + c * 32, v);
-            tm_wait_ld(v);
-            hide(v, c);
-            weights(v, c);
+              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+              refer(top * fac);
+              const float f = ex2(before - m);
+              const uint32_t ff = pack_h2(f, f);
+              for (int k = 0; k < c; ++k) {
+                uint32_t old[16];
+                tm_wait_st();
+                tm_ld16(s_tm + k * 16, old);
+                tm_wait_regs(old);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) old[q] = hfma2(old[q], ff, 0u);
+                tm_st16(s_tm + k * 16, old);
+              }
+              sum = make_float2(0.0f, 0.0f);
+              weights(x, p);
+              weights(x + 16, p + 8);
+            }
+            l += sum.x + sum.y;
+            tm_st16(s_tm + c * 16, p);
           }
         }
         tm_wait_st();
@@ -582,6 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         if (lane == 0) sc::bar_arrive(su32(&p_full[tile][n & 1u]));
         ++n;
       }
+      // the next unit's queries come while the last product runs
+      const Unit done = u;
+      have = next_unit(walk, a, r, tok, u);
+      if (have) load_queries(walk.row, u);
       // ---- the unit's end (here): a result, or a part of one
       wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
       tc_after();
@@ -590,10 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         asm volatile("bar.sync 1, 256;" ::: "memory");
         l += s_sum[wg ^ 1][row];
       }
-      const bool whole = u.blk0 == 0 && u.blk1 == u.blocks;
+      const bool whole = done.blk0 == 0 && done.blk1 == done.blocks;
       const float inv = l > 0.0f ? 1.0f / l : l;
-      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + u.kvh * r + row_h) * D;
-      float* part = parts + ((size_t)blockIdx.x * 2 + (u.blk0 == 0 ? 1 : 0)) * C::kPartial;
+      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + done.kvh * r + row_h) * D;
+      float* part = parts + ((size_t)blockIdx.x * 2 + (done.blk0 == 0 ? 1 : 0)) * C::kPartial;
       const int pr = tile * 128 + row;
       constexpr int kCols = NT == 1 ? D / 2 : D;
       const int c_at = NT == 1 ? wg * (D / 2) : 0;
@@ -601,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       for (int c = 0; c < kCols; c += 32) {
         uint32_t v[32];
         tm_ld32(o_tm + c_at + c, v);
-        tm_wait_ld(v);
+        tm_wait_regs(v);
         if (live) {
 #pragma unroll
         for (int k = 0; k < 32; k += 8) {
@@ -631,140 +702,88 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         part[(size_t)C::kRows * D + pr] = m;
         part[(size_t)C::kRows * (D + 1) + pr] = l;
       }
-      if (u.blk0 == 0 && !whole && tid == 0)  // begun here; it goes on at the next share's start
-        cuts[blockIdx.x] = Cut{(int)(blockIdx.x + (u.rest + s_share - 1) / s_share), ri.start, ri.n,
-                               u.tok0, u.kvh, {}};
+      if (done.blk0 == 0 && !whole && tid == 0)  // begun here; it goes on at the next share's start
+        cuts[blockIdx.x] = Cut{(int)(blockIdx.x + (done.rest + s_share - 1) / s_share), ri.start, ri.n,
+                               done.tok0, done.kvh, {}};
       tc_before();
       __syncwarp();
     }
-  } else if (wid < kSoftWarps + kSideWarps) {
-    // ------------- keys: a thread per key and half of a chunk's 64 columns
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
-    const int key = (tid - kSoftWarps * 32) & 127, half = (tid - kSoftWarps * 32) >> 7;
-    const int in_tile = key & 15, sw = swizzle<D>(in_tile);
-    uint4 code[KC];
-    uint32_t meta[KC];  // scale | bias << 16
-    uint32_t n = 0;     // blocks written
-    while (next_unit(walk, a, r, tok, u)) {
-      const int len = walk.row.len;
-      const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
-      auto tile_at = [&](int i) -> const uint8_t* {  // the key's tile; null: it is not there
-        const int j = i * kKeys + key;
-        if (i >= u.blk1 || j >= len) return nullptr;
-        const int block = table[j >> p_shift];
-        if ((unsigned)block >= (unsigned)a.kv.num_blocks) return nullptr;
-        return static_cast<const uint8_t*>(a.kv.pool) +
-               (((int64_t)block * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
-      };
-      auto load = [&](int c, const uint8_t* tile) {  // zeros for a key that is not there
-        code[c] = make_uint4(0, 0, 0, 0);
-        meta[c] = 0;
-        if (tile) {
-          code[c] = *reinterpret_cast<const uint4*>(tile + in_tile * (D / 2) +
-                                                    (((2 * c + half) ^ sw) << 4));
-          const uint16_t* x = reinterpret_cast<const uint16_t*>(tile + 16 * D);
-          meta[c] = x[Meta<D>::k_scale(in_tile, c)] |
-                    (uint32_t)x[Meta<D>::k_bias(in_tile, c)] << 16;
-        }
-      };
-      const uint8_t *tile = tile_at(u.blk0), *ahead = tile_at(u.blk0 + 1);
-#pragma unroll
-      for (int c = 0; c < KC; ++c) load(c, tile);
-      for (int i = u.blk0; i < u.blk1; ++i) {
-        tile = ahead;
-        ahead = tile_at(i + 2);
-        if (n >= S) wait_all(&s_full[NT - 1][(n - S) & 1u], (n - S) >> 1, s_stop);
-        const uint32_t to = k_at + n % S * C::kBlockBytes + key * 128;
-#pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const uint32_t w[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
-          const uint32_t sc = __byte_perm(meta[c], 0, 0x1010), bi = __byte_perm(meta[c], 0, 0x3232);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            sts128(to + c * (kKeys * 128) + (((half * 4 + k) ^ (key & 7)) << 4),
-                   dequant8(w[k], sc, bi));
-          load(c, tile);
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) sc::bar_arrive(su32(&k_full[n % S]));
-        ++n;
-      }
-    }
   } else if (wid < kMmaWarp) {
-    // ----------------- values: a thread per key of a chunk of 32 and D / 8 columns
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSideRegs));
-    constexpr int kWords = D / 64;  // of eight codes
-    const int part = wid - kSoftWarps - kSideWarps;
-    const int in_tile = lane & 15, g = part * D / 512;  // the columns' quantisation group
-    const int code_at = 8 * D + in_tile * (D / 2) +
-                        (((part * kWords / 4) ^ swizzle<D>(in_tile)) << 4) + part * kWords % 4 * 4;
-    uint32_t code[VC][kWords], meta[VC];
-    uint32_t n = 0;
-    while (next_unit(walk, a, r, tok, u)) {
-      const int len = walk.row.len;
-      const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
-      auto block_of = [&](int i, int c) {
-        const int j = i * kKeys + c * 32 + lane;
-        return i < u.blk1 && j < len ? table[j >> p_shift] : -1;
-      };
-      auto load = [&](int i, int block, int c) {
+    // ------------- keys (warps 8-15) and values (16-23): a thread per key and half of the columns
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kSideRegs));
+    auto side = [&](auto value_tag, uint32_t room, uint64_t* full, uint64_t* freed) {
+      constexpr bool kValues = decltype(value_tag)::value;
+      constexpr int KC = D / 64, KG = D == 256 ? 2 : 1;  // 16-byte chunks, quantisation groups
+      const int st = (tid - kSoftWarps * 32) & 255, key = st & 127, half = st >> 7;
+      const int in_tile = key & 15, sw = swizzle<D>(in_tile), g0 = half * KC / 2;
+      const int codes = (kValues ? 8 * D : 0) + in_tile * (D / 2);
+      const int scales =
+          16 * D + 2 * (kValues ? Meta<D>::v_scale(in_tile, g0) : Meta<D>::k_scale(in_tile, g0));
+      constexpr int kBias = 32 * (D / 64), kGroup = kValues ? 32 : 2;  // bytes from a scale on
+      uint4 code[KC];
+      uint32_t meta[KG];  // scale | bias << 16
+      uint32_t n = 0;     // blocks written
+      while (next_unit(walk, a, r, tok, u)) {
+        const int len = walk.row.len;
+        const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
+        const uint8_t* pool = static_cast<const uint8_t*>(a.kv.pool) +
+                              (int64_t)u.kvh * (P / kTile) * tile_bytes(D);
+        const int64_t stride = (int64_t)K * (P / kTile) * tile_bytes(D);
+        auto tile_at = [&](int i) -> const uint8_t* {  // the key's tile; null: it is not there
+          const int j = i * kKeys + key;
+          if (i >= u.blk1 || j >= len) return nullptr;
+          const int block = table[j >> p_shift];
+          if ((unsigned)block >= (unsigned)a.kv.num_blocks) return nullptr;
+          return pool + block * stride + (j & (P - 1)) / kTile * tile_bytes(D);
+        };
+        auto load = [&](const uint8_t* tile) {  // zeros for a key that is not there
 #pragma unroll
-        for (int k = 0; k < kWords; ++k) code[c][k] = 0;
-        meta[c] = 0;
-        if ((unsigned)block < (unsigned)a.kv.num_blocks) {
-          const int j = i * kKeys + c * 32 + lane;
-          const uint8_t* tile =
-              static_cast<const uint8_t*>(a.kv.pool) +
-              (((int64_t)block * K + u.kvh) * (P / kTile) + (j & (P - 1)) / kTile) * tile_bytes(D);
-          if constexpr (kWords == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(tile + code_at);
-            code[c][0] = v.x;
-            code[c][1] = v.y;
-            code[c][2] = v.z;
-            code[c][3] = v.w;
-          } else if constexpr (kWords == 2) {
-            const uint2 v = *reinterpret_cast<const uint2*>(tile + code_at);
-            code[c][0] = v.x;
-            code[c][1] = v.y;
-          } else {
-            code[c][0] = *reinterpret_cast<const uint32_t*>(tile + code_at);
+          for (int c = 0; c < KC; ++c) code[c] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < KG; ++c) meta[c] = 0;
+          if (tile) {
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+              code[c] = *reinterpret_cast<const uint4*>(tile + codes + (((half * KC + c) ^ sw) << 4));
+#pragma unroll
+            for (int c = 0; c < KG; ++c) {
+              const uint16_t* x = reinterpret_cast<const uint16_t*>(tile + scales + c * kGroup);
+              meta[c] = x[0] | (uint32_t)x[kBias / 2] << 16;
+            }
           }
-          const uint16_t* x = reinterpret_cast<const uint16_t*>(tile + 16 * D);
-          meta[c] = x[Meta<D>::v_scale(in_tile, g)] |
-                    (uint32_t)x[Meta<D>::v_bias(in_tile, g)] << 16;
-        }
-      };
-      int block[VC];
+        };
+        load(tile_at(u.blk0));
+        const uint8_t* next = tile_at(u.blk0 + 1);
+        for (int i = u.blk0; i < u.blk1; ++i) {
+          if (n >= S) wait_all(&freed[(n - S) & 1u], (n - S) >> 1, s_stop);
+          const uint32_t to = room + n % S * C::kBlockBytes + key * 128;
 #pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        load(u.blk0, block_of(u.blk0, c), c);
-        block[c] = block_of(u.blk0 + 1, c);
-      }
-      for (int i = u.blk0; i < u.blk1; ++i) {
-        if (n >= S) wait_all(&o_done[NT - 1][(n - S) & 1u], (n - S) >> 1, s_stop);
+          for (int c = 0; c < KC; ++c) {
+            const int chunk = half * KC + c, g = D == 256 ? c / 2 : 0;
+            const uint32_t w[4] = {code[c].x, code[c].y, code[c].z, code[c].w};
+            const uint32_t sc = __byte_perm(meta[g], 0, 0x1010);
+            const uint32_t bi = __byte_perm(meta[g], 0, 0x3232);
+            const uint32_t at = to + (chunk >> 1) * (kKeys * 128);
 #pragma unroll
-        for (int c = 0; c < VC; ++c) {
-          const int key = c * 32 + lane;
-          const uint32_t to = v_at + n % S * C::kBlockBytes + key * 128;
-          const uint32_t sc = __byte_perm(meta[c], 0, 0x1010), bi = __byte_perm(meta[c], 0, 0x3232);
-#pragma unroll
-          for (int k = 0; k < kWords; ++k) {
-            const int col8 = part * kWords + k;  // eight columns
-            sts128(to + (col8 >> 3) * (kKeys * 128) + (((col8 & 7) ^ (key & 7)) << 4),
-                   dequant8(code[c][k], sc, bi));
+            for (int k = 0; k < 4; ++k)
+              sts128(at + ((((chunk & 1) * 4 + k) ^ (key & 7)) << 4), dequant8(w[k], sc, bi));
           }
-          load(i + 1, block[c], c);
-          block[c] = block_of(i + 2, c);
+          load(next);
+          next = tile_at(i + 2);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) sc::bar_arrive(su32(&full[n % S]));
+          ++n;
         }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) sc::bar_arrive(su32(&v_full[n % S]));
-        ++n;
       }
-    }
+    };
+    // a buffer is free when the scores (the product) of its block are over
+    if (wid < kSoftWarps + kSideWarps)
+      side(std::false_type{}, k_at, k_full, s_full[NT - 1]);
+    else
+      side(std::true_type{}, v_at, v_full, o_done[NT - 1]);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
     if (wid == kMmaWarp) {
     // -------------------------------------------------------------------- MMAs
     uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
