@@ -9,9 +9,11 @@
 //
 // A row of D columns is held by D / 8 lanes, 8 columns each (one 16-byte
 // load); 8 lanes are one quantisation group, whose minimum and maximum take
-// three shuffles, and a lane's eight codes are one 32-bit word.  One CTA per
-// token: a lane keeps its norm weights, cosines and sines over the heads.
-// Bound by memory.
+// three shuffles, and a lane's eight codes are one 32-bit word.  One warp per
+// token and part of its heads (few tokens: one part per row, so that a decode
+// step's rows run side by side; many: one part, so that cosines, sines and norm
+// weights are read once per token): it keeps four rows' loads under way.  Bound
+// by memory.
 #include "kv_common.cuh"
 
 namespace moe {
@@ -90,98 +92,161 @@ __device__ __forceinline__ void quantise_store(const float (&x)[8], uint8_t* til
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) store_kernel(StoreArgs a) {
-  constexpr int kLanes = D / 8, kRows = 256 / kLanes;
-  const int t = blockIdx.x, sub = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+__global__ void __launch_bounds__(128) store_kernel(StoreArgs a, int parts) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAtOnce = 4;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
+  const int64_t id = blockIdx.x * 4ll + (threadIdx.x >> 5);
+  const int t = (int)(id / parts), part = (int)(id % parts);
+  griddep_wait();
+  if (t >= a.T) return;
   const int slot = a.slot[t];
   if (slot < 0) return;  // padding
   if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
-    if (threadIdx.x == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
+    if (lane == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
     return;
   }
   const int H = a.proj.q_heads, K = a.kv.kv_heads, rot = a.rope.rotary_dim, half = rot / 2;
+  const int total = H + 2 * K, rounds = (total + kRows - 1) / kRows;
+  const int r0 = (int)((int64_t)rounds * part / parts), r1 = (int)((int64_t)rounds * (part + 1) / parts);
+  auto row = [&](int i) { return i * kRows + mine; };
+  auto load = [&](int h) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (h < total) {
+      const void* base;
+      int64_t at;
+      if (h < H) {
+        base = a.proj.q;
+        at = t * a.proj.q_token_stride + h * a.proj.q_head_stride;
+      } else if (h < H + K) {
+        base = a.proj.k;
+        at = t * a.proj.k_token_stride + (h - H) * a.proj.k_head_stride;
+      } else {
+        base = a.proj.v;
+        at = t * a.proj.v_token_stride + (h - H - K) * a.proj.v_head_stride;
+      }
+      u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + sub * 8));
+    }
+    return u;
+  };
+  uint4 raw[kAtOnce];
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) raw[i] = load(r0 + i < r1 ? row(r0 + i) : total);
   // this lane's cosines and (signed) sines; the partner of column c is c + half
   // (halves) or c ^ 1 (adjacent)
   float cs[8], sn[8];
   const bool turns = sub * 8 < rot;
   bool bad = false;
-  if (rot) {
+  if (turns) {
+    const int first = a.rope.adjacent ? sub * 4 : sub * 8 < half ? sub * 8 : sub * 8 - half;
+    if (a.rope.axes == 1 && half % 4 == 0) {
+      // one position: the pairs lie side by side in the table
+      const int p = a.positions[t];
+      bad = p < 0 || p >= a.rope.max_pos;
+      if (!bad) {
+        const float* e = a.rope.table + (int64_t)p * rot + first;
+        const float4 c0 = *reinterpret_cast<const float4*>(e);
+        const float4 n0 = *reinterpret_cast<const float4*>(e + half);
+        if (a.rope.adjacent) {
+          const float c[4] = {c0.x, c0.y, c0.z, c0.w}, n[4] = {n0.x, n0.y, n0.z, n0.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = sub * 8 + i;
-      cs[i] = 1.0f;
-      sn[i] = 0.0f;
-      if (turns) {
-        const int pair = a.rope.adjacent ? c >> 1 : (c < half ? c : c - half);
+          for (int i = 0; i < 8; ++i) {
+            cs[i] = c[i / 2];
+            sn[i] = i & 1 ? n[i / 2] : -n[i / 2];
+          }
+        } else {
+          const float4 c1 = *reinterpret_cast<const float4*>(e + 4);
+          const float4 n1 = *reinterpret_cast<const float4*>(e + half + 4);
+          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+          const float n[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            cs[i] = c[i];
+            sn[i] = sub * 8 >= half ? n[i] : -n[i];
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int pair = a.rope.adjacent ? first + i / 2 : first + i;
         const int p = a.positions[(int64_t)a.rope.pair_axis[pair] * a.T + t];
+        cs[i] = sn[i] = 0.0f;
         if (p < 0 || p >= a.rope.max_pos) {
           bad = true;
         } else {
-          const float* e = a.rope.table + (int64_t)p * rot;
-          const bool second = a.rope.adjacent ? (c & 1) : c >= half;
-          cs[i] = e[pair];
-          sn[i] = second ? e[pair + half] : -e[pair + half];
+          const float* e = a.rope.table + (int64_t)p * rot + pair;
+          const bool second = a.rope.adjacent ? (i & 1) : sub * 8 >= half;
+          cs[i] = e[0];
+          sn[i] = second ? e[half] : -e[half];
         }
       }
     }
   }
-  if (__syncthreads_or(bad)) {  // a position outside the table: the token is skipped
-    if (threadIdx.x == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
+  if (__any_sync(~0u, bad)) {  // a position outside the table: the token is skipped
+    if (lane == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
     return;
   }
-  const int partner = (threadIdx.x & 31) - sub + (sub * 8 < half ? sub + half / 8 : sub - half / 8);
-  // rows: q heads, k heads, v heads; all lanes run the same number of rounds
-  const int total = H + 2 * K;
-  for (int h0 = 0; h0 < total; h0 += kRows) {
-    const int h = h0 + part;
-    const bool live = h < total;
-    const int which = h < H ? 0 : h < H + K ? 1 : 2;
-    const int hh = which == 0 ? h : which == 1 ? h - H : h - H - K;
-    float x[8] = {};
-    if (live) {
-      const void* base = which == 0 ? a.proj.q : which == 1 ? a.proj.k : a.proj.v;
-      const int64_t ts = which == 0 ? a.proj.q_token_stride
-                                    : which == 1 ? a.proj.k_token_stride : a.proj.v_token_stride;
-      const int64_t hs = which == 0 ? a.proj.q_head_stride
-                                    : which == 1 ? a.proj.k_head_stride : a.proj.v_head_stride;
-      unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + t * ts +
-                                              hh * hs + sub * 8),
-              x);
-    }
-    const float* w = which == 0 ? a.proj.q_norm : which == 1 ? a.proj.k_norm : nullptr;
-    float ss = 0.0f;
+  const int partner = (lane - sub + (sub * 8 < half ? sub + half / 8 : sub - half / 8)) & 31;
+  // norm weights of queries and keys
+  float wq[8], wk[8];
+  auto weights = [&](const float* w, float (&x)[8]) {
+    if (w == nullptr) return;
+    const float4 lo = *reinterpret_cast<const float4*>(w + sub * 8);
+    const float4 hi = *reinterpret_cast<const float4*>(w + sub * 8 + 4);
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
+    x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+  };
+  weights(a.proj.q_norm, wq);
+  weights(a.proj.k_norm, wk);
+  // rows: q heads, k heads, v heads; all lanes of the warp run the same number of rounds
+#pragma unroll 1
+  for (int i0 = r0; i0 < r1; i0 += kAtOnce) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (i0 + i >= r1) break;
+      const int h = row(i0 + i);
+      const bool live = h < total;
+      const int which = h < H ? 0 : h < H + K ? 1 : 2;
+      const int hh = which == 0 ? h : which == 1 ? h - H : h - H - K;
+      float x[8];
+      unpack8(raw[i], x);
+      raw[i] = load(i0 + i + kAtOnce < r1 ? row(i0 + i + kAtOnce) : total);
+      const bool normed = which == 0 ? a.proj.q_norm != nullptr
+                                     : which == 1 && a.proj.k_norm != nullptr;
+      if (__any_sync(~0u, normed)) {
+        float ss = 0.0f;
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
-    if (w) {
-      const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.proj.eps);
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[sub * 8 + i];
-    }
-    if (rot) {
+        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+        if (normed) {
+          const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.proj.eps);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        float u = x[i + 1], v = x[i];
-        if (!a.rope.adjacent) {
-          u = __shfl_sync(~0u, x[i], partner & 31);
-          v = __shfl_sync(~0u, x[i + 1], partner & 31);
-        }
-        if (which < 2 && turns) {
-          x[i] = fmaf(u, sn[i], x[i] * cs[i]);
-          x[i + 1] = fmaf(v, sn[i + 1], x[i + 1] * cs[i + 1]);
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (which == 0 ? wq[j] : wk[j]);
         }
       }
-    }
-    if (which == 0) {
-      if (live)
-        *reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * H + hh) * D + sub * 8) = pack8(x);
-    }
-    const bool store = live && which > 0;
-    if (__any_sync(~0u, store)) {
-      int key;
-      uint8_t* tile = tile_of<D>(a.kv, slot, store ? hh : 0, key);
-      quantise_store<D>(x, tile, key, which == 2, sub, store);
+      if (rot && __any_sync(~0u, which < 2)) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          float u = x[j + 1], v = x[j];
+          if (!a.rope.adjacent) {
+            u = __shfl_sync(~0u, x[j], partner);
+            v = __shfl_sync(~0u, x[j + 1], partner);
+          }
+          if (which < 2 && turns) {
+            x[j] = fmaf(u, sn[j], x[j] * cs[j]);
+            x[j + 1] = fmaf(v, sn[j + 1], x[j + 1] * cs[j + 1]);
+          }
+        }
+      }
+      if (which == 0 && live)
+        __stcs(reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * H + hh) * D + sub * 8), pack8(x));
+      const bool store = live && which > 0;
+      if (__any_sync(~0u, store)) {
+        int key;
+        uint8_t* tile = tile_of<D>(a.kv, slot, store ? hh : 0, key);
+        quantise_store<D>(x, tile, key, which == 2, sub, store);
+      }
     }
   }
 }
@@ -191,6 +256,7 @@ template <int D>
 __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes;
   const int K = a.kv.kv_heads, sub = threadIdx.x % kLanes;
+  griddep_wait();
   const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;  // [T][2][K]
   if (row >= (int64_t)a.T * 2 * K) return;
   const int t = (int)(row / (2 * K)), which = (int)(row / K) & 1, h = (int)(row % K);
@@ -216,15 +282,19 @@ __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
 
 template <int D>
 cudaError_t store_d(const StoreArgs& a, cudaStream_t st) {
-  store_kernel<D><<<a.T, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  // about 32 warps per SM where there are rows for them
+  const int total = a.proj.q_heads + 2 * a.kv.kv_heads, per = 32 / (D / 8);
+  const int rounds = (total + per - 1) / per;
+  const int64_t want = ((int64_t)kGrid * 32 + a.T - 1) / a.T;
+  const int parts = (int)(want < rounds ? want : rounds);
+  const int64_t warps = (int64_t)a.T * parts;
+  return launch_pdl(store_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a, parts);
 }
 
 template <int D>
 cudaError_t load_d(const LoadArgs& a, cudaStream_t st) {
   const int64_t rows = (int64_t)a.T * 2 * a.kv.kv_heads, per = 256 / (D / 8);
-  load_kernel<D><<<(unsigned)((rows + per - 1) / per), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(load_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
 }
 
 }  // namespace
