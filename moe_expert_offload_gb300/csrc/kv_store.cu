@@ -14,6 +14,8 @@
 // step's rows run side by side; many: one part, so that cosines, sines and norm
 // weights are read once per token): it keeps four rows' loads under way.  Bound
 // by memory.
+#include <type_traits>
+
 #include "kv_common.cuh"
 
 namespace moe {
@@ -40,12 +42,23 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(bf2(x[0], x[1]), bf2(x[2], x[3]), bf2(x[4], x[5]), bf2(x[6], x[7]));
 }
 
+// {a, b} * {c, d} + s, two at a time
+__device__ __forceinline__ float2 fma2(float a, float b, float c, float d, float2 s) {
+  float2 r;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mov.b64 z, {%6, %7};\n fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(c), "f"(d), "f"(s.x), "f"(s.y));
+  return r;
+}
+
 // The tile of (block, head, token) and the token's row in it.
 template <int D>
 __device__ __forceinline__ uint8_t* tile_of(const moe_kv& kv, int slot, int head, int& key) {
-  const int P = kv.block_tokens, at = slot % P;
+  const int p_shift = 31 - __clz(kv.block_tokens), at = slot & (kv.block_tokens - 1);
   key = at % kTile;
-  const int64_t tile = ((int64_t)(slot / P) * kv.kv_heads + head) * (P / kTile) + at / kTile;
+  const int64_t tile =
+      (((int64_t)(slot >> p_shift) * kv.kv_heads + head) << (p_shift - 4)) + at / kTile;
   return static_cast<uint8_t*>(kv.pool) + tile * tile_bytes(D);
 }
 
@@ -72,12 +85,25 @@ __device__ __forceinline__ void quantise_store(const float (&x)[8], uint8_t* til
   if (!store) return;
   __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.0f)), bh = __float2half_rn(lo);
   const float s = __half2float(sh), b = __half2float(bh);
+  // (y - bias) / scale by the reciprocal, 4e-6 off at most; where that comes near a border the
+  // quotient itself decides, so that a code is always the definition's
+  const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;
   uint32_t word = 0;
+  bool near = false;
+  float c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float c = s > 0.0f ? rintf(__fdiv_rn(v[i] - b, s)) : 0.0f;
-    word |= (uint32_t)fminf(fmaxf(c, 0.0f), 15.0f) << (4 * i);
+    const float q = (v[i] - b) * inv;
+    c[i] = rintf(q);
+    near |= fabsf(fabsf(q - c[i]) - 0.5f) < 1e-5f;
   }
+  if (near && s > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = rintf(__fdiv_rn(v[i] - b, s));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)  // (the sum's low bits are the code)
+    word |= (__float_as_uint(fminf(fmaxf(c[i], 0.0f), 15.0f) + 8388608.0f) & 15u) << (4 * i);
   // a NaN makes its whole group NaN
   if (nans & (0xFFu << (threadIdx.x & 24))) sh = bh = __ushort_as_half(0x7FFFu);
   const int chunk = (sub >> 2) ^ swizzle<D>(key);
@@ -106,31 +132,27 @@ __global__ void __launch_bounds__(128) store_kernel(StoreArgs a, int parts) {
     return;
   }
   const int H = a.proj.q_heads, K = a.kv.kv_heads, rot = a.rope.rotary_dim, half = rot / 2;
-  const int total = H + 2 * K, rounds = (total + kRows - 1) / kRows;
+  const int rq = (H + kRows - 1) / kRows, rk = (K + kRows - 1) / kRows, rounds = rq + 2 * rk;
   const int r0 = (int)((int64_t)rounds * part / parts), r1 = (int)((int64_t)rounds * (part + 1) / parts);
-  auto row = [&](int i) { return i * kRows + mine; };
-  auto load = [&](int h) {
+  // one region after the other: rounds of kRows query heads, of key heads, of value heads
+  const int64_t lane_at = sub * 8;
+  auto pointer = [&](int which) {
+    const int64_t at = which == 0 ? t * a.proj.q_token_stride
+                                  : which == 1 ? t * a.proj.k_token_stride : t * a.proj.v_token_stride;
+    return static_cast<const uint16_t*>(which == 0 ? a.proj.q : which == 1 ? a.proj.k : a.proj.v) +
+           at + lane_at;
+  };
+  const uint16_t* const base[3] = {pointer(0), pointer(1), pointer(2)};
+  const int64_t stride[3] = {a.proj.q_head_stride, a.proj.k_head_stride, a.proj.v_head_stride};
+  const int heads[3] = {H, K, K};
+  const int begin[4] = {0, rq, rq + rk, rounds};
+  auto load = [&](int which, int round) {
+    const int h = (round - begin[which]) * kRows + mine;
     uint4 u = make_uint4(0, 0, 0, 0);
-    if (h < total) {
-      const void* base;
-      int64_t at;
-      if (h < H) {
-        base = a.proj.q;
-        at = t * a.proj.q_token_stride + h * a.proj.q_head_stride;
-      } else if (h < H + K) {
-        base = a.proj.k;
-        at = t * a.proj.k_token_stride + (h - H) * a.proj.k_head_stride;
-      } else {
-        base = a.proj.v;
-        at = t * a.proj.v_token_stride + (h - H - K) * a.proj.v_head_stride;
-      }
-      u = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + sub * 8));
-    }
+    if (h < heads[which])
+      u = __ldcs(reinterpret_cast<const uint4*>(base[which] + h * stride[which]));
     return u;
   };
-  uint4 raw[kAtOnce];
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) raw[i] = load(r0 + i < r1 ? row(r0 + i) : total);
   // this lane's cosines and (signed) sines; the partner of column c is c + half
   // (halves) or c ^ 1 (adjacent)
   float cs[8], sn[8];
@@ -198,57 +220,64 @@ __global__ void __launch_bounds__(128) store_kernel(StoreArgs a, int parts) {
   };
   weights(a.proj.q_norm, wq);
   weights(a.proj.k_norm, wk);
-  // rows: q heads, k heads, v heads; all lanes of the warp run the same number of rounds
+  auto region = [&](auto which_tag) {
+    constexpr int kWhich = decltype(which_tag)::value;
+    const int from = max(r0, begin[kWhich]), to = min(r1, begin[kWhich + 1]);
+    const bool normed = kWhich == 0 ? a.proj.q_norm != nullptr
+                                    : kWhich == 1 && a.proj.k_norm != nullptr;
+    if (from >= to) return;
+    uint4 raw[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      raw[i] = from + i < to ? load(kWhich, from + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-  for (int i0 = r0; i0 < r1; i0 += kAtOnce) {
+    for (int i0 = from; i0 < to; i0 += kAtOnce) {
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (i0 + i >= r1) break;
-      const int h = row(i0 + i);
-      const bool live = h < total;
-      const int which = h < H ? 0 : h < H + K ? 1 : 2;
-      const int hh = which == 0 ? h : which == 1 ? h - H : h - H - K;
-      float x[8];
-      unpack8(raw[i], x);
-      raw[i] = load(i0 + i + kAtOnce < r1 ? row(i0 + i + kAtOnce) : total);
-      const bool normed = which == 0 ? a.proj.q_norm != nullptr
-                                     : which == 1 && a.proj.k_norm != nullptr;
-      if (__any_sync(~0u, normed)) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(~0u, ss, o);
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i0 + i >= to) break;
+        const int h = (i0 + i - begin[kWhich]) * kRows + mine;
+        float x[8];
+        unpack8(raw[i], x);
+        if (i0 + i + kAtOnce < to) raw[i] = load(kWhich, i0 + i + kAtOnce);
         if (normed) {
-          const float r = 1.0f / sqrtf(ss * (1.0f / D) + a.proj.eps);
+          float2 ss = make_float2(0.0f, 0.0f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (which == 0 ? wq[j] : wk[j]);
-        }
-      }
-      if (rot && __any_sync(~0u, which < 2)) {
+          for (int j = 0; j < 8; j += 2) ss = fma2(x[j], x[j + 1], x[j], x[j + 1], ss);
+          float sum = ss.x + ss.y;
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          float u = x[j + 1], v = x[j];
-          if (!a.rope.adjacent) {
-            u = __shfl_sync(~0u, x[j], partner);
-            v = __shfl_sync(~0u, x[j + 1], partner);
-          }
-          if (which < 2 && turns) {
-            x[j] = fmaf(u, sn[j], x[j] * cs[j]);
-            x[j + 1] = fmaf(v, sn[j + 1], x[j + 1] * cs[j + 1]);
+          for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+          const float r = rsqrtf(fmaf(sum, 1.0f / D, a.proj.eps));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = x[j] * r * (kWhich == 0 ? wq[j] : wk[j]);
+        }
+        if (kWhich < 2 && rot) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            float u = x[j + 1], v = x[j];
+            if (!a.rope.adjacent) {
+              u = __shfl_sync(~0u, x[j], partner);
+              v = __shfl_sync(~0u, x[j + 1], partner);
+            }
+            if (turns) {
+              x[j] = fmaf(u, sn[j], x[j] * cs[j]);
+              x[j + 1] = fmaf(v, sn[j + 1], x[j + 1] * cs[j + 1]);
+            }
           }
         }
-      }
-      if (which == 0 && live)
-        __stcs(reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * H + hh) * D + sub * 8), pack8(x));
-      const bool store = live && which > 0;
-      if (__any_sync(~0u, store)) {
-        int key;
-        uint8_t* tile = tile_of<D>(a.kv, slot, store ? hh : 0, key);
-        quantise_store<D>(x, tile, key, which == 2, sub, store);
+        if constexpr (kWhich == 0) {
+          if (h < H)
+            __stcs(reinterpret_cast<uint4*>(a.q_out + ((int64_t)t * H + h) * D + lane_at), pack8(x));
+        } else {
+          int key;
+          uint8_t* tile = tile_of<D>(a.kv, slot, h < K ? h : 0, key);
+          quantise_store<D>(x, tile, key, kWhich == 2, sub, h < K);
+        }
       }
     }
-  }
+  };
+  region(std::integral_constant<int, 0>{});
+  region(std::integral_constant<int, 1>{});
+  region(std::integral_constant<int, 2>{});
 }
 
 // Slots read back: scale * code + bias in fp32, rounded once to bf16.
@@ -257,9 +286,9 @@ __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   constexpr int kLanes = D / 8, kRows = 256 / kLanes;
   const int K = a.kv.kv_heads, sub = threadIdx.x % kLanes;
   griddep_wait();
-  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;  // [T][2][K]
-  if (row >= (int64_t)a.T * 2 * K) return;
-  const int t = (int)(row / (2 * K)), which = (int)(row / K) & 1, h = (int)(row % K);
+  const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / kLanes;  // [T][K]
+  if (row >= (int64_t)a.T * K) return;
+  const int t = (int)(row / K), h = (int)(row - (int64_t)t * K);
   const int slot = a.slot[t];
   if (slot < 0) return;
   if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
@@ -270,22 +299,31 @@ __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   const uint8_t* tile = tile_of<D>(a.kv, slot, h, key);
   const __half* meta = reinterpret_cast<const __half*>(tile + 16 * D);
   const int g = sub >> 3, chunk = (sub >> 2) ^ swizzle<D>(key);
-  const float s = __half2float(meta[which ? Meta<D>::v_scale(key, g) : Meta<D>::k_scale(key, g)]);
-  const float b = __half2float(meta[which ? Meta<D>::v_bias(key, g) : Meta<D>::k_bias(key, g)]);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + which * 8 * D + key * (D / 2) +
-                                                        chunk * 16 + (sub & 3) * 4);
-  float x[8];
+  const uint8_t* codes = tile + key * (D / 2) + chunk * 16 + (sub & 3) * 4;
+  const uint32_t wk = *reinterpret_cast<const uint32_t*>(codes);
+  const uint32_t wv = *reinterpret_cast<const uint32_t*>(codes + 8 * D);
+  const float ks = __half2float(meta[Meta<D>::k_scale(key, g)]);
+  const float kb = __half2float(meta[Meta<D>::k_bias(key, g)]);
+  const float vs = __half2float(meta[Meta<D>::v_scale(key, g)]);
+  const float vb = __half2float(meta[Meta<D>::v_bias(key, g)]);
+  float x[8], y[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = fmaf(s, (float)((w >> (4 * i)) & 15u), b);
-  *reinterpret_cast<uint4*>((which ? a.v : a.k) + ((int64_t)t * K + h) * D + sub * 8) = pack8(x);
+  for (int i = 0; i < 8; ++i) {
+    x[i] = fmaf(ks, (float)((wk >> (4 * i)) & 15u), kb);
+    y[i] = fmaf(vs, (float)((wv >> (4 * i)) & 15u), vb);
+  }
+  const int64_t at = row * D + sub * 8;
+  *reinterpret_cast<uint4*>(a.k + at) = pack8(x);
+  *reinterpret_cast<uint4*>(a.v + at) = pack8(y);
 }
 
 template <int D>
 cudaError_t store_d(const StoreArgs& a, cudaStream_t st) {
-  // about 32 warps per SM where there are rows for them
-  const int total = a.proj.q_heads + 2 * a.kv.kv_heads, per = 32 / (D / 8);
-  const int rounds = (total + per - 1) / per;
-  const int64_t want = ((int64_t)kGrid * 32 + a.T - 1) / a.T;
+  // about 16 warps per SM where there are rows for them (32 measured slower: 20.0 against
+  // 16.5 us for 1237 tokens of 48 rows of 128, read back)
+  const int per = 32 / (D / 8);
+  const int rounds = (a.proj.q_heads + per - 1) / per + 2 * ((a.kv.kv_heads + per - 1) / per);
+  const int64_t want = ((int64_t)kGrid * 16 + a.T - 1) / a.T;
   const int parts = (int)(want < rounds ? want : rounds);
   const int64_t warps = (int64_t)a.T * parts;
   return launch_pdl(store_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a, parts);
@@ -293,7 +331,7 @@ cudaError_t store_d(const StoreArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t load_d(const LoadArgs& a, cudaStream_t st) {
-  const int64_t rows = (int64_t)a.T * 2 * a.kv.kv_heads, per = 256 / (D / 8);
+  const int64_t rows = (int64_t)a.T * a.kv.kv_heads, per = 256 / (D / 8);
   return launch_pdl(load_kernel<D>, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, st, a);
 }
 
