@@ -488,14 +488,12 @@ class DeviceKv:
                  device="cuda", layers=1, with_pool=True):
         import torch
 
-        def ints(*n):
-            return torch.zeros(n, dtype=torch.int32, device=device)
+        def ints(n, value):
+            return torch.full(n, value, dtype=torch.int32, device=device)
 
-        self.block_table, self.seq_len = ints(max_rows, max_blocks), ints(max_rows)
-        self.free_list, self.free_count = ints(num_blocks), ints(1)
-        self.block_table.fill_(-1)
-        self.free_list.copy_(torch.arange(num_blocks - 1, -1, -1, device=device))
-        self.free_count.fill_(num_blocks)
+        self.block_table, self.seq_len = ints((max_rows, max_blocks), -1), ints((max_rows,), 0)
+        self.free_list = torch.arange(num_blocks - 1, -1, -1, dtype=torch.int32, device=device)
+        self.free_count = ints((1,), num_blocks)
 
         def struct(pool):
             return MoeKv(num_blocks, block_tokens, kv_heads, head_dim, max_rows, max_blocks,
@@ -505,7 +503,7 @@ class DeviceKv:
         n = moe_kv_block_bytes(struct(None))
         if n == 0:
             raise MoeError(MOE_EINVAL, moe_last_error())
-        self.pools = [torch.zeros((num_blocks, n), dtype=torch.uint8, device=device)
+        self.pools = [torch.empty((num_blocks, n), dtype=torch.uint8, device=device)
                       if with_pool else None for _ in range(layers)]
         self.pool = self.pools[0]
         self.layers = [struct(p) for p in self.pools]

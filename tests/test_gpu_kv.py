@@ -111,6 +111,7 @@ def _store_case(T, H, K, D, P, rot, adjacent, axes, norms, seed, gap=0):
     g = torch.Generator(device=DEV).manual_seed(seed)
     blocks = -(-T // P) + 2
     kv = m.DeviceKv(1, blocks, blocks, P, K, D)
+    kv.pool.zero_()
     batch = m.DeviceKvBatch(T, 1)
     batch.slot.copy_(_slots(rng, T, blocks, P))
     max_pos = 5000
@@ -499,6 +500,129 @@ def test_attention_on_two_streams_at_once():
     torch.cuda.synchronize()
     for i, o in enumerate(got):
         assert torch.equal(o, want[i % 2])
+
+
+def test_attention_of_many_rows():
+    """More rows than the kernels' scans take at a time, most of them short, some idle, two long
+    ones among them; decode and prompt rows in one call."""
+    rng = np.random.default_rng(23)
+    B = 1000
+    lens = rng.integers(0, 40, B)
+    lens[17], lens[901], lens[999] = 700, 300, 1
+    news = np.minimum(lens, rng.integers(0, 3, B))
+    news[901], news[999] = 100, 1
+    c = _attend_case(16, 1, 64, 4, lens.tolist(), news.tolist(), 24, poison=True)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_attend(c, out)
+
+
+def test_attention_without_work():
+    c = _attend_case(16, 2, 128, 4, [30, 0, 9], [1, 0, 1], 25)
+    c["batch"].q_start.zero_()
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0 and torch.all(out == 5.0)
+    out = _run_attend(c, max_new=500)
+    assert int(c["batch"].err[0]) == 0 and torch.all(out == 5.0)
+
+
+@pytest.mark.parametrize("max_new", [1, 3, 100])
+def test_attention_flags_rows_past_max_new(max_new):
+    lens, news = [50, 300, 41, 200], [1, 150, 1, 4]
+    c = _attend_case(16, 1, 128, 4, lens, news, 26)
+    out = _run_attend(c, max_new=max_new)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    start = 0
+    for b, n in enumerate(news):
+        if n > max_new:
+            assert torch.all(out[start:start + n] == 5.0)
+        start += n
+    _check_attend(c, out, rows=[b for b, n in enumerate(news) if n <= max_new])
+
+
+@pytest.mark.parametrize("news", [[1, 1], [4, 120]])
+def test_attention_of_broken_queries_stays_in_its_rows(news):
+    """An infinite or NaN query spoils its own output row and no other."""
+    c = _attend_case(16, 2, 256, 4, [200, 300], news, 27)
+    good = _run_attend(c)
+    q = c["q"].clone()
+    q[0, 1, 7] = float("nan")
+    q[sum(news) - 1, 5, 0] = float("inf")
+    out = _run_attend(c, q=q)
+    touched = torch.zeros(c["T"], c["H"], dtype=torch.bool, device=DEV)
+    touched[0, 1] = touched[sum(news) - 1, 5] = True
+    assert torch.equal(out[~touched], good[~touched])
+    assert torch.all(torch.isnan(out[0, 1].float()))
+
+
+@pytest.mark.parametrize("news", [[1, 2], [70, 1]])
+def test_far_blocks_of_a_large_pool(news):
+    """A pool of over 4 GB whose last blocks are in use: store, load and attention."""
+    P, K, D, r = 128, 8, 256, 2
+    blocks = (4 << 30) // (K * P * D * 9 // 8) + 40
+    kv = m.DeviceKv(2, 4, blocks, P, K, D)
+    lens = [300, 140]
+    batch = m.DeviceKvBatch(sum(lens), 2)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    # the cache was filled from the low blocks up: these rows get the last ones
+    kv.free_list.copy_(torch.arange(blocks, dtype=torch.int32, device=DEV))
+    m.moe_kv_plan(kv.c, _ints(lens), 2, batch.c)
+    assert int(batch.slot.min()) > (blocks - 6) * P
+    x = torch.randn(sum(lens), K * r + 2 * K, D, generator=g, device=DEV).bfloat16()
+    q = torch.empty(sum(lens), K * r, D, dtype=torch.bfloat16, device=DEV)
+    proj = m.make_qkv(x[:, :K * r], x[:, K * r:K * r + K], x[:, K * r + K:])
+    m.moe_qkv_store(kv.c, batch.c, None, proj, sum(lens), None, q)
+    assert torch.equal(q, x[:, :K * r])
+    k, v = (torch.empty(sum(lens), K, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    m.moe_kv_load(kv.c, batch.slot, sum(lens), k, v)
+    table = _np(kv.block_table)
+    first = int(table[table >= 0].min())
+    tail = _np(kv.pool[first:])
+    step = m.DeviceKvBatch(sum(news), 2)
+    step.q_start.copy_(_ints([0, news[0], sum(news)]))
+    step.kv_len.copy_(_ints(lens))
+    qq = (torch.randn(sum(news), K * r, D, generator=g, device=DEV)).bfloat16()
+    out = torch.empty_like(qq)
+    n = m.moe_kv_attention_workspace_bytes(kv.c, 2, sum(news), K * r, max(news))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    m.moe_kv_attention(kv.c, step.c, 2, qq, sum(news), K * r, max(news), D ** -0.5, ws, n, out)
+    assert int(step.err[0]) == 0 and int(batch.err[0]) == 0
+    start = 0
+    for b, (L, t) in enumerate(zip(lens, news)):
+        j = np.arange(L)
+        slots = (table[b, j // P] - first) * P + j % P
+        kk, vv = ref.read_slots(tail, slots, K, P, D)
+        at = sum(lens[:b])
+        for got, want in ((k, kk), (v, vv)):
+            assert np.all(np.abs(_f64(got[at:at + L]) - want) <= np.abs(want) * 2.0 ** -8)
+        _check_quantised(kk, _f64(x[at:at + L, K * r:K * r + K]), "k")
+        want = ref.attention(_f64(qq[start:start + t]), kk, vv, D ** -0.5, L - t)
+        tol = ref.attention_bound(_f64(qq[start:start + t]), kk, vv, D ** -0.5, want)
+        assert np.all(np.abs(_f64(out[start:start + t]) - want) <= tol)
+        start += t
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different shapes over one workspace, replayed one after the other."""
+    a = _attend_case(64, 2, 128, 8, [900, 30], [1, 1], 28)
+    b = _attend_case(16, 2, 128, 8, [400, 200], [300, 2], 29)
+    want = [_run_attend(x).clone() for x in (a, b)]
+    n = max(m.moe_kv_attention_workspace_bytes(x["kv"].c, x["B"], x["T"], x["H"], x["max_new"])
+            for x in (a, b))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    outs, graphs = [torch.full_like(x["q"], 5.0) for x in (a, b)], []
+    for x, o in zip((a, b), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            m.moe_kv_attention(x["kv"].c, x["batch"].c, x["B"], x["q"], x["T"], x["H"], x["max_new"],
+                               x["scale"], ws, n, o)
+        graphs.append(g)
+    for _ in range(3):
+        for g, o in zip(graphs, outs):
+            o.fill_(5.0)
+            g.replay()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
 
 
 # ------------------------------------------------------------------ all of them, as they are used
