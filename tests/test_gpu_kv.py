@@ -449,7 +449,8 @@ def test_attention_of_values_of_all_sizes(D, news):
     _check_attend(c, _run_attend(c))
 
 
-@pytest.mark.parametrize("lens,news", [([300, 70, 200], [1, 1, 1]), ([300, 260, 200], [150, 9, 130])])
+@pytest.mark.parametrize("lens,news", [([300, 70, 200], [1, 1, 1]), ([300, 260, 200], [150, 9, 130]),
+                                       ([300, 260, 200], [150, 90, 130])])
 def test_attention_leaves_out_bad_blocks_and_rows(lens, news):
     """Block ids outside the pool and rows whose bounds do not fit are flagged; the others'
     results stay."""
