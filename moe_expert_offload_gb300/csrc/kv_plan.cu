@@ -170,16 +170,27 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
       const int* rank = pass == 0 ? s_back : s_need;
       const long long from = carry[pass], to = carry[pass] + s_scan[pass][31];
       if (!(pass == 1 && refused)) {
-        for (int k = (int)from + tid; k < (int)to; k += kThreads) {
-          const int i = last_below(rank, kThreads, k);
-          int32_t* entry = a.kv.block_table + (int64_t)(b0 + i) * W + s_first[i] + (k - rank[i]);
-          int32_t* place = a.kv.free_list + (count1 - 1 - k);
-          if (pass == 0) {
-            *place = *entry;
-            *entry = -1;
-          } else {
-            *entry = *place;
+        // four blocks of a thread on their way at a time
+        for (int k0 = (int)from + tid; k0 < (int)to; k0 += 4 * kThreads) {
+          int32_t *src[4], *dst[4], v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j * kThreads;
+            if (k < (int)to) {
+              const int i = last_below(rank, kThreads, k);
+              int32_t* entry = a.kv.block_table + (int64_t)(b0 + i) * W + s_first[i] + (k - rank[i]);
+              int32_t* place = a.kv.free_list + (count1 - 1 - k);
+              src[j] = pass == 0 ? entry : place;
+              dst[j] = pass == 0 ? place : entry;
+              v[j] = *src[j];
+            }
           }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (k0 + j * kThreads < (int)to) {
+              *dst[j] = v[j];
+              if (pass == 0) *src[j] = -1;
+            }
         }
       }
       for (int i = 0; i < 3; ++i) carry[i] += s_scan[i][31];
