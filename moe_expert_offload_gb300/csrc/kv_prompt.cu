@@ -56,7 +56,9 @@ struct Cfg {
   static constexpr int kStages = D == 256 ? 1 : 2;  // key and value blocks held
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kBlockBytes = kKeys * D * 2;  // one block of keys (or values, or queries)
-  static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes;
+  // results on their way out: each softmax warp's 32 rows of 64 bytes, 80 apart
+  static constexpr int kOutBytes = kSoftWarps * 32 * 80;
+  static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes + kOutBytes;
   static constexpr int kPartial = kRows * (D + 2);  // floats: o [row][D], m [row], l [row]
   static constexpr uint32_t kIdescS = (1u << 4) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   const uint32_t r_inv = (65536 + r - 1) / r;         // x * r_inv >> 16 = x / r for x < 128
   const uint32_t base = (su32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + NT * C::kBlockBytes, v_at = k_at + S * C::kBlockBytes;
+  const uint32_t out_at = v_at + S * C::kBlockBytes;
 
   if (wid == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -455,49 +458,46 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
     const uint32_t o_tm = tmem + lanes + tile * C::kO;
     uint32_t n = 0;  // blocks seen
-    // A unit's queries: a warp's rows, 8 columns a lane, a few loads under way at a time.  The
+    // A unit's queries: a warp's rows, 8 columns a lane, all loads under way at once.  The
     // buffer is free once the last block's scores of the unit before are there.
     auto load_queries = [&](const Row& w_row, const Unit& u) {
       constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = C::kRows / kSoftWarps / kAtOnce;
-#pragma unroll 1
-      for (int i0 = 0; i0 < kRounds; i0 += 8) {
-        uint4 raw[8];
+      constexpr uint32_t kGroup = kLanes == 32 ? ~0u : (1u << kLanes) - 1u;
+      const uint32_t group = kGroup << (lane / kLanes * kLanes);
+      uint4 raw[kRounds];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int qr = (wid * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
-          const int i_tok = (int)(in * r_inv >> 16), t = u.tok0 + (qr >> 7) * per_tile + i_tok;
-          raw[i] = make_uint4(0, 0, 0, 0);
-          if (in < per_tile * r && t < w_row.n)
-            raw[i] = *reinterpret_cast<const uint4*>(
-                a.q + ((int64_t)(w_row.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
-                lane % kLanes * 8);
+      for (int i = 0; i < kRounds; ++i) {
+        const int qr = (wid * kRounds + i) * kAtOnce + lane / kLanes, in = qr & 127;
+        const int i_tok = (int)(in * r_inv >> 16), t = u.tok0 + (qr >> 7) * per_tile + i_tok;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (in < per_tile * r && t < w_row.n)
+          raw[i] = *reinterpret_cast<const uint4*>(
+              a.q + ((int64_t)(w_row.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
+              lane % kLanes * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kRounds; ++i) {
+        const int qr = (wid * kRounds + i) * kAtOnce + lane / kLanes, in = qr & 127;
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint32_t big = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
+        big = __reduce_max_sync(group, max(big & 0xFFFFu, big >> 16));
+        const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
+        const float up = pow2(14 - e);
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[2 * k] = __uint_as_float(w[k] << 16) * up;
+          x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int qr = (wid * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
-          const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-          uint32_t big = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
-          big = max(big & 0xFFFFu, big >> 16);
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(~0u, big, o));
-          const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
-          const float up = pow2(14 - e);
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(w[k] << 16) * up;
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
-          }
-          const int col8 = lane % kLanes;
-          sts128(q_at + (qr >> 7) * C::kBlockBytes + (col8 >> 3) * (kKeys * 128) + in * 128 +
-                     (((col8 & 7) ^ (in & 7)) << 4),
-                 make_uint4(pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]),
-                            pack_h2(x[3], x[7])));
-          // score = fac * accumulated, in units of log2
-          if (col8 == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
-        }
+        const int col8 = lane % kLanes;
+        sts128(q_at + (qr >> 7) * C::kBlockBytes + (col8 >> 3) * (kKeys * 128) + in * 128 +
+                   (((col8 & 7) ^ (in & 7)) << 4),
+               make_uint4(pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]),
+                          pack_h2(x[3], x[7])));
+        // score = fac * accumulated, in units of log2
+        if (col8 == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
       }
       fence_async();
       __syncwarp();
@@ -510,6 +510,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       const int b = walk.b;
       asm volatile("bar.sync 1, 256;" ::: "memory");  // s_fac of all rows
       const float fac = s_fac[tile * 128 + row];
+      {
+        // the next unit's queries come to L2 meanwhile: a row of queries a thread
+        Walk ahead = walk;
+        Unit un;
+        if (next_unit(ahead, a, r, tok, un) && tid < C::kRows) {
+          const int in = tid & 127, i_tok = (int)(in * r_inv >> 16);
+          const int t = un.tok0 + (tid >> 7) * per_tile + i_tok;
+          if (in < per_tile * r && t < ahead.row.n) {
+            const uint16_t* src =
+                a.q + ((int64_t)(ahead.row.start + t) * a.heads + un.kvh * r + in - i_tok * r) * D;
+#pragma unroll
+            for (int k = 0; k < D; k += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + k));
+          }
+        }
+      }
       const int row_tok = (int)(row * r_inv >> 16), row_h = row - row_tok * r;
       const int t = u.tok0 + tile * per_tile + row_tok;
       const bool live = row < per_tile * r && t < ri.n;
@@ -664,40 +679,66 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       }
       const bool whole = done.blk0 == 0 && done.blk1 == done.blocks;
       const float inv = l > 0.0f ? 1.0f / l : l;
-      uint16_t* dst = a.out + ((int64_t)(ri.start + t) * a.heads + done.kvh * r + row_h) * D;
+      // A lane holds a row's columns; through shared memory four lanes get 64 bytes of a row each
+      // time, so that stores fill sectors (a row per lane: 2.5 times as long).
+      const long long out_row =
+          live ? (long long)(ri.start + t) * a.heads + done.kvh * r + row_h : -1ll;
       float* part = parts + ((size_t)blockIdx.x * 2 + (done.blk0 == 0 ? 1 : 0)) * C::kPartial;
       const int pr = tile * 128 + row;
       constexpr int kCols = NT == 1 ? D / 2 : D;
       const int c_at = NT == 1 ? wg * (D / 2) : 0;
+      const uint32_t stage = out_at + wid * (32 * 80), mine = stage + lane * 80;
+      auto flush = [&](auto&& store) {  // store(row of the warp, its output row, 16-byte piece, data)
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2);
+          const long long to = __shfl_sync(~0u, out_row, rr);
+          uint4 d;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w)
+                       : "r"(stage + rr * 80 + (lane & 3) * 16)
+                       : "memory");
+          if (to >= 0) store(rr, to, lane & 3, d);
+        }
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int c = 0; c < kCols; c += 32) {
         uint32_t v[32];
         tm_ld32(o_tm + c_at + c, v);
         tm_wait_regs(v);
-        if (live) {
+        // columns in order: 0,4,1,5,2,6,3,7 -> 0..7
+        auto y = [&](int k) { return __uint_as_float(v[(k & ~7) + (k & 3) * 2 + ((k >> 2) & 1)]); };
+        if (whole) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          // columns in order: 0,4,1,5,2,6,3,7 -> 0..7
-          const float y[8] = {__uint_as_float(v[k]),     __uint_as_float(v[k + 2]),
-                              __uint_as_float(v[k + 4]), __uint_as_float(v[k + 6]),
-                              __uint_as_float(v[k + 1]), __uint_as_float(v[k + 3]),
-                              __uint_as_float(v[k + 5]), __uint_as_float(v[k + 7])};
-          if (whole) {
+          for (int k = 0; k < 32; k += 8) {
             uint32_t h[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(y[2 * q] * inv, y[2 * q + 1] * inv);
+              const __nv_bfloat162 x =
+                  __floats2bfloat162_rn(y(k + 2 * q) * inv, y(k + 2 * q + 1) * inv);
               h[q] = *reinterpret_cast<const uint32_t*>(&x);
             }
-            *reinterpret_cast<uint4*>(dst + c_at + c + k) = make_uint4(h[0], h[1], h[2], h[3]);
-          } else {
-            float* at = part + (size_t)pr * D + c_at + c + k;
-            *reinterpret_cast<float4*>(at) = make_float4(y[0], y[1], y[2], y[3]);
-            *reinterpret_cast<float4*>(at + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            sts128(mine + k * 2, make_uint4(h[0], h[1], h[2], h[3]));
+          }
+          flush([&](int, long long to, int piece, uint4 d) {
+            *reinterpret_cast<uint4*>(a.out + to * D + c_at + c + piece * 8) = d;
+          });
+        } else {
+#pragma unroll
+          for (int half = 0; half < 32; half += 16) {
+#pragma unroll
+            for (int k = half; k < half + 16; k += 4)
+              sts128(mine + (k - half) * 4,
+                     make_uint4(__float_as_uint(y(k)), __float_as_uint(y(k + 1)),
+                                __float_as_uint(y(k + 2)), __float_as_uint(y(k + 3))));
+            flush([&](int rr, long long, int piece, uint4 d) {
+              *reinterpret_cast<uint4*>(part + (size_t)(pr - lane + rr) * D + c_at + c + half +
+                                        piece * 4) = d;
+            });
           }
         }
-        }
-        __syncwarp();
       }
       if (!whole && (NT == 2 || wg == 0)) {
         part[(size_t)C::kRows * D + pr] = m;
@@ -772,12 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             for (int k = 0; k < 4; ++k)
               sts128(at + ((((chunk & 1) * 4 + k) ^ (key & 7)) << 4), dequant8(w[k], sc, bi));
           }
-          load(next);
-          next = tile_at(i + 2);
           fence_async();
           __syncwarp();
           if (lane == 0) sc::bar_arrive(su32(&full[n % S]));
           ++n;
+          // (not before the fence, which would wait for them)
+          load(next);
+          next = tile_at(i + 2);
         }
       }
     };
