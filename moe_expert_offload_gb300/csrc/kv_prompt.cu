@@ -47,7 +47,6 @@ constexpr int kKeys = 128;  // keys of a block
 constexpr int kSoftWarps = 8, kSideWarps = 8, kMmaWarp = 24;
 constexpr int kThreads = 28 * 32;  // seven warp groups; three warps of the last one idle
 constexpr int kStartRegs = 72;
-constexpr int kUnitKeys = 384;  // a unit's fixed cost, in keys
 constexpr float kNone = -1e30f;
 
 template <int D>
@@ -55,6 +54,9 @@ struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;   // query tiles of a unit
   static constexpr int kStages = D == 256 ? 1 : 2;  // key and value blocks held
   static constexpr int kRows = 128 * kTiles;
+  // a unit's fixed cost, in keys: queries in, results out (8192 tokens, head_dim 256: 576, 516, 523
+  // and 539 us at 384, 512, 640 and 1024; shorter rows and head_dim 128 do not care)
+  static constexpr int kUnitKeys = D == 256 ? 512 : 384;
   static constexpr int kBlockBytes = kKeys * D * 2;  // one block of keys (or values, or queries)
   // results on their way out: each softmax warp's 32 rows of 64 bytes, 80 apart
   static constexpr int kOutBytes = kSoftWarps * 32 * 80;
@@ -98,8 +100,9 @@ __device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok
 
 // Cost of the first j units of a head of the row: each its keys (taking every
 // tile for a full one) and a fixed part.
+template <int D>
 __device__ __forceinline__ long long cost_before(const Row& i, int tok, long long j) {
-  return j * (i.len - i.n + kUnitKeys) + (long long)tok * (j * (j + 1) / 2);
+  return j * (i.len - i.n + Cfg<D>::kUnitKeys) + (long long)tok * (j * (j + 1) / 2);
 }
 
 struct Unit {
@@ -116,7 +119,9 @@ struct Walk {
   Row row;
 };
 
+template <int D>
 __device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int tok, Unit& u) {
+  constexpr int kUnitKeys = Cfg<D>::kUnitKeys;
   while (w.left > 0) {
     if (w.row.tiles == 0 || w.kvh >= a.kv.kv_heads) {
       do {
@@ -391,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       long long cost = 0;
       if (b < a.rows) {
         const Row i = row_info(a, b, r, tok);
-        if (i.tiles) cost = K * cost_before(i, tok, i.tiles);
+        if (i.tiles) cost = K * cost_before<D>(i, tok, i.tiles);
       }
       long long v = cost;
 #pragma unroll
@@ -435,18 +440,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     walk.b = s_row;
     walk.row = row_info(a, walk.b, r, tok);
     walk.left = min(s_share, total - blockIdx.x * s_share);
-    const long long per_head = cost_before(walk.row, tok, walk.row.tiles);
+    const long long per_head = cost_before<D>(walk.row, tok, walk.row.tiles);
     long long x = s_at;
     walk.kvh = (int)(x / per_head);
     x -= walk.kvh * per_head;
     int lo = 0, hi = walk.row.tiles;  // the last unit whose cost_before is <= x
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (cost_before(walk.row, tok, mid) <= x) lo = mid;
+      if (cost_before<D>(walk.row, tok, mid) <= x) lo = mid;
       else hi = mid;
     }
     walk.j = lo;
-    walk.at = x - cost_before(walk.row, tok, lo);
+    walk.at = x - cost_before<D>(walk.row, tok, lo);
   }
   Unit u;
 
@@ -503,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       __syncwarp();
       if (lane == 0) sc::bar_arrive(su32(&q_full));
     };
-    bool have = next_unit(walk, a, r, tok, u);
+    bool have = next_unit<D>(walk, a, r, tok, u);
     if (have) load_queries(walk.row, u);
     while (have) {
       const Row ri = walk.row;
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         // the next unit's queries come to L2 meanwhile: a row of queries a thread
         Walk ahead = walk;
         Unit un;
-        if (next_unit(ahead, a, r, tok, un) && tid < C::kRows) {
+        if (next_unit<D>(ahead, a, r, tok, un) && tid < C::kRows) {
           const int in = tid & 127, i_tok = (int)(in * r_inv >> 16);
           const int t = un.tok0 + (tid >> 7) * per_tile + i_tok;
           if (in < per_tile * r && t < ahead.row.n) {
@@ -623,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           tm_st16(s_tm + wg * 32 + 16, p + 16);
         } else {
           // 32 columns at a time (loads under way one part ahead measured 10% slower)
-#pragma unroll 2
+#pragma unroll(D == 128 ? 4 : 1)
           for (int c = 0; c < 4; ++c) {
             uint32_t x[32], p[16];
             tm_ld32(s_tm + c * 32, x);
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       }
       // the next unit's queries come while the last product runs
       const Unit done = u;
-      have = next_unit(walk, a, r, tok, u);
+      have = next_unit<D>(walk, a, r, tok, u);
       if (have) load_queries(walk.row, u);
       // ---- the unit's end (here): a result, or a part of one
       wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
@@ -765,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       uint4 code[KC];
       uint32_t meta[KG];  // scale | bias << 16
       uint32_t n = 0;     // blocks written
-      while (next_unit(walk, a, r, tok, u)) {
+      while (next_unit<D>(walk, a, r, tok, u)) {
         const int len = walk.row.len;
         const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
         const uint8_t* pool = static_cast<const uint8_t*>(a.kv.pool) +
@@ -833,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     if (wid == kMmaWarp) {
     // -------------------------------------------------------------------- MMAs
     uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
+    const bool leader = elect_one();
     // descriptors: a byte offset moves them by a sixteenth
     const uint64_t dq = smem_desc(q_at, 16), dk = smem_desc(k_at, 16);
     const uint64_t dv = smem_desc(v_at, kKeys * 128);
@@ -841,11 +847,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     // ordered by themselves.
     auto scores = [&](int tile) {
       const int slot = NT == 1 ? (int)(n_k & 1u) : tile, st = n_k % S;
-      if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
-      if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
-      tc_after();
       const uint64_t da = dq + tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
-      if (elect_one()) {
+      // (the wait that is over first comes first: it is not on the way then)
+      if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
+      if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
+      tc_after();
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const int off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16;
@@ -857,11 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     };
     auto product = [&](int tile, uint32_t n, bool more) {
       const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n % S;
-      wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
-      if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
-      tc_after();
       const uint64_t db = dv + st * (C::kBlockBytes / 16);
-      if (elect_one()) {
+      if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
+      wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
+      tc_after();
+      if (leader) {
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
           mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8, db + k * (2048 / 16),
@@ -871,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       __syncwarp();
     };
     auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
-    while (next_unit(walk, a, r, tok, u)) {
+    while (next_unit<D>(walk, a, r, tok, u)) {
       wait_all(&q_full, n_u++, s_stop);
       const int nb = u.blk1 - u.blk0;
       if constexpr (NT == 1) {
@@ -899,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       }
       if (stopped()) break;
     }
-    if (elect_one()) commit(su32(&drained));  // nothing is under way when TMEM goes back
+    if (leader) commit(su32(&drained));  // nothing is under way when TMEM goes back
     __syncwarp();
     if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
     }
