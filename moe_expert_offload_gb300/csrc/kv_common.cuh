@@ -22,9 +22,17 @@ namespace kv {
 
 constexpr int kTile = 16;  // tokens of a tile
 constexpr int kGrid = 152; // CTAs of the attention kernels: one per SM
-// rows of up to this many queries per kv head (new tokens x query heads on it)
+// Rows of up to this many queries per kv head (new tokens x query heads on it)
 // go through the decode kernel, longer ones through the prompt kernel
-constexpr int kDecodeCols = 64;
+// (microseconds, decode | prompt, 8 query heads on a kv head; 1 and 16 rows of
+// 2000 to 4000 keys, 4 of 30000 to 60000):
+//   head_dim 256, 32 queries  13 | 26   35 | 37    86 |  82
+//                 48          15 | 27   43 | 38   123 |  85
+//   head_dim 128, 64          15 | 29   54 | 53   154 | 112
+//                 96          17 | 31   80 | 57   240 | 116
+//   head_dim 64,  64          13 | 24   36 | 43    97 |  92
+//                 96          14 | 25   48 | 42   149 |  98
+__host__ __device__ constexpr int decode_cols(int D) { return D == 256 ? 32 : 64; }
 
 __host__ __device__ constexpr int tile_bytes(int D) { return 18 * D; }
 

@@ -8,8 +8,12 @@
 // warp.  Where a unit is cut between warps or CTAs, its
 // running maximum, sum and accumulator are merged afterwards, in a fixed order.
 //
-// A unit's queries are the columns: 8 per tensor-core tile, column c = (token
-// c / r, head c % r) of the r query heads that share the kv head.  Both
+// A unit's queries are 8 columns, column c = (token c / r, head c % r) of the r
+// query heads that share the kv head; more columns are more units, each with a
+// walk of its own over the keys.  (16 columns a unit, one walk instead of two,
+// took 1.3 to 2 times as long at head_dim 256, whose registers it spilled, and
+// was no faster at 64; at 128, 32 columns over 60000 keys took 77 instead of 88
+// us, but over 100 rows of up to 1000 keys 62 instead of 52.)  Both
 // products take the codes as the A operand, 16 keys x 16 columns (or their
 // transpose, by ldmatrix.trans) at a time:
 //   S^T[key][col] = sum_g scale_K[key][g] (codes . q_g) + sum_g bias_K[key][g] sum(q_g)
@@ -46,20 +50,17 @@ using sc::su32;
 using sc::warp_wait;
 
 // Warps: as many as the registers allow, which are shared out by SM quarters: 16 warps of 128
-// registers or 8 of 255, by what accumulators and queries take (R = D * NT / 128 multiples of
-// 32 + 16).  16 columns of 256 dims keep their query fragments in shared memory.
-template <int D, int NT>
+// registers or 8 of 255, by what accumulators and query fragments take (48 registers at
+// head_dim 128, 96 at 256).
+template <int D>
 struct Cfg {
-  static constexpr int R = D * NT / 128;
-  static constexpr bool kQShared = R == 4;
-  static constexpr int kWarps = R <= 1 ? 16 : 8;
+  static constexpr int kWarps = D == 256 ? 8 : 16;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kTiles = D == 64 && NT == 1 ? 4 : 2;  // key tiles of a stage
+  static constexpr int kTiles = D == 64 ? 4 : 2;  // key tiles of a stage
   static constexpr int kStageBytes = kTiles * tile_bytes(D);
-  static constexpr int kStages = kQShared ? 2 : NT == 2 ? 4 : 3;
-  static constexpr int kQBytes = kQShared ? 16 * D * 2 : 0;
-  static constexpr int kWarpBytes = kStages * kStageBytes + kQBytes;
-  static constexpr int kCols = 8 * NT;
+  static constexpr int kStages = 3;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kCols = 8;
   static constexpr int kPartial = kCols * (D + 2);  // floats: o [col][D], m [col], l [col]
   static constexpr int kUnitCost = 512 / D;  // a unit's fixed cost, in key tiles
   static constexpr int kCentre = 16 / kTiles;       // stages between two moves of the mean
@@ -98,7 +99,7 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int b, int r, int
     if (flag) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
     return i;
   }
-  if (i.n * r <= kDecodeCols) i.ntb = (i.n * r + cols - 1) / cols;
+  if (i.n * r <= decode_cols(a.kv.head_dim)) i.ntb = (i.n * r + cols - 1) / cols;
   return i;
 }
 
@@ -195,9 +196,9 @@ struct Stage {
 };
 constexpr uint32_t kBegin = 1u << 8, kEnd = 1u << 9, kLast = 1u << 10;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArgs a) {
-  using C = Cfg<D, NT>;
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a) {
+  using C = Cfg<D>;
   constexpr int G = D / 64, W = C::kWarps, TS = C::kTiles, S = C::kStages;
   constexpr int C0 = C::kUnitCost;
   extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -289,7 +290,6 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
   bool failed = false;
   if (s_row[wid] >= 0) {
     constexpr int NK = D / 16;  // MMAs along a head
-    constexpr int NQ = C::kQShared ? 1 : NK;
     const uint32_t ring = ring0 + wid * C::kWarpBytes;
     // ---- the walk: units in order, each unit's tiles in stages that end at multiples of the stage
     auto row_of = [&](int b) {
@@ -376,10 +376,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
     while (issued < S && issue(issued)) ++issued;
     bool fill = issued == S;
 
-    const uint32_t q_at = ring + S * C::kStageBytes + lane * 8;  // kQShared: [nt][k][lane]
-    uint32_t qf[NT][NQ][2], qs[NT][2];
-    float fac[NT][2], m[NT][2], o[NT][NK][4], off[NT][G][2], ob[NT][4];
-    int sigma = 0, lim[NT][2], open = 0, len = 0, age = 0, c_base = 0, cols = 0;
+    uint32_t qf[NK][2], qs[2];
+    float fac[2], m[2], o[NK][4], off[G][2], ob[4];
+    int sigma = 0, lim[2], open = 0, len = 0, age = 0, c_base = 0, cols = 0;
     bool first = false;
     const int key_l = ((lane >> 3) & 1) * 8 + (lane & 7), c0 = (lane >> 4) ^ swizzle<D>(key_l);
     const uint32_t row_off = key_l * (D / 2), c_off = c0 << 4;
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
       constexpr bool Edge = decltype(edge_tag)::value;
       auto has = [&](int tt) { return !Edge || tt < cnt; };  // (a stage without an edge is full)
       // ---- scores
-      float x[NT][TS][4];
+      float x[TS][4];
 #pragma unroll
       for (int tt = 0; tt < TS; ++tt) {
         if (has(tt)) {
@@ -424,16 +423,13 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
               }
             }
           }
+          float sum[4] = {};
+          mma_f16(sum, b0, b1, b0, b1, qs[0], qs[1]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float d[4] = {};
-            mma_f16(d, b0, b1, b0, b1, qs[nt][0], qs[nt][1]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[nt][tt][j] = d[j] * 1.52587890625e-05f;  // 2^-16
-          }
+          for (int j = 0; j < 4; ++j) x[tt][j] = sum[j] * 1.52587890625e-05f;  // 2^-16
           // the groups' chains side by side
           uint32_t w[G][4];
-          float d[G][NT][4] = {};
+          float d[G][4] = {};
 #pragma unroll
           for (int grp = 0; grp < G; ++grp) ldsm4(w[grp], base + row_off + (c_off ^ (grp << 5)));
 #pragma unroll
@@ -442,34 +438,20 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
             for (int grp = 0; grp < G; ++grp) {
               const uint32_t u0 = w[grp][(i >> 1) * 2] >> (8 * (i & 1));
               const uint32_t u1 = w[grp][(i >> 1) * 2 + 1] >> (8 * (i & 1));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                uint32_t q0, q1;
-                if constexpr (C::kQShared) {
-                  lds64(q0, q1, q_at + (nt * NK + 4 * grp + i) * 256);
-                } else {
-                  q0 = qf[nt][4 * grp + i][0];
-                  q1 = qf[nt][4 * grp + i][1];
-                }
-                mma_f16(d[grp][nt], u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u,
-                        u1 & 0x00F000F0u, q0, q1);
-              }
+              mma_f16(d[grp], u0 & 0x000F000Fu, u1 & 0x000F000Fu, u0 & 0x00F000F0u,
+                      u1 & 0x00F000F0u, qf[4 * grp + i][0], qf[4 * grp + i][1]);
             }
 #pragma unroll
           for (int grp = 0; grp < G; ++grp)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                x[nt][tt][j] = fmaf(sk[j >> 1][grp], d[grp][nt][j], x[nt][tt][j]);
+            for (int j = 0; j < 4; ++j)
+              x[tt][j] = fmaf(sk[j >> 1][grp], d[grp][j], x[tt][j]);
           if constexpr (Edge) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int key = key0 + tt * kTile + g + 8 * (j >> 1);
-                if (key > lim[nt][j & 1] || !((present >> tt) & 1)) x[nt][tt][j] = -INFINITY;
-              }
+            for (int j = 0; j < 4; ++j) {
+              const int key = key0 + tt * kTile + g + 8 * (j >> 1);
+              if (key > lim[j & 1] || !((present >> tt) & 1)) x[tt][j] = -INFINITY;
+            }
           }
         }
       }
@@ -477,14 +459,12 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
       // (two keys of one group per word)
       bool grow = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int tt = 0; tt < TS; ++tt)
+        if (has(tt)) {
 #pragma unroll
-        for (int tt = 0; tt < TS; ++tt)
-          if (has(tt)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              grow |= fmaf(x[nt][tt][j], fac[nt][j & 1], -m[nt][j & 1]) > 8.0f;
-          }
+          for (int j = 0; j < 4; ++j)
+            grow |= fmaf(x[tt][j], fac[j & 1], -m[j & 1]) > 8.0f;
+        }
       uint32_t big = 0;
 #pragma unroll
       for (int i = 0; i < TS * G * 8; i += 32) {
@@ -507,53 +487,44 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
         big = __reduce_max_sync(~0u, big);
         const int to = max(sigma, big >= 0x7C00u ? 16 : (int)(big >> 10) - 14);
         const float turn = pow2(sigma - to);
+        float f[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float f[2];
+        for (int i = 0; i < 2; ++i) {
+          float top = m[i];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float top = m[nt][i];
+          for (int tt = 0; tt < TS; ++tt)
+            if (has(tt))
+              top = fmaxf(top, fmaxf(x[tt][i] * fac[i], x[tt][2 + i] * fac[i]));
 #pragma unroll
-            for (int tt = 0; tt < TS; ++tt)
-              if (has(tt))
-                top = fmaxf(top, fmaxf(x[nt][tt][i] * fac[nt][i], x[nt][tt][2 + i] * fac[nt][i]));
-#pragma unroll
-            for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, sh));
-            f[i] = exp2_fast(m[nt][i] - top);
-            m[nt][i] = top;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ob[nt][j] *= f[j & 1];
-#pragma unroll
-            for (int i = 0; i < NK; ++i) o[nt][i][j] *= f[j & 1] * turn;
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int grp = 0; grp < G; ++grp) off[nt][grp][i] *= f[i] * turn;
+          for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, sh));
+          f[i] = exp2_fast(m[i] - top);
+          m[i] = top;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ob[j] *= f[j & 1];
+#pragma unroll
+          for (int i = 0; i < NK; ++i) o[i][j] *= f[j & 1] * turn;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int grp = 0; grp < G; ++grp) off[grp][i] *= f[i] * turn;
         sigma = to;
       }
       const uint32_t s_one = pack_h2(pow2(-sigma), pow2(-sigma));  // keeps p * scale in range
       // ---- weights and the second product
-      float bsum[NT][4] = {};
+      float bsum[4] = {};
 #pragma unroll
       for (int tt = 0; tt < TS; ++tt) {
         if (has(tt)) {
           const uint32_t base = st + tt * tile_bytes(D), meta = base + 16 * D;
-          uint32_t p0[NT], p1[NT], ps0[NT], ps1[NT];
+          float p[4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              p[j] = exp2_fast(fmaf(x[nt][tt][j], fac[nt][j & 1], 7.0f - m[nt][j & 1]));
-            p0[nt] = transpose8(pack_h2(p[0], p[1]));
-            p1[nt] = transpose8(pack_h2(p[2], p[3]));
-            ps0[nt] = hmul2(p0[nt], s_one);
-            ps1[nt] = hmul2(p1[nt], s_one);
-          }
+          for (int j = 0; j < 4; ++j)
+            p[j] = exp2_fast(fmaf(x[tt][j], fac[j & 1], 7.0f - m[j & 1]));
+          const uint32_t p0 = transpose8(pack_h2(p[0], p[1])), p1 = transpose8(pack_h2(p[2], p[3]));
+          const uint32_t ps0 = hmul2(p0, s_one), ps1 = hmul2(p1, s_one);
           uint32_t live0 = ~0u, live1 = ~0u;
           if constexpr (Edge) {  // this lane's keys: 2t, 2t + 1, 2t + 8, 2t + 9
             const int n = (present >> tt) & 1 ? len - (key0 + tt * kTile + 2 * t) : 0;
@@ -566,51 +537,39 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
             a0 = lds32(meta + 96 * G + (g * 16 + 2 * t) * 2) & live0;
             a2 = lds32(meta + 96 * G + (g * 16 + 2 * t + 8) * 2) & live1;
           }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(bsum[nt], a0, 0, a2, 0, p0[nt], p1[nt]);
+          mma_f16(bsum, a0, 0, a2, 0, p0, p1);
 #pragma unroll
           for (int grp = 0; grp < G; ++grp) {
             const uint32_t v0 = lds32(meta + 64 * G + (grp * 16 + 2 * t) * 2) & live0;
             const uint32_t v1 = lds32(meta + 64 * G + (grp * 16 + 2 * t + 8) * 2) & live1;
             uint32_t w[4];
             ldsm4t(w, base + 8 * D + row_off + (c_off ^ (grp << 5)));
-            uint32_t f0[NT], f1[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              f0[nt] = hmul2(ps0[nt], v0);
-              f1[nt] = hmul2(ps1[nt], v1);
-            }
+            const uint32_t f0 = hmul2(ps0, v0), f1 = hmul2(ps1, v1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t u0 = w[(i >> 1) * 2] >> (8 * (i & 1));
               const uint32_t u1 = w[(i >> 1) * 2 + 1] >> (8 * (i & 1));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(o[nt][4 * grp + i], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu,
-                        u1 & 0x00F000F0u, f0[nt], f1[nt]);
+              mma_f16(o[4 * grp + i], u0 & 0x000F000Fu, u0 & 0x00F000F0u, u1 & 0x000F000Fu,
+                      u1 & 0x00F000F0u, f0, f1);
             }
           }
         }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ob[nt][j] += bsum[nt][j];
+      for (int j = 0; j < 4; ++j) ob[j] += bsum[j];
       if (++age % C::kCentre == 0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int grp = 0; grp < G; ++grp)
 #pragma unroll
-          for (int grp = 0; grp < G; ++grp)
+          for (int i = 0; i < 2; ++i) {
+            const float d = 0.5f * fmaf(o[4 * grp][2 + i], 0.0625f, o[4 * grp][i]);
+            off[grp][i] += d;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float d = 0.5f * fmaf(o[nt][4 * grp][2 + i], 0.0625f, o[nt][4 * grp][i]);
-              off[nt][grp][i] += d;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                o[nt][4 * grp + k][i] -= d;
-                o[nt][4 * grp + k][2 + i] -= 16.0f * d;
-              }
+            for (int k = 0; k < 4; ++k) {
+              o[4 * grp + k][i] -= d;
+              o[4 * grp + k][2 + i] -= 16.0f * d;
             }
+          }
       }
     };
 
@@ -630,86 +589,74 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
         open = len - n + 1;  // keys below are seen by every column
         sigma = 0;
         age = 0;
+        const int c = c_base + g;
+        const uint16_t* src = a.q + ((int64_t)(start + c / r) * a.heads + kvh * r + c % r) * D;
+        uint4 raw[2 * G];
+        float big = 0.0f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int c = c_base + nt * 8 + g;
-          const uint16_t* src = a.q + ((int64_t)(start + c / r) * a.heads + kvh * r + c % r) * D;
-          uint4 raw[2 * G];
-          float big = 0.0f;
+        for (int ch = 0; ch < 2 * G; ++ch) {
+          raw[ch] = c < cols ? *reinterpret_cast<const uint4*>(src + ch * 32 + t * 8)
+                             : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
 #pragma unroll
-          for (int ch = 0; ch < 2 * G; ++ch) {
-            raw[ch] = c < cols ? *reinterpret_cast<const uint4*>(src + ch * 32 + t * 8)
-                               : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              big = fmaxf(big, fabsf(__uint_as_float(w[i] << 16)));
-              big = fmaxf(big, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
-            }
-          }
-          big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-          int e = (int)((__float_as_uint(big) >> 23) & 255u) - 127;  // 2^e <= big < 2^(e+1)
-          e = max(e, -100);
-          const float up = pow2(14 - e);
-          float sum[4] = {};
-#pragma unroll
-          for (int ch = 0; ch < 2 * G; ++ch) {
-            const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] = __uint_as_float(w[i] << 16) * up;
-              v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t q0 = pack_h2(v[2 * i], v[2 * i + 4]);
-              const uint32_t q1 = pack_h2(v[2 * i + 1] * 0.0625f, v[2 * i + 5] * 0.0625f);
-              if constexpr (C::kQShared) {
-                asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_at + (nt * NK + 2 * ch + i) * 256),
-                             "r"(q0), "r"(q1)
-                             : "memory");
-              } else {
-                qf[nt][2 * ch + i][0] = q0;
-                qf[nt][2 * ch + i][1] = q1;
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum[ch / 2] += v[i];
-          }
-          float hi[4] = {}, lo[4] = {};
-#pragma unroll
-          for (int i = 0; i < G; ++i) {
-            sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
-            sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
-            const float v = sum[i] * 0.00390625f;  // 2^-8: into fp16's range
-            hi[i] = __half2float(__float2half_rn(v));
-            lo[i] = v - hi[i];
-          }
-          qs[nt][0] = t == 0 ? pack_h2(hi[0], hi[1]) : t == 1 ? pack_h2(hi[2], hi[3]) : 0u;
-          qs[nt][1] = t == 0 ? pack_h2(lo[0], lo[1]) : t == 1 ? pack_h2(lo[2], lo[3]) : 0u;
-          // score = fac * accumulated, in units of log2; per C-fragment column 2t, 2t+1
-          const float f = a.scale * 1477.3197218702985f * pow2(e);  // log2(e) 2^24 2^(e-14)
-          fac[nt][0] = __shfl_sync(~0u, f, 8 * t);
-          fac[nt][1] = __shfl_sync(~0u, f, 8 * t + 4);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int cc = c_base + nt * 8 + 2 * t + i;
-            // the last key that the column's token sees
-            lim[nt][i] = len - n + min(cc, cols - 1) / r;
-            m[nt][i] = kNone;
-#pragma unroll
-            for (int grp = 0; grp < G; ++grp) off[nt][grp][i] = 0.0f;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            ob[nt][j] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NK; ++i) o[nt][i][j] = 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            big = fmaxf(big, fabsf(__uint_as_float(w[i] << 16)));
+            big = fmaxf(big, fabsf(__uint_as_float(w[i] & 0xFFFF0000u)));
           }
         }
-        if constexpr (C::kQShared) __syncwarp();
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        int e = (int)((__float_as_uint(big) >> 23) & 255u) - 127;  // 2^e <= big < 2^(e+1)
+        e = max(e, -100);
+        const float up = pow2(14 - e);
+        float sum[4] = {};
+#pragma unroll
+        for (int ch = 0; ch < 2 * G; ++ch) {
+          const uint32_t w[4] = {raw[ch].x, raw[ch].y, raw[ch].z, raw[ch].w};
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16) * up;
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            qf[2 * ch + i][0] = pack_h2(v[2 * i], v[2 * i + 4]);
+            qf[2 * ch + i][1] = pack_h2(v[2 * i + 1] * 0.0625f, v[2 * i + 5] * 0.0625f);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum[ch / 2] += v[i];
+        }
+        float hi[4] = {}, lo[4] = {};
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
+          sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
+          const float v = sum[i] * 0.00390625f;  // 2^-8: into fp16's range
+          hi[i] = __half2float(__float2half_rn(v));
+          lo[i] = v - hi[i];
+        }
+        qs[0] = t == 0 ? pack_h2(hi[0], hi[1]) : t == 1 ? pack_h2(hi[2], hi[3]) : 0u;
+        qs[1] = t == 0 ? pack_h2(lo[0], lo[1]) : t == 1 ? pack_h2(lo[2], lo[3]) : 0u;
+        // score = fac * accumulated, in units of log2; per C-fragment column 2t, 2t+1
+        const float f = a.scale * 1477.3197218702985f * pow2(e);  // log2(e) 2^24 2^(e-14)
+        fac[0] = __shfl_sync(~0u, f, 8 * t);
+        fac[1] = __shfl_sync(~0u, f, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int cc = c_base + 2 * t + i;
+          // the last key that the column's token sees
+          lim[i] = len - n + min(cc, cols - 1) / r;
+          m[i] = kNone;
+#pragma unroll
+          for (int grp = 0; grp < G; ++grp) off[grp][i] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          ob[j] = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NK; ++i) o[i][j] = 0.0f;
+        }
       }
       if (!warp_wait(su32(&full[wid][s]), (uint32_t)(used / S) & 1u)) {
         failed = true;
@@ -740,45 +687,42 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
             Part{unit, start, n_new, ntb, first, (len + kTile - 1) / kTile - key0 / kTile - cnt};
       const int kvh = unit / ntb;
       const float even = pow2(24 + sigma), odd = pow2(20 + sigma);
+      float l[2], inv[2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float l[2], inv[2];
+      for (int i = 0; i < 2; ++i) {
+        l[i] = __shfl_sync(~0u, ob[i], 28 + t);
+        inv[i] = l[i] > 0.0f ? 1.0f / l[i] : l[i];  // no key: 0; NaN stays
+      }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[i] = __shfl_sync(~0u, ob[nt][i], 28 + t);
-          inv[i] = l[i] > 0.0f ? 1.0f / l[i] : l[i];  // no key: 0; NaN stays
-        }
+      for (int grp = 0; grp < G; ++grp) {
+        float bias[2];
 #pragma unroll
-        for (int grp = 0; grp < G; ++grp) {
-          float bias[2];
+        for (int i = 0; i < 2; ++i)
+          bias[i] = fmaf(off[grp][i], even, __shfl_sync(~0u, ob[i], 4 * grp + t));
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            bias[i] = fmaf(off[nt][grp][i], even, __shfl_sync(~0u, ob[nt][i], 4 * grp + t));
+        for (int ch = 0; ch < 2; ++ch) {
+          const int d0 = grp * 64 + ch * 32 + 4 * g;
 #pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const int d0 = grp * 64 + ch * 32 + 4 * g;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {  // columns 2t, 2t + 1
-              const int cc = nt * 8 + 2 * t + i;
-              const float(&u)[4] = o[nt][4 * grp + 2 * ch], (&v)[4] = o[nt][4 * grp + 2 * ch + 1];
-              const float4 y = make_float4(fmaf(u[i], even, bias[i]), fmaf(u[2 + i], odd, bias[i]),
-                                           fmaf(v[i], even, bias[i]), fmaf(v[2 + i], odd, bias[i]));
-              if (part) {
-                *reinterpret_cast<float4*>(part + cc * D + d0) = y;
-              } else if (c_base + cc < cols) {
-                const int c = c_base + cc;
-                store_bf16(a.out + ((int64_t)(start + c / r) * a.heads + kvh * r + c % r) * D + d0,
-                           y, inv[i]);
-              }
+          for (int i = 0; i < 2; ++i) {  // columns 2t, 2t + 1
+            const int cc = 2 * t + i;
+            const float(&u)[4] = o[4 * grp + 2 * ch], (&v)[4] = o[4 * grp + 2 * ch + 1];
+            const float4 y = make_float4(fmaf(u[i], even, bias[i]), fmaf(u[2 + i], odd, bias[i]),
+                                         fmaf(v[i], even, bias[i]), fmaf(v[2 + i], odd, bias[i]));
+            if (part) {
+              *reinterpret_cast<float4*>(part + cc * D + d0) = y;
+            } else if (c_base + cc < cols) {
+              const int c = c_base + cc;
+              store_bf16(a.out + ((int64_t)(start + c / r) * a.heads + kvh * r + c % r) * D + d0,
+                         y, inv[i]);
             }
           }
         }
-        if (part && g == 0) {
+      }
+      if (part && g == 0) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            part[C::kCols * D + nt * 8 + 2 * t + i] = m[nt][i];
-            part[C::kCols * (D + 1) + nt * 8 + 2 * t + i] = l[i];
-          }
+        for (int i = 0; i < 2; ++i) {
+          part[C::kCols * D + 2 * t + i] = m[i];
+          part[C::kCols * (D + 1) + 2 * t + i] = l[i];
         }
       }
     }
@@ -882,9 +826,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::kThreads, 1) decode_kernel(AttnArg
 
 // Units that were cut between CTAs, each found at the CTA that began it: their
 // parts in order, a few warps per column.
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
-  using C = Cfg<D, NT>;
+  using C = Cfg<D>;
   constexpr int kSplit = 32 / C::kCols;  // warps side by side on a column's parts
   __shared__ float s_y[kSplit - 1][C::kCols][D], s_m[kSplit][C::kCols], s_l[kSplit][C::kCols];
   griddep_wait();
@@ -963,24 +907,22 @@ __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
                  y, l, lane);
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
-  using C = Cfg<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, NT>,
+  using C = Cfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e == cudaSuccess)
-    e = launch_pdl(decode_kernel<D, NT>, dim3(kGrid), dim3(C::kThreads), C::kSmem, st, a);
+    e = launch_pdl(decode_kernel<D>, dim3(kGrid), dim3(C::kThreads), C::kSmem, st, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D, NT>, dim3(kGrid), dim3(1024), 0, st, a);
+  return launch_pdl(combine_kernel<D>, dim3(kGrid), dim3(1024), 0, st, a);
 }
 
 template <int D>
-size_t bytes_for() {
-  const size_t one = (2 + Cfg<D, 1>::kWarps) * (size_t)Cfg<D, 1>::kPartial;
-  const size_t two = (2 + Cfg<D, 2>::kWarps) * (size_t)Cfg<D, 2>::kPartial;
-  return (kCutBytes + kGrid * 4 * (one > two ? one : two) + 255) / 256 * 256;
+constexpr size_t bytes_for() {
+  return (kCutBytes + kGrid * 4 * (2 + Cfg<D>::kWarps) * (size_t)Cfg<D>::kPartial + 255) /
+         256 * 256;
 }
-
 }  // namespace
 
 size_t decode_workspace_bytes(int D) {
@@ -988,11 +930,8 @@ size_t decode_workspace_bytes(int D) {
 }
 
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st) {
-  const long long cols = (long long)a.max_new * (a.heads / a.kv.kv_heads);
   const int D = a.kv.head_dim;
-  if (cols <= 8)
-    return D == 256 ? launch<256, 1>(a, st) : D == 128 ? launch<128, 1>(a, st) : launch<64, 1>(a, st);
-  return D == 256 ? launch<256, 2>(a, st) : D == 128 ? launch<128, 2>(a, st) : launch<64, 2>(a, st);
+  return D == 256 ? launch<256>(a, st) : D == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace kv

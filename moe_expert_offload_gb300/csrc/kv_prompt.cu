@@ -92,7 +92,7 @@ __device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok
   // (the decode kernel, which sees every row, reports what does not fit)
   if (i.n <= 0 || i.start < 0 || i.n > a.max_new || i.n > i.len ||
       (long long)i.len > (long long)a.kv.max_blocks * a.kv.block_tokens ||
-      (long long)i.start + i.n > a.T || (long long)i.n * r <= kDecodeCols)
+      (long long)i.start + i.n > a.T || (long long)i.n * r <= decode_cols(a.kv.head_dim))
     return i;
   i.tiles = (i.n + tok - 1) / tok;
   return i;
