@@ -319,12 +319,14 @@ __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
 
 template <int D>
 cudaError_t store_d(const StoreArgs& a, cudaStream_t st) {
-  // about 16 warps per SM where there are rows for them (32 measured slower: 20.0 against
-  // 16.5 us for 1237 tokens of 48 rows of 128, read back)
+  // As many parts as run at once: 20 warps per SM have registers (16-byte loads of
+  // 16 query and 2 + 2 key and value heads of 256, read back, us: 8 tokens 10.8 in
+  // one part and 4.5 in six; 1024 tokens 12.4 in one, 10.1 in two, 13.8 in three, whose
+  // last warps come in a second wave)
   const int per = 32 / (D / 8);
   const int rounds = (a.proj.q_heads + per - 1) / per + 2 * ((a.kv.kv_heads + per - 1) / per);
-  const int64_t want = ((int64_t)kGrid * 16 + a.T - 1) / a.T;
-  const int parts = (int)(want < rounds ? want : rounds);
+  const int64_t want = (int64_t)kGrid * 20 / a.T;
+  const int parts = (int)(want < 1 ? 1 : want < rounds ? want : rounds);
   const int64_t warps = (int64_t)a.T * parts;
   return launch_pdl(store_kernel<D>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, st, a, parts);
 }
