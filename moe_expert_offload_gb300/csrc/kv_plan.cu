@@ -231,23 +231,25 @@ __global__ void __launch_bounds__(512) map_kernel(PlanArgs a, int wide) {
   }
   const int T = start[B], all = a.batch.max_tokens;
   const int step = gridDim.x * blockDim.x * 4;
-  for (int t0 = (blockIdx.x * blockDim.x + threadIdx.x) * 4; t0 < all; t0 += step) {
+  // (64 bits: the last step of a thread may pass 2^31)
+  for (int64_t at = (blockIdx.x * blockDim.x + threadIdx.x) * 4; at < all; at += step) {
+    const int t0 = (int)at;
     int slot[4], pos[4], row = t0 < T ? last_below(start, B, t0) : B;
     int len = row < B ? a.batch.kv_len[row] : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       slot[i] = -1;
       pos[i] = 0;
-      if (t0 + i < T) {
+      if (i < T - t0) {
         while (start[row + 1] <= t0 + i) len = a.batch.kv_len[++row];
         map_token(a, t0 + i, row, start[row], start[row + 1], len, slot[i], pos[i]);
       }
     }
-    if (wide && t0 + 4 <= all) {
+    if (wide && all - t0 >= 4) {
       *reinterpret_cast<int4*>(a.batch.slot + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
       *reinterpret_cast<int4*>(a.batch.pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
     } else {
-      for (int i = 0; i < 4 && t0 + i < all; ++i) {
+      for (int i = 0; i < 4 && i < all - t0; ++i) {
         a.batch.slot[t0 + i] = slot[i];
         a.batch.pos[t0 + i] = pos[i];
       }

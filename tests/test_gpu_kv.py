@@ -88,6 +88,28 @@ def test_plan_of_fewer_rows_and_edges():
     assert _check_plan(kv, batch, tab, [32, 32, 1, 0], 64)
 
 
+def test_plan_of_the_longest_batch():
+    """Entries up to 2^31 - 2 of a batch of 2^31 - 1 tokens."""
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    kv = m.DeviceKv(2, 700, 1400, 16, 1, 64, with_pool=False)
+    batch = m.DeviceKvBatch(n, 2)
+    m.moe_kv_reset(kv.c)
+    batch.slot.fill_(7)
+    batch.pos.fill_(7)
+    tab = ref.Tables(2, 700, 1400, 16)
+    refused, start, length, slot, pos = tab.plan([5000, 6001], 11001)
+    assert not refused
+    m.moe_kv_plan(kv.c, _ints([5000, 6001]), 2, batch.c)
+    assert int(batch.err[0]) == 0
+    assert np.array_equal(_np(batch.slot[:11001]), slot)
+    assert np.array_equal(_np(batch.pos[:11001]), pos)
+    for a in range(11001, n, 1 << 28):
+        assert (batch.slot[a:a + (1 << 28)] == -1).all()
+        assert not batch.pos[a:a + (1 << 28)].any()
+
+
 def test_plan_refuses_tables_that_are_not_its_own():
     """A free count and row lengths that together pass the pool's blocks: flagged, nothing moves."""
     kv = m.DeviceKv(2, 4, 5, 16, 1, 64, with_pool=False)
