@@ -612,7 +612,7 @@ typedef struct moe_qkv {
  * quantised store of keys and values, in one kernel.
  *   y = x * rsqrt(mean(x^2) + eps) * w   (q and k, where a norm is given)
  *   then the rotation (q and k); v is stored as it is.  All in fp32.
- *   q_out      device bf16 [T][q_heads][D], contiguous
+ *   q_out      device bf16 [T][q_heads][D], contiguous; must not overlap q, k, v
  *   cache      k and v of token t at batch->slot[t], straight from fp32: per
  *              64 columns scale = fp16((max - min) / 15), bias = fp16(min),
  *              code = round((y - bias) / scale), half to even, in 0..15 (scale
@@ -660,6 +660,7 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
  *   heads      query heads, a multiple of kv_heads, at most
  *              MOE_KV_MAX_GROUP per kv head
  *   max_new    upper bound of n over the rows (1: a decode step)
+ *   scale      finite and > 0
  *   workspace  device, >= moe_kv_attention_workspace_bytes for the same
  *              arguments, 256-byte aligned, any contents; calls whose
  *              execution overlaps need one each

@@ -539,6 +539,11 @@ def rope_table(max_pos, rotary_dim, base=10000.0, device="cuda"):
 
 def make_rope(table, rotary_dim, adjacent=False, axes=1, pair_axis=None) -> MoeRope:
     """table: device fp32 [max_pos][rotary_dim], cosines then sines of each pair."""
+    if (str(table.dtype) != "torch.float32" or not table.is_contiguous()
+            or table.shape != (table.shape[0], rotary_dim)):
+        raise MoeError(MOE_EINVAL, "table must be contiguous fp32 [max_pos][rotary_dim]")
+    if any(not 0 <= a < axes for a in pair_axis or []) or len(pair_axis or []) > 128:
+        raise MoeError(MOE_EINVAL, "pair_axis must hold up to 128 axes below `axes`")
     r = MoeRope(_ptr(table), table.shape[0], rotary_dim, 1 if adjacent else 0, axes)
     for i, a in enumerate(pair_axis or []):
         r.pair_axis[i] = a
@@ -547,11 +552,19 @@ def make_rope(table, rotary_dim, adjacent=False, axes=1, pair_axis=None) -> MoeR
 
 
 def make_qkv(q, k, v, q_norm=None, k_norm=None, eps=1e-6) -> MoeQkv:
-    """q [T, heads, D], k and v [T, kv_heads, D]: bf16 device tensors whose columns are
-    contiguous (slices of one projection buffer are fine)."""
+    """q [T, heads, D], k and v [T, kv_heads, D]: bf16 device tensors (or their bits as
+    int16) whose columns are contiguous (slices of one projection buffer are fine); norms
+    fp32 [D]."""
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or t.element_size() != 2:
+        if (t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1)
+                or str(t.dtype) not in ("torch.bfloat16", "torch.int16", "torch.uint16")):
             raise MoeError(MOE_EINVAL, f"{name} must be bf16 [T, heads, D] with contiguous columns")
+    if k.shape != v.shape or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]:
+        raise MoeError(MOE_EINVAL, "q, k and v differ in tokens, columns or kv heads")
+    for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+        if t is not None and (str(t.dtype) != "torch.float32" or not t.is_contiguous()
+                              or t.shape != (q.shape[2],)):
+            raise MoeError(MOE_EINVAL, f"{name} must be contiguous fp32 [D]")
     p = MoeQkv(_ptr(q), _ptr(k), _ptr(v), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
                v.stride(0), v.stride(1), q.shape[1], eps, _ptr(q_norm), _ptr(k_norm))
     p.tensors = (q, k, v, q_norm, k_norm)

@@ -124,6 +124,7 @@ int moe_qkv_store(const moe_kv* kv, const moe_kv_batch* batch, const moe_rope* r
   if (!rc) rc = check_batch(batch);
   if (!rc) rc = check_tokens(batch, T);
   if (rc) return rc;
+  if (T == 0) return set_ok();
   if (!proj) return set_error(MOE_EINVAL, "proj is NULL");
   if (proj->q_heads < 1 || proj->q_heads > MOE_KV_MAX_HEADS)
     return set_error(MOE_EINVAL, "q_heads must be in 1..%d", MOE_KV_MAX_HEADS);
@@ -154,7 +155,6 @@ int moe_qkv_store(const moe_kv* kv, const moe_kv_batch* batch, const moe_rope* r
                          (int)rope->pair_axis[i], rope->axes);
     a.rope = *rope;
   }
-  if (T == 0) return set_ok();
   a.kv = *kv;
   a.proj = *proj;
   a.slot = batch->slot;
@@ -173,10 +173,10 @@ int moe_kv_load(const moe_kv* kv, const int32_t* slots, int32_t T, void* k, void
   if (!rc) rc = check_pool(kv);
   if (rc) return rc;
   if (T < 0) return set_error(MOE_EINVAL, "T must be >= 0");
+  if (T == 0) return set_ok();
   if (!slots || !k || !v) return set_error(MOE_EINVAL, "moe_kv_load: NULL argument");
   if (!aligned(k, 16) || !aligned(v, 16))
     return set_error(MOE_EINVAL, "moe_kv_load: k and v must be 16-byte aligned");
-  if (T == 0) return set_ok();
   moe::kv::LoadArgs a;
   a.kv = *kv;
   a.slot = slots;
@@ -219,6 +219,7 @@ int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, 
   if (!rc) rc = check_tokens(batch, T);
   if (!rc) rc = check_heads(kv, heads, max_new);
   if (rc) return rc;
+  if (T == 0) return set_ok();
   if (!q || !out || !workspace) return set_error(MOE_EINVAL, "moe_kv_attention: NULL argument");
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256))
     return set_error(MOE_EINVAL, "q and out (16 B) and workspace (256 B) alignment");
@@ -227,7 +228,6 @@ int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, 
   const size_t need = moe::kv::attn_workspace_bytes(*kv, rows, T, heads, max_new);
   if (workspace_bytes < need)
     return set_error(MOE_ECAPACITY, "workspace %zu < %zu bytes", workspace_bytes, need);
-  if (T == 0) return set_ok();
   moe::kv::AttnArgs a;
   a.kv = *kv;
   a.batch = *batch;

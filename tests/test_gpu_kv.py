@@ -408,6 +408,22 @@ def test_attention(i, poison):
     _check_attend(c, out)
 
 
+@pytest.mark.parametrize("K,D,r,lens,news", [
+    (1, 256, 64, [500, 1, 40], [1, 1, 1]),  # single tokens of more queries than a decode unit takes
+    (1, 256, 33, [300, 17], [1, 1]),
+    (2, 256, 32, [129, 700], [1, 1]),
+    (1, 256, 48, [260, 16], [3, 16]),
+    (2, 256, 8, [90, 1200, 33], [4, 5, 1]),  # 32 and 40 queries per kv head
+    (1, 128, 64, [300, 4], [1, 2]),
+    (1, 64, 63, [200, 1], [2, 1]),
+])
+def test_attention_where_the_kernels_meet(K, D, r, lens, news):
+    c = _attend_case(32, K, D, r, lens, news, 60 + D + r, poison=True)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_attend(c, out)
+
+
 def test_attention_is_repeatable_and_ignores_its_workspace():
     c = _attend_case(64, 2, 128, 8, [3000, 5, 777, 1200], [1, 2, 200, 1], 7)
     first = _run_attend(c)

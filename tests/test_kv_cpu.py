@@ -189,6 +189,33 @@ def test_workspace_size():
         assert m.moe_kv_attention_workspace_bytes(_kv(), *a) == 0
 
 
+def test_no_tokens_need_no_buffers():
+    """An empty step's tensors have no address."""
+    proj = _proj(q=None, k=None, v=None)
+    assert _store(T=0, proj=proj, q_out=None) == m.MOE_OK
+    assert m.moe_kv_load(_kv(), None, 0, None, None, None, 0) == m.MOE_OK
+    assert _attend(T=0, q=None, out=None) == m.MOE_OK
+
+
+def test_binding_refusals():
+    import torch
+
+    t = m.rope_table(7, 32, device="cpu")
+    for a in ((t.double(), 32), (t[:, :16], 16), (t, 48), (t, 32, False, 2, [0, 2]),
+              (t, 32, False, 1, [0, 256]), (t, 32, False, 1, [-1]), (t, 32, False, 1, [0] * 129)):
+        with pytest.raises(m.MoeError):
+            m.make_rope(*a)
+    x = torch.zeros(5, 12, 64, dtype=torch.bfloat16)
+    q, k, v, w = x[:, :8], x[:, 8:10], x[:, 10:], torch.ones(64)
+    m.make_qkv(q, k, v, w, w)
+    m.make_qkv(q.view(torch.int16), k, v)
+    for a in ((q.half(), k, v), (q, k.float(), v), (q, k, x[:, 9:]), (q, k[:4], v[:4]),
+              (q, k[..., :32], v[..., :32]), (q, k, v, w.half()), (q, k, v, w[:32]),
+              (q, k, v, None, torch.ones(128)[::2])):
+        with pytest.raises(m.MoeError):
+            m.make_qkv(*a)
+
+
 def test_binding_helpers():
     import torch
 
