@@ -34,6 +34,12 @@
 // it to the MMA's truncating sums (measured at 128k keys: 2.1e-3 from fp64
 // against 1.6e-3 for bf16 rounding alone): every 16 tiles each group's mean is
 // moved from them into a rounded fp32 sum of its own.
+//
+// Measured: 64 rows of 150 to 8191 keys, 32 query heads on 8 of 128 (330 MB): 75.6 us,
+// 4.4 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 112 us, 5.3 TB/s.
+// The stream alone takes 54.7 and 88 us; the rest is instruction issue, 316 and
+// 400 per tile, most of them unpacking codes.  Few keys are latency: 1000 keys of
+// one row 11.7 us, 2.2 of them the scan over the rows and 2.5 the combine kernel.
 #include <type_traits>
 
 #include "kv_common.cuh"

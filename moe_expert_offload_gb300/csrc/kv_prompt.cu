@@ -30,6 +30,14 @@
 // near 2^15, so that small ones keep their bits); queries are scaled by a power
 // of two per row.  The maximum that weights refer to follows the scores only
 // when they pass it by 2^8, so the accumulator in TMEM is rarely rescaled.
+//
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 515 us, 1068 TFLOP/s (55% of a
+// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 876 us,
+// 1187 TFLOP/s (61%).  Bound by the chain of a block (scores, TMEM load, maximum,
+// exponentials, TMEM store, product): the tensor pipe is busy 47 and 51% of the
+// time, the issue slots 60 and 53%.  At head_dim 256 a second score tile does not
+// fit TMEM beside the 256 columns of results and the two slots in use, and a second
+// key block not the shared memory.
 #include <type_traits>
 
 #include "kv_common.cuh"

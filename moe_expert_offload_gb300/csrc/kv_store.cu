@@ -12,8 +12,13 @@
 // three shuffles, and a lane's eight codes are one 32-bit word.  One warp per
 // token and part of its heads (few tokens: one part per row, so that a decode
 // step's rows run side by side; many: one part, so that cosines, sines and norm
-// weights are read once per token): it keeps four rows' loads under way.  Bound
-// by memory.
+// weights are read once per token): it keeps four rows' loads under way.
+// Measured with the read-back: 8192 tokens of 16 query and 2 + 2 key and value
+// heads of 256, 47 us (179 MB: 3.8 TB/s); 1237 tokens of 32 and 8 + 8 heads of 128
+// with three axes 16 us; 8 tokens 4.6 us.  Large calls are bound by instruction
+// issue and latency together: 168 instructions a row at 55% of the issue slots,
+// 17 warps per SM (96 registers), waiting on loads and shuffles in equal parts;
+// a persistent loop over tokens took 63 us.
 #include <type_traits>
 
 #include "kv_common.cuh"
