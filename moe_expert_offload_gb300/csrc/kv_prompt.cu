@@ -75,7 +75,7 @@ struct Cfg {
                                       ((128u >> 4) << 24);  // bit 16: B is MN-major
   static constexpr int kO = D == 256 ? 256 : 128;   // TMEM columns between the tiles' results
   static constexpr int kS = 256;                    // scores: two slots of 128 columns
-  static constexpr int kSoftRegs = D == 256 ? 112 : 128, kSideRegs = D == 256 ? 56 : 48;
+  static constexpr int kSoftRegs = D == 256 ? 112 : 136, kSideRegs = D == 256 ? 56 : 48;
   static constexpr int kMmaRegs = D == 256 ? 48 : 40;
   static_assert(kSoftRegs * 256 + kSideRegs * 512 + kMmaRegs * 128 <= kStartRegs * kThreads,
                 "the registers given out are there");
@@ -635,27 +635,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           tm_st16(s_tm + wg * 32, p);
           tm_st16(s_tm + wg * 32 + 16, p + 16);
         } else {
-          // 32 columns at a time (loads under way one part ahead measured 10% slower)
-#pragma unroll(D == 128 ? 4 : 1)
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], p[16];
-            tm_ld32(s_tm + c * 32, x);
+          // 64 columns at a time (2048 tokens on 30000 of head_dim 128: 790 us, 863 with 32 at a
+          // time, 926 with loads under way one part ahead, whose registers spill)
+#pragma unroll(D == 128 ? 2 : 1)
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[64], p[32];
+            tm_ld32(s_tm + c * 64, x);
+            tm_ld32(s_tm + c * 64 + 32, x + 32);
             tm_wait_regs(x);
-            hide(x, 2 * c);
-            hide(x + 16, 2 * c + 1);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) hide(x + 16 * q, 4 * c + q);
             sum = make_float2(0.0f, 0.0f);
-            weights(x, p);
-            weights(x + 16, p + 8);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) weights(x + 16 * q, p + 8 * q);
             if (__any_sync(~0u, sum.x + sum.y > kMost)) {
-              // (the block's earlier weights are in TMEM by now, and scaled there)
               const float before = m;
               float top = kNone;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(x[k]));
+              for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(x[k]));
               refer(top * fac);
               const float f = ex2(before - m);
               const uint32_t ff = pack_h2(f, f);
-              for (int k = 0; k < c; ++k) {
+              for (int k = 0; k < 2 * c; ++k) {
                 uint32_t old[16];
                 tm_wait_st();
                 tm_ld16(s_tm + k * 16, old);
@@ -665,11 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
                 tm_st16(s_tm + k * 16, old);
               }
               sum = make_float2(0.0f, 0.0f);
-              weights(x, p);
-              weights(x + 16, p + 8);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) weights(x + 16 * q, p + 8 * q);
             }
             l += sum.x + sum.y;
-            tm_st16(s_tm + c * 16, p);
+            tm_st16(s_tm + c * 32, p);
+            tm_st16(s_tm + c * 32 + 16, p + 16);
           }
         }
         tm_wait_st();
