@@ -25,7 +25,7 @@
 // per 16 keys (the groups' biases as A; for O together with a row of ones that
 // sums p).  Queries are scaled by a power of two per column into fp16's range
 // (exact but for columns 2^-29 below the largest).  p is rounded to fp16 with
-// its largest value near 2^15, and its product with the values' scale (after a
+// its largest value between 2^7 and 2^15, and its product with the values' scale (after a
 // power of two that keeps scales above 1 in range) once more: 2^-11 each against
 // the output's 2^-8; weights below 2^-21 scale of the largest lose that precision
 // to fp16's subnormals.  The maximum that p refers to follows the scores only when they

@@ -26,18 +26,23 @@
 // The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
 // order in which one LOP3 yields pairs): the queries are laid out alike, and the
 // result is put in order when it is stored.
-// fp16 roundings: keys and values 2^-11 once, weights 2^-11 once (their largest
-// near 2^15, so that small ones keep their bits); queries are scaled by a power
-// of two per row.  The maximum that weights refer to follows the scores only
-// when they pass it by 2^8, so the accumulator in TMEM is rarely rescaled.
+// fp16 roundings: keys and values 2^-11 once, weights 2^-11 once (2^7 for the
+// maximum that they refer to, so that small ones keep their bits); queries are
+// scaled by a power of two per row.  That maximum follows the scores only when
+// weights may pass fp16's range (a score 2^3 to 2^9 above it), so the accumulator in
+// TMEM is rarely rescaled.
 //
 // Measured: 8192 tokens, 16 query heads on 2 of 256: 515 us, 1068 TFLOP/s (55% of a
-// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 876 us,
-// 1187 TFLOP/s (61%).  Bound by the chain of a block (scores, TMEM load, maximum,
-// exponentials, TMEM store, product): the tensor pipe is busy 47 and 51% of the
-// time, the issue slots 60 and 53%.  At head_dim 256 a second score tile does not
-// fit TMEM beside the 256 columns of results and the two slots in use, and a second
-// key block not the shared memory.
+// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 788 us,
+// 1320 TFLOP/s (68%).  Bound by the chain of a block: at head_dim 64 and 128 scores,
+// TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
+// takes all the shared memory there is, values freed, dequantised (1400 cycles),
+// fenced (570), seen by the issuer (350) and multiplied (1500).  The tensor pipe is
+// busy 57% (128) and 47% (256) of the time, the issue slots 58 and 60%.  Measured and
+// dropped: two tiles with the next scores in halves of 64 keys, the first before
+// the product (975 us then against 876), a warp of its own that issues for each
+// tile (1046); one tile with keys and values handed over by halves of the columns
+// (575 against 516), with a second issuing warp for the products (556).
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -570,8 +575,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           }
         };
         // The weights relative to the maximum so far, 2^7 above it.  While a part's sum is below
-        // 2^16 each of them fits fp16; where it is not, some score passes the maximum by 2^4 or
-        // more: the maximum follows, what there is is scaled and the weights are formed again.
+        // 2^16 each of them fits fp16; where it is not, some weight of the 64 passes the maximum's
+        // by 2^3 or more: the maximum follows, what there is is scaled and the weights are formed
+        // again.
         float2 sum;
         auto weights = [&](const uint32_t* v, uint32_t* p) {
           const float off = 7.0f - m;
@@ -846,79 +852,79 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
     if (wid == kMmaWarp) {
-    // -------------------------------------------------------------------- MMAs
-    uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
-    const bool leader = elect_one();
-    // descriptors: a byte offset moves them by a sixteenth
-    const uint64_t dq = smem_desc(q_at, 16), dk = smem_desc(k_at, 16);
-    const uint64_t dv = smem_desc(v_at, kKeys * 128);
-    // A tile's scores of block n_k go where the weights of the block before (two blocks before,
-    // with one tile) were: their product has to be over, as MMAs of other accumulators are not
-    // ordered by themselves.
-    auto scores = [&](int tile) {
-      const int slot = NT == 1 ? (int)(n_k & 1u) : tile, st = n_k % S;
-      const uint64_t da = dq + tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
-      // (the wait that is over first comes first: it is not on the way then)
-      if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
-      if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
-      tc_after();
-      if (leader) {
+      // -------------------------------------------------------------------- MMAs
+      uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
+      const bool leader = elect_one();
+      // descriptors: a byte offset moves them by a sixteenth
+      const uint64_t dq = smem_desc(q_at, 16), dk = smem_desc(k_at, 16);
+      const uint64_t dv = smem_desc(v_at, kKeys * 128);
+      // A tile's scores of block n_k go where the weights of the block before (two blocks before,
+      // with one tile) were: their product has to be over, as MMAs of other accumulators are not
+      // ordered by themselves.
+      auto scores = [&](int tile) {
+        const int slot = NT == 1 ? (int)(n_k & 1u) : tile, st = n_k % S;
+        const uint64_t da = dq + tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
+        // (the wait that is over first comes first: it is not on the way then)
+        if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
+        if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
+        tc_after();
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const int off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16;
-          mma_ss(tmem + C::kS + slot * 128, da + off, db + off, C::kIdescS, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            const int off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16;
+            mma_ss(tmem + C::kS + slot * 128, da + off, db + off, C::kIdescS, k > 0);
+          }
+          commit(su32(&s_full[tile][n_k & 1u]));
         }
-        commit(su32(&s_full[tile][n_k & 1u]));
-      }
-      __syncwarp();
-    };
-    auto product = [&](int tile, uint32_t n, bool more) {
-      const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n % S;
-      const uint64_t db = dv + st * (C::kBlockBytes / 16);
-      if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
-      wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
-      tc_after();
-      if (leader) {
+        __syncwarp();
+      };
+      auto product = [&](int tile, uint32_t n, bool more) {
+        const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n % S;
+        const uint64_t db = dv + st * (C::kBlockBytes / 16);
+        if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
+        wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
+        tc_after();
+        if (leader) {
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8, db + k * (2048 / 16),
-                 C::kIdescO, more || k > 0);
-        commit(su32(&o_done[tile][n & 1u]));
+          for (int k = 0; k < kKeys / 16; ++k)
+            mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8, db + k * (2048 / 16),
+                   C::kIdescO, more || k > 0);
+          commit(su32(&o_done[tile][n & 1u]));
+        }
+        __syncwarp();
+      };
+      auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
+      while (next_unit<D>(walk, a, r, tok, u)) {
+        wait_all(&q_full, n_u++, s_stop);
+        const int nb = u.blk1 - u.blk0;
+        if constexpr (NT == 1) {
+          for (int i = 0; i <= nb && !stopped(); ++i) {
+            if (i < nb) {
+              scores(0);
+              ++n_k;
+            }
+            if (i > 0) product(0, n_p++, i > 1);
+          }
+        } else {
+          scores(0);
+          scores(1);
+          ++n_k;
+          for (int i = 0; i < nb && !stopped(); ++i) {
+            product(0, n_p, i > 0);
+            ++n_p;
+            if (i + 1 < nb) scores(0);
+            product(1, n_p - 1, i > 0);
+            if (i + 1 < nb) {
+              scores(1);
+              ++n_k;
+            }
+          }
+        }
+        if (stopped()) break;
       }
+      if (leader) commit(su32(&drained));  // nothing is under way when TMEM goes back
       __syncwarp();
-    };
-    auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
-    while (next_unit<D>(walk, a, r, tok, u)) {
-      wait_all(&q_full, n_u++, s_stop);
-      const int nb = u.blk1 - u.blk0;
-      if constexpr (NT == 1) {
-        for (int i = 0; i <= nb && !stopped(); ++i) {
-          if (i < nb) {
-            scores(0);
-            ++n_k;
-          }
-          if (i > 0) product(0, n_p++, i > 1);
-        }
-      } else {
-        scores(0);
-        scores(1);
-        ++n_k;
-        for (int i = 0; i < nb && !stopped(); ++i) {
-          product(0, n_p, i > 0);
-          ++n_p;
-          if (i + 1 < nb) scores(0);
-          product(1, n_p - 1, i > 0);
-          if (i + 1 < nb) {
-            scores(1);
-            ++n_k;
-          }
-        }
-      }
-      if (stopped()) break;
-    }
-    if (leader) commit(su32(&drained));  // nothing is under way when TMEM goes back
-    __syncwarp();
-    if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
+      if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
     }
   }
   tc_before();
