@@ -667,7 +667,9 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
  * Scores, maxima, sums and accumulators are fp32; the weights enter the second
  * product in fp16.  Results do not depend on the order in which the GPU runs
  * its blocks.  Cache entries that no token sees (the rest of a last block,
- * free blocks) may hold anything, NaN included.
+ * free blocks) may hold anything, NaN included; a NaN or an infinity among the
+ * values that one of a row's new tokens sees may reach the results of the row's
+ * other new tokens in the same call, but of no other row.
  * A row whose bounds are not consistent (n < 0, n > max_new, n > kv_len,
  * kv_len beyond the block table, q_start outside 0..T) is skipped, and keys in
  * a block whose id lies outside the pool are left out, with MOE_DERR_KV_INDEX

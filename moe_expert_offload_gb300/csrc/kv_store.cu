@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(128) store_kernel(StoreArgs a, int parts) {
   griddep_wait();
   if (t >= a.T) return;
   const int slot = a.slot[t];
-  if (slot < 0) return;  // padding
-  if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
+  if (slot == -1) return;  // padding
+  if ((unsigned)slot >= (unsigned)(a.kv.num_blocks * a.kv.block_tokens)) {
     if (lane == 0) atomicOr(a.err, MOE_DERR_KV_INDEX);
     return;
   }
@@ -295,8 +295,8 @@ __global__ void __launch_bounds__(256) load_kernel(LoadArgs a) {
   if (row >= (int64_t)a.T * K) return;
   const int t = (int)(row / K), h = (int)(row - (int64_t)t * K);
   const int slot = a.slot[t];
-  if (slot < 0) return;
-  if (slot >= a.kv.num_blocks * a.kv.block_tokens) {
+  if (slot == -1) return;
+  if ((unsigned)slot >= (unsigned)(a.kv.num_blocks * a.kv.block_tokens)) {
     if (sub == 0 && a.err) atomicOr(a.err, MOE_DERR_KV_INDEX);
     return;
   }

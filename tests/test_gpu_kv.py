@@ -252,6 +252,21 @@ def test_store_skips_padding_and_flags_bad_tokens():
     assert torch.all(k2[1:3] == 9.0) and torch.equal(k2[3], k2[0]) and not torch.any(k2[4:] == 9.0)
 
 
+@pytest.mark.parametrize("slot", [-2, -64, -2 ** 31])
+def test_store_and_load_flag_slots_below_the_pool(slot):
+    c = _store_case(3, 4, 2, 128, 16, 64, False, 1, (1, 1), 6)
+    c["batch"].slot[1] = slot
+    q_out = _run_store(c)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    assert torch.all(q_out[1] == 7.0) and not torch.any(q_out[[0, 2]] == 7.0)
+    k = torch.full((3, 2, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    c["batch"].err.zero_()
+    m.moe_kv_load(c["kv"].c, c["batch"].slot, 3, k, v, c["batch"].err)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    assert torch.all(k[1] == 9.0) and not torch.any(k[[0, 2]] == 9.0)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_store_of_unusual_values(D):
     """Constant groups, zeros, subnormals, infinities, NaN, and values past the clamp."""
@@ -577,6 +592,23 @@ def test_attention_flags_rows_past_max_new(max_new):
             assert torch.all(out[start:start + n] == 5.0)
         start += n
     _check_attend(c, out, rows=[b for b, n in enumerate(news) if n <= max_new])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D,news", [(64, [1, 1, 2]), (128, [1, 200, 100]), (256, [1, 3, 100])])
+def test_attention_of_broken_values_stays_in_its_row(D, news, bad):
+    """A value's scale that is NaN or infinite spoils the row that holds it and no other."""
+    c = _attend_case(16, 2, D, 4, [250, 300, 120], news, 29)
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16)  # [tile][part][...]
+    G = D // 64
+    block = int(c["table"][0, 3])  # row 0's tokens 48 .. 63, kv head 1
+    meta[block * 2 + 1, 2 * 16 * G + 5] = bad  # V scale of group 0, token 53
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_attend(c, out, rows=[1, 2])
+    heads = out[:news[0]].float()
+    assert not torch.isfinite(heads[:, 4:, :64]).all()
+    assert torch.isfinite(heads[:, :4]).all()
 
 
 @pytest.mark.parametrize("news", [[1, 1], [4, 120]])
