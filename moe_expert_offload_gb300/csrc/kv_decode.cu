@@ -39,7 +39,7 @@
 // 4.4 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 112 us, 5.3 TB/s.
 // The stream alone takes 54.7 and 88 us; the rest is instruction issue, 316 and
 // 400 per tile, most of them unpacking codes.  Few keys are latency: 1000 keys of
-// one row 11.7 us, 2.2 of them the scan over the rows and 2.5 the combine kernel.
+// one row 11.5 us, 1.8 of them the scan over the rows and 2.5 the combine kernel.
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -225,19 +225,49 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
   float* cta_part = cta_parts(a.ws);
   float* warp_part = cta_part + (size_t)kGrid * 2 * C::kPartial;
   if (tid < W * S) bar_init(su32(&full[0][0] + tid), 1);
-  if (tid < W) {
-    s_row[tid] = -1;
-    s_part[tid][0].unit = s_part[tid][1].unit = -1;
+  if (lane == 0) {
+    s_row[wid] = -1;
+    s_part[wid][0].unit = s_part[wid][1].unit = -1;
   }
+  __syncwarp();
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   griddep_wait();
 
   // ------------------------------------------------------------- the shares
-  // cost of the rows before each row; chunks of kThreads rows, twice over when
-  // there is more than one (the total comes first)
+  // cost of the rows before each row
   long long total = 0, share = 0;
   const int chunks = (a.rows + C::kThreads - 1) / C::kThreads;
-  for (int pass = chunks > 1 ? 0 : 1; pass < 2; ++pass) {
+  auto share_of = [&] {
+    return max((total + (long long)kGrid * W - 1) / ((long long)kGrid * W), (long long)TS);
+  };
+  if (a.rows <= 32) {
+    // up to 32 rows: every warp for itself, a lane per row (1000 keys of one row: 11.4 us, 11.8
+    // the other way)
+    RowInfo i = {};
+    if (lane < a.rows) i = row_info(a, lane, r, C::kCols, blockIdx.x == 0 && wid == 0);
+    const long long cost = (long long)K * i.ntb * (i.tiles + C0);
+    if (wid == 0) {
+      s_rows[0][lane] = i.start;
+      s_rows[1][lane] = i.ntb ? i.n : 0;
+      s_rows[2][lane] = i.len;
+    }
+    long long v = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += u;
+    }
+    total = __shfl_sync(~0u, v, 31);
+    share = share_of();
+    const long long x0 = ((long long)blockIdx.x * W + wid) * share;
+    if (x0 < v && x0 >= v - cost) {
+      s_row[wid] = lane;
+      s_x[wid] = x0 - (v - cost);
+    }
+    __syncthreads();
+  }
+  // more: chunks of kThreads rows, twice over when there is more than one (the total comes first)
+  for (int pass = a.rows <= 32 ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
     long long carry = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c * C::kThreads + tid;
@@ -267,10 +297,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
       }
       if (pass == 0 || chunks == 1) total = carry + sum;
       if (pass == 1) {
-        if (c == 0) {
-          share = (total + (long long)kGrid * W - 1) / ((long long)kGrid * W);
-          if (share < TS) share = TS;
-        }
+        if (c == 0) share = share_of();
         const long long pre = before + v - cost;
         s_pre[tid] = pre;
         __syncthreads();

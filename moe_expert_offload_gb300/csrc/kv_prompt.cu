@@ -32,7 +32,7 @@
 // weights may pass fp16's range (a score 2^3 to 2^9 above it), so the accumulator in
 // TMEM is rarely rescaled.
 //
-// Measured: 8192 tokens, 16 query heads on 2 of 256: 515 us, 1068 TFLOP/s (55% of a
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 507 us, 1084 TFLOP/s (56% of a
 // large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 788 us,
 // 1320 TFLOP/s (68%).  Bound by the chain of a block: at head_dim 64 and 128 scores,
 // TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
@@ -397,12 +397,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     s_stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  __syncwarp();
   griddep_wait();
 
   // ------------------------------------------------------- this CTA's share
   long long total = 0;
+  auto share_of = [&] { return max((total + kGrid - 1) / kGrid, 2ll * kKeys); };
+  if (a.rows <= 32) {
+    // every warp for itself, a lane per row (7 short prompts: 48.8 us, 52.0 the other way)
+    long long cost = 0;
+    if (lane < a.rows) {
+      const Row i = row_info(a, lane, r, tok);
+      if (i.tiles) cost = K * cost_before<D>(i, tok, i.tiles);
+    }
+    long long v = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(~0u, v, o);
+      if (lane >= o) v += u;
+    }
+    total = __shfl_sync(~0u, v, 31);
+    const long long share = share_of(), x0 = blockIdx.x * share;
+    if (wid == 0 && x0 < v && x0 >= v - cost) {
+      s_row = lane;
+      s_at = x0 - (v - cost);
+    }
+    if (tid == 0) s_share = share;
+  }
   const int chunks = (a.rows + kThreads - 1) / kThreads;
-  for (int pass = 0; pass < 2; ++pass) {
+  // more: chunks of kThreads rows, twice over when there is more than one (the total comes first)
+  for (int pass = a.rows <= 32 ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
     long long carry = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
@@ -425,10 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         if (i < wid) before += s_scan[i];
         sum += s_scan[i];
       }
-      if (pass == 0) {
-        total = carry + sum;
-      } else {
-        const long long share = max((total + kGrid - 1) / kGrid, 2ll * kKeys);
+      if (pass == 0 || chunks == 1) total = carry + sum;
+      if (pass == 1) {
+        const long long share = share_of();
         const long long pre = before + v - cost, x0 = blockIdx.x * share;
         if (x0 < total && x0 >= pre && x0 < pre + cost) {
           s_row = b;

@@ -571,6 +571,22 @@ def test_attention_of_many_rows():
     _check_attend(c, out)
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 200, 300, 600])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_of_row_counts(B, D):
+    """Around the row counts where the shares are found in another way: decode rows, idle ones and
+    prompts among them, the last row a prompt."""
+    rng = np.random.default_rng(B + D)
+    lens = rng.integers(0, 90, B)
+    news = np.minimum(lens, rng.integers(0, 3, B))
+    lens[B // 2], news[B // 2] = 400, 130
+    lens[B - 1], news[B - 1] = 140, 140
+    c = _attend_case(16, 1, D, 4, lens.tolist(), news.tolist(), 70 + B, poison=True)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_attend(c, out)
+
+
 def test_attention_without_work():
     c = _attend_case(16, 2, 128, 4, [30, 0, 9], [1, 0, 1], 25)
     c["batch"].q_start.zero_()
