@@ -39,7 +39,7 @@
 // 4.4 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 112 us, 5.3 TB/s.
 // The stream alone takes 54.7 and 88 us; the rest is instruction issue, 316 and
 // 400 per tile, most of them unpacking codes.  Few keys are latency: 1000 keys of
-// one row 11.5 us, 1.8 of them the scan over the rows and 2.5 the combine kernel.
+// one row 11.5 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
 #include <type_traits>
 
 #include "kv_common.cuh"
