@@ -67,9 +67,10 @@ struct Cfg {
   static constexpr int kTiles = D == 256 ? 1 : 2;   // query tiles of a unit
   static constexpr int kStages = D == 256 ? 1 : 2;  // key and value blocks held
   static constexpr int kRows = 128 * kTiles;
-  // a unit's fixed cost, in keys: queries in, results out (8192 tokens, head_dim 256: 576, 516, 523
-  // and 539 us at 384, 512, 640 and 1024; shorter rows and head_dim 128 do not care)
-  static constexpr int kUnitKeys = D == 256 ? 512 : 384;
+  // a unit's fixed cost, in keys: queries in, results out (two rows of 1700 to 5000 new tokens,
+  // us at 384, 512, 768 and 1024: head_dim 64 155, 148, 151, 153; 128 317, 293, 272, 280;
+  // 256, 16 heads on 2, from 512 on 278, 285, 296)
+  static constexpr int kUnitKeys = D == 128 ? 768 : 512;
   static constexpr int kBlockBytes = kKeys * D * 2;  // one block of keys (or values, or queries)
   // results on their way out: each softmax warp's 32 rows of 64 bytes, 80 apart
   static constexpr int kOutBytes = kSoftWarps * 32 * 80;
