@@ -39,7 +39,7 @@
 // 4.4 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 112 us, 5.3 TB/s.
 // The stream alone takes 54.7 and 88 us; the rest is instruction issue, 316 and
 // 400 per tile, most of them unpacking codes.  Few keys are latency: 1000 keys of
-// one row 11.5 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
+// one row 11.3 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -68,7 +68,9 @@ struct Cfg {
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kCols = 8;
   static constexpr int kPartial = kCols * (D + 2);  // floats: o [col][D], m [col], l [col]
-  static constexpr int kUnitCost = 512 / D;  // a unit's fixed cost, in key tiles
+  // a unit's fixed cost, in key tiles (100 rows of up to 1000 keys, us at half of it, at it and at
+  // twice: head_dim 64 16.9, 16.5, 16.5; 128 30.8, 29.0, 29.0; 256 25.2, 22.3, 22.9)
+  static constexpr int kUnitCost = D == 64 ? 8 : 4;
   static constexpr int kCentre = 16 / kTiles;       // stages between two moves of the mean
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + 128;
   static_assert(kPartial * 4 <= kStages * kStageBytes, "a partial fits its warp's ring");

@@ -32,9 +32,9 @@
 // weights may pass fp16's range (a score 2^3 to 2^9 above it), so the accumulator in
 // TMEM is rarely rescaled.
 //
-// Measured: 8192 tokens, 16 query heads on 2 of 256: 507 us, 1084 TFLOP/s (56% of a
-// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 788 us,
-// 1320 TFLOP/s (68%).  Bound by the chain of a block: at head_dim 64 and 128 scores,
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 508 us, 1082 TFLOP/s (56% of a
+// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 790 us,
+// 1316 TFLOP/s (68%).  Bound by the chain of a block: at head_dim 64 and 128 scores,
 // TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
 // takes all the shared memory there is, values freed, dequantised (1400 cycles),
 // fenced (570), seen by the issuer (350) and multiplied (1500).  The tensor pipe is
