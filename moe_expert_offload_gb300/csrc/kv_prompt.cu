@@ -60,7 +60,10 @@ constexpr int kKeys = 128;  // keys of a block
 constexpr int kSoftWarps = 8, kSideWarps = 8, kMmaWarp = 24;
 constexpr int kThreads = 28 * 32;  // seven warp groups; three warps of the last one idle
 constexpr int kStartRegs = 72;
-constexpr float kNone = -1e30f;
+constexpr float kNone = -1e30f;  // below every raw score (q and k in fp16's range: 2^38 at most)
+// Scores this far from zero (in log2) have their reference taken off before they are scaled: the
+// offset of the fused form is rounded by up to 2^-24 of itself, 2^-11 here.
+constexpr float kFar = 8192.0f;
 
 template <int D>
 struct Cfg {
@@ -75,7 +78,7 @@ struct Cfg {
   // results on their way out: each softmax warp's 32 rows of 64 bytes, 80 apart
   static constexpr int kOutBytes = kSoftWarps * 32 * 80;
   static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes + kOutBytes;
-  static constexpr int kPartial = kRows * (D + 2);  // floats: o [row][D], m [row], l [row]
+  static constexpr int kPartial = kRows * (D + 3);  // floats: o [row][D], top, l, fac [row]
   static constexpr uint32_t kIdescS = (1u << 4) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
                                       ((128u >> 4) << 24);  // bit 16: B is MN-major
@@ -572,7 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       const bool live = row < per_tile * r && t < ri.n;
       const int lim = ri.len - ri.n + min(t, ri.n - 1);             // last key that the row sees
       const int open = ri.len - ri.n + u.tok0 + tile * per_tile;   // all rows see the keys up to it
-      float m = kNone, l = 0.0f;
+      // the row's reference, a raw score; a score x weighs 2^(x fac + off), off = 7 - top fac
+      float top = kNone, off, l = 0.0f;
+      auto set_off = [&] { off = fminf(fmaf(-top, fac, 7.0f), 3e38f); };
+      set_off();
       // the tiles of a block that are missing (a block id outside the pool), looked up a block ahead
       auto block_of = [&](int i) {
         const int at = i * (kKeys / kTile) + lane;
@@ -601,13 +607,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         // The weights relative to the maximum so far, 2^7 above it.  While a part's sum is below
         // 2^16 each of them fits fp16; where it is not, some weight of the 64 passes the maximum's
         // by 2^3 or more: the maximum follows, what there is is scaled and the weights are formed
-        // again.
+        // again, now from each score's distance to the maximum: of any finite scores none weighs
+        // more than 2^7 then.  (x fac + off of the maximum itself is as far from 7 as the two
+        // roundings of top fac: for top fac past 2^27 that may pass fp16's range, or lose all.)
         float2 sum;
-        auto weights = [&](const uint32_t* v, uint32_t* p) {
-          const float off = 7.0f - m;
+        auto weights = [&](auto apart_tag, const uint32_t* v, uint32_t* p) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            float2 x = fma2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]), fac, off);
+            float2 x = make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+            if constexpr (decltype(apart_tag)::value) {
+              x = add2(x, make_float2(-top, -top));
+              x = fma2(x.x, x.y, fac, 7.0f);
+            } else {
+              x = fma2(x.x, x.y, fac, off);
+            }
             x.x = ex2(x.x);
             x.y = ex2(x.y);
             sum = add2(sum, x);
@@ -615,9 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           }
         };
         constexpr float kMost = 65504.0f;
-        auto refer = [&](float top) {
-          const float f = ex2(m - fmaxf(m, top));
-          m = fmaxf(m, top);
+        using Fused = std::false_type;
+        using Apart = std::true_type;
+        auto too_far = [&] { return l > 0.0f && fabsf(off) > kFar; };
+        auto refer = [&](float seen) {  // the largest score there is here
+          const float to = fmaxf(top, seen), f = ex2((top - to) * fac);
+          top = to;
+          set_off();
           l *= f;
           if (i > u.blk0 && __any_sync(~0u, f != 1.0f)) {
             wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
@@ -638,29 +655,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         };
         if constexpr (NT == 1) {
           uint32_t p[32];
-          auto attempt = [&](bool follow) {
+          auto attempt = [&](auto apart_tag) {
             uint32_t v[64];
             tm_ld32(s_tm + wg * 64, v);
             tm_ld32(s_tm + wg * 64 + 32, v + 32);
             tm_wait_regs(v);
 #pragma unroll
             for (int c = 0; c < 4; ++c) hide(v + 16 * c, wg * 4 + c);
-            if (follow) {
-              float top = kNone;
+            if constexpr (decltype(apart_tag)::value) {
+              float seen = kNone;
 #pragma unroll
-              for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(v[k]));
-              s_max[wg][row] = top;
+              for (int k = 0; k < 64; ++k) seen = fmaxf(seen, __uint_as_float(v[k]));
+              s_max[wg][row] = seen;
               asm volatile("bar.sync 1, 256;" ::: "memory");
-              refer(fmaxf(top, s_max[wg ^ 1][row]) * fac);
+              refer(fmaxf(seen, s_max[wg ^ 1][row]));
             }
             sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) weights(v + 16 * c, p + 8 * c);
+            for (int c = 0; c < 4; ++c) weights(apart_tag, v + 16 * c, p + 8 * c);
           };
-          attempt(i == u.blk0);
-          // both halves of the rows agree (and every score has been read by then: the weights
-          // may go over the scores)
-          while (any_of_256(sum.x + sum.y > kMost)) attempt(true);
+          // Both halves of the rows agree on whether the reference follows, which it does once at
+          // most.  Every score has been read by the barrier on the way: the weights may go over
+          // the scores.
+          bool follow = i == u.blk0;
+          if (!follow) {
+            attempt(Fused{});
+            follow = any_of_256(sum.x + sum.y > kMost || too_far());
+          }
+          if (follow) attempt(Apart{});
           l += sum.x + sum.y;
           tm_st16(s_tm + wg * 32, p);
           tm_st16(s_tm + wg * 32 + 16, p + 16);
@@ -677,14 +699,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             for (int q = 0; q < 4; ++q) hide(x + 16 * q, 4 * c + q);
             sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) weights(x + 16 * q, p + 8 * q);
+            for (int q = 0; q < 4; ++q) weights(Fused{}, x + 16 * q, p + 8 * q);
             if (__any_sync(~0u, sum.x + sum.y > kMost)) {
-              const float before = m;
-              float top = kNone;
+              const float before = top;
+              float seen = kNone;
 #pragma unroll
-              for (int k = 0; k < 64; ++k) top = fmaxf(top, __uint_as_float(x[k]));
-              refer(top * fac);
-              const float f = ex2(before - m);
+              for (int k = 0; k < 64; ++k) seen = fmaxf(seen, __uint_as_float(x[k]));
+              refer(seen);
+              const float f = ex2((before - top) * fac);
               const uint32_t ff = pack_h2(f, f);
               for (int k = 0; k < 2 * c; ++k) {
                 uint32_t old[16];
@@ -697,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
               }
               sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) weights(x + 16 * q, p + 8 * q);
+              for (int q = 0; q < 4; ++q) weights(Fused{}, x + 16 * q, p + 8 * q);
             }
             l += sum.x + sum.y;
             tm_st16(s_tm + c * 32, p);
@@ -786,8 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         }
       }
       if (!whole && (NT == 2 || wg == 0)) {
-        part[(size_t)C::kRows * D + pr] = m;
+        part[(size_t)C::kRows * D + pr] = top;
         part[(size_t)C::kRows * (D + 1) + pr] = l;
+        part[(size_t)C::kRows * (D + 2) + pr] = fac;
       }
       if (done.blk0 == 0 && !whole && tid == 0)  // begun here; it goes on at the next share's start
         cuts[blockIdx.x] = Cut{(int)(blockIdx.x + (done.rest + s_share - 1) / s_share), ri.start, ri.n,
@@ -977,14 +1000,15 @@ __global__ void __launch_bounds__(512) combine_kernel(AttnArgs a) {
   const int t = cut.tok0 + (row >> 7) * per_tile + in / r;
   if (in >= per_tile * r || t >= cut.n) return;
   const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kCutBytes);
-  float m = kNone, l = 0.0f;
+  float m = kNone, l = 0.0f;  // (raw scores, as the parts have them)
+  const float fac = parts[((size_t)first * 2 + 1) * C::kPartial + (size_t)C::kRows * (D + 2) + row];
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int k = first; k <= cut.last; ++k) {
     const float* src = parts + ((size_t)k * 2 + (k == first)) * C::kPartial;
     const float mk = src[(size_t)C::kRows * D + row], lk = src[(size_t)C::kRows * (D + 1) + row];
     const float4 v = *reinterpret_cast<const float4*>(src + (size_t)row * D + c);
-    const float mm = fmaxf(m, mk), f = ex2(m - mm), h = ex2(mk - mm);
+    const float mm = fmaxf(m, mk), f = ex2((m - mm) * fac), h = ex2((mk - mm) * fac);
     m = mm;
     l = l * f + lk * h;
     y.x = y.x * f + v.x * h;

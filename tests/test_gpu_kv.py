@@ -484,6 +484,55 @@ def test_attention_of_extreme_scores(D, news):
         start += n
 
 
+FAR = [(256, [130, 260, 33])]  # head_dim, new tokens
+
+
+@pytest.mark.parametrize("size", [1e2, 1e4, 3e6, 1e9, 1e12, 1e30])
+@pytest.mark.parametrize("below", [False, True])
+@pytest.mark.parametrize("D,news", FAR)
+def test_attention_of_far_scores(D, news, below, size):
+    """Scores up to 2^100 from zero, on both sides or all below it: the result is the top key's
+    value wherever no other key comes near.
+
+    How near: a key may be formed in fp16 (2^-11 of scale * code and of the bias, and of their
+    sum) and D products are summed in fp32 (2^-24 of them per addition), so a score is off by at
+    most 2^-9 of the sum of its products' sizes.  Where two scores keep 2^-8 of it and 40 (of
+    log2) apart, the others' weights are below L 2^-40 in all.  What is left is a value formed in
+    fp16 (once, on terms of up to twice its group's largest), its weight and its product with a
+    scale (2^-11 each), and the result's rounding to bf16."""
+    lens, P, r = [500, 260, 33], 32, 8
+    c = _attend_case(P, 1, D, r, lens, news, 31)
+    q = c["q"].float() * size
+    if below:  # keys about 6 above zero, queries below it
+        meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16).view(-1, 4, D // 4)
+        meta[:, 1] += 6
+        q = -q.abs()
+    q = q.bfloat16()
+    out = _run_attend(c, q=q)
+    assert int(c["batch"].err[0]) == 0
+    got, pool, start, checked = _f64(out), _np(c["kv"].pool), 0, 0
+    assert np.all(np.isfinite(got[:sum(news)]))
+    for b, (L, n) in enumerate(zip(lens, news)):
+        j = np.arange(L)
+        k, v = (x[:, 0] for x in ref.read_slots(pool, c["table"][b, j // P] * P + j % P, 1, P, D))
+        qq = _f64(q)[start:start + n]
+        seen = (j[None] <= L - n + np.arange(n)[:, None])[:, None]  # [n, 1, L]
+        x = np.where(seen, qq @ k.T, -np.inf) * (c["scale"] * np.log2(np.e))
+        reach = np.where(seen, np.abs(qq) @ np.abs(k).T, 0).max(-1) * (c["scale"] * 1.5)
+        order = np.sort(x, -1)
+        clear = order[..., -1] - (order[..., -2] if L > 1 else -np.inf) > reach * 2.0 ** -8 + 40
+        clear |= seen.sum(-1) == 1
+        want = v[x.argmax(-1)]
+        big = np.abs(v).max(0).reshape(-1, 64).max(-1).repeat(64)
+        tol = np.abs(want) * 2.0 ** -8 + 2 * big * 3 * 2.0 ** -11
+        off = np.abs(got[start:start + n] - want)
+        assert np.all((off <= tol)[clear]), (b, float((off - tol)[clear].max()))
+        checked += int(clear.sum())
+        start += n
+    if size >= 1e4 and not below:
+        assert checked > sum(news) * r // 2
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("news", [[1, 1], [1, 150]])
 def test_attention_of_values_of_all_sizes(D, news):
