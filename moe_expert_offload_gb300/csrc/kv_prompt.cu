@@ -64,6 +64,7 @@ constexpr float kNone = -1e30f;  // below every raw score (q and k in fp16's ran
 // Scores this far from zero (in log2) have their reference taken off before they are scaled: the
 // offset of the fused form is rounded by up to 2^-24 of itself, 2^-11 here.
 constexpr float kFar = 8192.0f;
+constexpr float kMost = 65504.0f;  // fp16's largest
 
 template <int D>
 struct Cfg {
@@ -575,9 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       const bool live = row < per_tile * r && t < ri.n;
       const int lim = ri.len - ri.n + min(t, ri.n - 1);             // last key that the row sees
       const int open = ri.len - ri.n + u.tok0 + tile * per_tile;   // all rows see the keys up to it
-      // the row's reference, a raw score; a score x weighs 2^(x fac + off), off = 7 - top fac
+      // The row's reference, a raw score; a score x weighs 2^(x fac + off), off = 7 - top fac.
+      // Where that is far from zero every visible score shall weigh too much (an infinite query's
+      // row is lost anyway, and the others' references shall not follow for it).
       float top = kNone, off, l = 0.0f;
-      auto set_off = [&] { off = fminf(fmaf(-top, fac, 7.0f), 3e38f); };
+      auto set_off = [&] {
+        off = fmaf(-top, fac, 7.0f);
+        if (fabsf(off) > kFar && top < -kNone) off = 3e38f;
+      };
       set_off();
       // the tiles of a block that are missing (a block id outside the pool), looked up a block ahead
       auto block_of = [&](int i) {
@@ -627,10 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             p[k] = pack_h2(x.x, x.y);
           }
         };
-        constexpr float kMost = 65504.0f;
         using Fused = std::false_type;
         using Apart = std::true_type;
-        auto too_far = [&] { return l > 0.0f && fabsf(off) > kFar; };
         auto refer = [&](float seen) {  // the largest score there is here
           const float to = fmaxf(top, seen), f = ex2((top - to) * fac);
           top = to;
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           bool follow = i == u.blk0;
           if (!follow) {
             attempt(Fused{});
-            follow = any_of_256(sum.x + sum.y > kMost || too_far());
+            follow = any_of_256(sum.x + sum.y > kMost);
           }
           if (follow) attempt(Apart{});
           l += sum.x + sum.y;
@@ -719,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
               }
               sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) weights(Fused{}, x + 16 * q, p + 8 * q);
+              for (int q = 0; q < 4; ++q) weights(Apart{}, x + 16 * q, p + 8 * q);
             }
             l += sum.x + sum.y;
             tm_st16(s_tm + c * 32, p);
