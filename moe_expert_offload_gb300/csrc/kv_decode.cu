@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int kStages = 3;
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kCols = 8;
-  static constexpr int kPartial = kCols * (D + 2);  // floats: o [col][D], m [col], l [col]
+  static constexpr int kPartial = kCols * (D + 3);  // floats: o [col][D], m, l, fac [col]
   // a unit's fixed cost, in key tiles (100 rows of up to 1000 keys, us at half of it, at it and at
   // twice: head_dim 64 16.9, 16.5, 16.5; 128 30.8, 29.0, 29.0; 256 25.2, 22.3, 22.9)
   static constexpr int kUnitCost = D == 64 ? 8 : 4;
@@ -75,7 +75,8 @@ struct Cfg {
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + 128;
   static_assert(kPartial * 4 <= kStages * kStageBytes, "a partial fits its warp's ring");
 };
-constexpr float kNone = -1e30f;  // a maximum before the first key: finite, so that it subtracts
+constexpr float kNone = -1e30f;  // a maximum before the first key: finite, so that it subtracts,
+                                 // and below every raw score (2^15 at most)
 
 // workspace: cuts [kGrid] | CTA parts [kGrid][2] | warp parts [kGrid * warps]
 // The unit that a CTA began and did not end: the last CTA with a part of it
@@ -185,6 +186,8 @@ __device__ __forceinline__ void store_row(uint16_t* dst, const float (&y)[D / 32
     *reinterpret_cast<uint32_t*>(dst + lane * 2 + i * 64) = *reinterpret_cast<const uint32_t*>(&v);
   }
 }
+// 2^8 above the reference, rounded down: no weight passes 2^15 before it follows
+__device__ __forceinline__ float reach(float m, float fac) { return __fadd_rd(m, __fdividef(8.0f, fac)); }
 __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
   return __int_as_float((e + 127) << 23);
 }
@@ -412,7 +415,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     bool fill = issued == S;
 
     uint32_t qf[NK][2], qs[2];
-    float fac[2], m[2], o[NK][4], off[G][2], ob[4];
+    // per column: the factor of its scores (to log2), the reference (a raw score), the raw score
+    // from which on the reference follows
+    float fac[2], m[2], high[2], o[NK][4], off[G][2], ob[4];
     int sigma = 0, lim[2], open = 0, len = 0, age = 0, c_base = 0, cols = 0;
     bool first = false;
     const int key_l = ((lane >> 3) & 1) * 8 + (lane & 7), c0 = (lane >> 4) ^ swizzle<D>(key_l);
@@ -498,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
         if (has(tt)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            grow |= fmaf(x[tt][j], fac[j & 1], -m[j & 1]) > 8.0f;
+            grow |= x[tt][j] > high[j & 1];
         }
       uint32_t big = 0;
 #pragma unroll
@@ -529,11 +534,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
 #pragma unroll
           for (int tt = 0; tt < TS; ++tt)
             if (has(tt))
-              top = fmaxf(top, fmaxf(x[tt][i] * fac[i], x[tt][2 + i] * fac[i]));
+              top = fmaxf(top, fmaxf(x[tt][i], x[tt][2 + i]));
 #pragma unroll
           for (int sh = 4; sh < 32; sh <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, sh));
-          f[i] = exp2_fast(m[i] - top);
+          f[i] = exp2_fast((m[i] - top) * fac[i]);
           m[i] = top;
+          high[i] = reach(m[i], fac[i]);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -554,10 +560,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
       for (int tt = 0; tt < TS; ++tt) {
         if (has(tt)) {
           const uint32_t base = st + tt * tile_bytes(D), meta = base + 16 * D;
+          // (The reference is taken off before the scaling: the largest weight is 2^7 however
+          // large the scores are.  Of scaled scores past 2^27 the roundings alone could take it out
+          // of fp16's range.)
           float p[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            p[j] = exp2_fast(fmaf(x[tt][j], fac[j & 1], 7.0f - m[j & 1]));
+            p[j] = exp2_fast(fmaf(x[tt][j] - m[j & 1], fac[j & 1], 7.0f));
           const uint32_t p0 = transpose8(pack_h2(p[0], p[1])), p1 = transpose8(pack_h2(p[2], p[3]));
           const uint32_t ps0 = hmul2(p0, s_one), ps1 = hmul2(p1, s_one);
           uint32_t live0 = ~0u, live1 = ~0u;
@@ -683,6 +692,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
           // the last key that the column's token sees
           lim[i] = len - n + min(cc, cols - 1) / r;
           m[i] = kNone;
+          high[i] = reach(m[i], fac[i]);
 #pragma unroll
           for (int grp = 0; grp < G; ++grp) off[grp][i] = 0.0f;
         }
@@ -758,6 +768,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
         for (int i = 0; i < 2; ++i) {
           part[C::kCols * D + 2 * t + i] = m[i];
           part[C::kCols * (D + 1) + 2 * t + i] = l[i];
+          part[C::kCols * (D + 2) + 2 * t + i] = fac[i];
         }
       }
     }
@@ -798,24 +809,26 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     float* dst = cta_part + ((size_t)blockIdx.x * 2 + (closed || !begun ? 0 : 1)) * C::kPartial;
     for (; task < C::kCols; task += W) {
       const int cc = task;
-      // lane w: warp w's maximum, weight and sum
-      float mk = kNone, lk = 0.0f;
+      // lane w: warp w's maximum, sum and (one of the column's) factor
+      float mk = kNone, lk = 0.0f, fac = 0.0f;
       if (lane >= w0 && lane <= w1) {
         const float* src = closed && lane == to
                                ? head_part
                                : reinterpret_cast<const float*>(rings + lane * C::kWarpBytes);
         mk = src[C::kCols * D + cc];
         lk = src[C::kCols * (D + 1) + cc];
+        fac = src[C::kCols * (D + 2) + cc];
       }
       float mm = mk;
 #pragma unroll
       for (int o = 8; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-      const float fk = exp2_fast(mk - mm);
+      const float fk = exp2_fast((mk - mm) * fac);
       lk *= fk;
 #pragma unroll
       for (int o = 8; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
       mm = __shfl_sync(~0u, mm, 0);
       lk = __shfl_sync(~0u, lk, 0);
+      fac = __shfl_sync(~0u, fac, w1);
       float y[D / 32] = {};
       auto add = [&](const float* src, float f) {
 #pragma unroll
@@ -842,6 +855,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
         if (lane == 0) {
           dst[C::kCols * D + cc] = mm;
           dst[C::kCols * (D + 1) + cc] = lk;
+          dst[C::kCols * (D + 2) + cc] = fac;
         }
       }
     }
@@ -872,6 +886,7 @@ __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
   const Cut cut = static_cast<const Cut*>(a.ws)[first];
   if (cut.last <= first) return;
   const float* cta_part = cta_parts(a.ws);
+  const float fac = cta_part[((size_t)first * 2 + 1) * C::kPartial + C::kCols * (D + 2) + cc];
   float m = kNone, l = 0.0f, y[D / 32] = {};
   for (int k0 = first + split; k0 <= cut.last; k0 += kSplit * 32) {
     // lane i: part k0 + i * kSplit
@@ -885,7 +900,7 @@ __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
     float mm = fmaxf(mk, m);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    const float fk = exp2_fast(mk - mm), f0 = exp2_fast(m - mm);
+    const float fk = exp2_fast((mk - mm) * fac), f0 = exp2_fast((m - mm) * fac);
     lk *= fk;
 #pragma unroll
     for (int o = 16; o; o >>= 1) lk += __shfl_xor_sync(~0u, lk, o);
@@ -921,13 +936,13 @@ __global__ void __launch_bounds__(1024) combine_kernel(AttnArgs a) {
   float mm = kNone;
 #pragma unroll
   for (int k = 0; k < kSplit; ++k) mm = fmaxf(mm, s_m[k][cc]);
-  const float f0 = exp2f(m - mm);
+  const float f0 = exp2f((m - mm) * fac);
   l *= f0;
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) y[i] *= f0;
 #pragma unroll
   for (int k = 1; k < kSplit; ++k) {
-    const float f = exp2f(s_m[k][cc] - mm);
+    const float f = exp2f((s_m[k][cc] - mm) * fac);
     l = fmaf(f, s_l[k][cc], l);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {

@@ -484,7 +484,7 @@ def test_attention_of_extreme_scores(D, news):
         start += n
 
 
-FAR = [(D, [130, 260, 33]) for D in (256, 128, 64)]  # head_dim, new tokens
+FAR = [(D, n) for D in (256, 128, 64) for n in ([130, 260, 33], [1, 4, 2])]  # head_dim, new tokens
 
 
 @pytest.mark.parametrize("size", [1e2, 1e4, 3e6, 1e9, 1e12, 1e30])
