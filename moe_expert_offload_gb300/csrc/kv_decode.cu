@@ -26,9 +26,9 @@
 // sums p).  Queries are scaled by a power of two per column into fp16's range
 // (exact but for columns 2^-29 below the largest).  p is rounded to fp16 with
 // its largest value between 2^7 and 2^15, and its product with the values' scale (after a
-// power of two that keeps scales above 1 in range) once more: 2^-11 each against
-// the output's 2^-8; weights below 2^-21 scale of the largest lose that precision
-// to fp16's subnormals.  The maximum that p refers to follows the scores only when they
+// power of two that brings the largest scale to between 2^-3 and 1) once more: 2^-11 each
+// against the output's 2^-8; where both are not the largest, products below 2^-21 of the
+// largest weight lose that precision to fp16's subnormals.  The maximum that p refers to follows the scores only when they
 // pass it by 2^8, so it rarely moves.  Codes are positive and the bias takes
 // their mean back, so the accumulators would grow far past the result and lose
 // it to the MMA's truncating sums (measured at 128k keys: 2.1e-3 from fp64
@@ -146,6 +146,9 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void lds64(uint32_t& x, uint32_t& y, uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(addr) : "memory");
 }
@@ -205,6 +208,7 @@ struct Stage {
   int unit, ntb;
   int start, n, len, pad;
 };
+constexpr int kLeast = -14;  // a unit's first sigma: scales are below 2^sigma
 constexpr uint32_t kBegin = 1u << 8, kEnd = 1u << 9, kLast = 1u << 10;
 
 template <int D>
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     // per column: the factor of its scores (to log2), the reference (a raw score), the raw score
     // from which on the reference follows
     float fac[2], m[2], high[2], o[NK][4], off[G][2], ob[4];
-    int sigma = 0, lim[2], open = 0, len = 0, age = 0, c_base = 0, cols = 0;
+    int sigma = kLeast, lim[2], open = 0, len = 0, age = 0, c_base = 0, cols = 0;
     bool first = false;
     const int key_l = ((lane >> 3) & 1) * 8 + (lane & 7), c0 = (lane >> 4) ^ swizzle<D>(key_l);
     const uint32_t row_off = key_l * (D / 2), c_off = c0 << 4;
@@ -506,26 +510,32 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
             grow |= x[tt][j] > high[j & 1];
         }
       uint32_t big = 0;
+      auto scales = [&](auto&& f) {  // f(address, tile, word in it): the stage's value scales
 #pragma unroll
-      for (int i = 0; i < TS * G * 8; i += 32) {
-        const int word = i + lane, tt = word / (G * 8), in = word % (G * 8);
-        if (tt < TS && has(tt)) {
-          uint32_t v = lds32(st + tt * tile_bytes(D) + 16 * D + 64 * G + in * 4) & 0x7FFF7FFFu;
-          if constexpr (Edge) {
-            const int key = key0 + tt * kTile + (in & 7) * 2;
-            const bool in_tile = (present >> tt) & 1;
-            if (!in_tile || key >= len) v &= 0xFFFF0000u;
-            if (!in_tile || key + 1 >= len) v &= 0x0000FFFFu;
-          }
-          big = __vmaxu2(big, v);
+        for (int i = 0; i < TS * G * 8; i += 32) {
+          const int word = i + lane, tt = word / (G * 8), in = word % (G * 8);
+          if (tt < TS && has(tt)) f(st + tt * tile_bytes(D) + 16 * D + 64 * G + in * 4, tt, in);
         }
-      }
+      };
+      scales([&](uint32_t at, int tt, int in) {
+        uint32_t v = lds32(at) & 0x7FFF7FFFu;
+        if constexpr (Edge) {
+          const int key = key0 + tt * kTile + (in & 7) * 2;
+          const bool in_tile = (present >> tt) & 1;
+          if (!in_tile || key >= len) v &= 0xFFFF0000u;
+          if (!in_tile || key + 1 >= len) v &= 0x0000FFFFu;
+        }
+        big = __vmaxu2(big, v);
+      });
       big = max(big & 0xFFFFu, big >> 16);
       // largest < 2^sigma, or the accumulators' scale moves
       const bool more_scale = (int)(big >> 10) - 14 > sigma;
       if (__any_sync(~0u, grow || more_scale)) {
         big = __reduce_max_sync(~0u, big);
-        const int to = max(sigma, big >= 0x7C00u ? 16 : (int)(big >> 10) - 14);
+        // (below 1 a bit to spare, so that sigma moves less often)
+        int to = big >= 0x7C00u ? 16 : (int)(big >> 10) - 14;
+        to = max(sigma, to < 0 ? to + 1 : to);
+        if (to == -1) to = 0;
         const float turn = pow2(sigma - to);
         float f[2];
 #pragma unroll
@@ -553,7 +563,15 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
           for (int grp = 0; grp < G; ++grp) off[grp][i] *= f[i] * turn;
         sigma = to;
       }
-      const uint32_t s_one = pack_h2(pow2(-sigma), pow2(-sigma));  // keeps p * scale in range
+      // p * scale stays in range: large scales take p down (the scale itself could become
+      // subnormal), small ones are moved up where they lie, exactly
+      if (sigma < 0) {
+        const uint32_t up = pack_h2(pow2(-sigma), pow2(-sigma));
+        scales([&](uint32_t at, int, int) { sts32(at, hmul2(lds32(at), up)); });
+        __syncwarp();
+      }
+      const float down = pow2(-max(sigma, 0));
+      const uint32_t s_one = pack_h2(down, down);
       // ---- weights and the second product
       float bsum[4] = {};
 #pragma unroll
@@ -631,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
         cols = n * r;
         first = d.tile == 0;
         open = len - n + 1;  // keys below are seen by every column
-        sigma = 0;
+        sigma = kLeast;
         age = 0;
         const int c = c_base + g;
         const uint16_t* src = a.q + ((int64_t)(start + c / r) * a.heads + kvh * r + c % r) * D;
@@ -713,6 +731,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
       else
         stage(std::false_type{}, st, key0, cnt, present);
       const int unit = d.unit, ntb = d.ntb, start = d.start, n_new = d.n;
+      if (sigma < 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // scales moved
       __syncwarp();  // every lane has read the stage: its buffer may be filled again
       if (fill) {
         fill = issue(s);

@@ -533,6 +533,52 @@ def test_attention_of_far_scores(D, news, below, size):
         assert checked > sum(news) * r // 2
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-2, 1e-3, 1e-4, 1e-5, "up", "down"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,n", [(256, 1), (100, 4), (16, 130)])
+def test_attention_of_small_values_under_one_large_weight(B, n, D, size):
+    """The first key outweighs each of the others by 2^9 to 2^13, and all of them together do not
+    fall far behind it; values of one size from 1 down to where their scales are subnormal, or of
+    sizes that grow (shrink) along the row.  Rows enough that one warp meets both kinds of keys.
+
+    Scores are exact here (keys are a bias alone; 2^-20 of them for the sums and the factor, on 9
+    at most), so a weight is off by 2^-11 for itself and 2^-11 for its product with a scale, a
+    value formed in fp16 by 2^-11, the fp32 sums by below 2^-11 of the same terms, the score by
+    2^-16; all of them act on scale * code and on the bias.  Below fp16's normal range a product
+    is off by 2^-25, where the largest weight is 2^7 and the largest scale was moved to 2^-3 or
+    more: 2^-29 of the largest weight and scale a key, times a code."""
+    L, K, r = 1000, 8, 4
+    c = _attend_case(16, K, D, r, [L] * B, [n] * B, 33)
+    c["kv"].block_table[:] = c["kv"].block_table[0].clone()  # all rows read one context
+    blocks, G = c["table"][0, :-(-L // 16)], D // 64
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16).view(-1, K, 4, 16 * G)
+    meta[:, :, :2] = 0
+    meta[int(blocks[0]), :, 1, :G] = 13 * np.log(2) / D ** 0.5  # the first key of every head
+    if isinstance(size, str):
+        e = -16 + 24 * torch.arange(len(blocks), device=DEV) / len(blocks)
+        s = torch.exp2(e if size == "up" else e.flip(0))[:, None, None].expand(-1, K, 16 * G)
+    else:
+        s = torch.full((len(blocks), K, 16 * G), size / 7.5, device=DEV)
+    s = s.half()
+    at = torch.tensor(blocks, device=DEV)
+    meta[at, :, 2], meta[at, :, 3] = s, -7 * s
+    q = torch.ones_like(c["q"])
+    for h in range(c["H"]):
+        q[:, h] = (9 + h % r * 4 / 3) / 13
+    out = _run_attend(c, q=q)
+    assert int(c["batch"].err[0]) == 0
+    j = np.arange(L)
+    k, v = ref.read_slots(_np(c["kv"].pool), blocks[j // 16] * 16 + j % 16, K, 16, D)
+    qq = _f64(q)[:n]
+    want = ref.attention(qq, k, v, c["scale"], L - n)
+    step = _f64(s)[j // 16, 0, 0][:, None, None]
+    terms = ref.attention(qq, k, np.abs(v + 7 * step) + 7 * step, c["scale"], L - n)
+    tol = (np.abs(want) * 2.0 ** -8 + terms * (4 * 2.0 ** -11 + 2.0 ** -15)
+           + L * 15 * step.max() * 2.0 ** -29)
+    off = np.abs(_f64(out)[:B * n].reshape(B, n, -1, D) - want)
+    assert np.all(off <= tol), (float((off / tol).max()), float(off.max()))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("news", [[1, 1], [1, 150]])
 def test_attention_of_values_of_all_sizes(D, news):
