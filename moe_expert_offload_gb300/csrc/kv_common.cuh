@@ -41,6 +41,14 @@ __device__ __forceinline__ int swizzle(int r) {
   return D == 256 ? (r & 7) : D == 128 ? ((r >> 1) & 3) : ((r >> 2) & 1);
 }
 
+// scale * unit * 2^e, kept positive and finite: a hidden key's -inf stays one (times 0 it would be
+// NaN), and a score's distance of 0 stays 0.  At either end it makes no difference to the weights:
+// distances of raw scores are 0 or between 2^-80 and 2^40.
+__device__ __forceinline__ float score_factor(float scale, float unit, int e) {
+  const float f = scale * __int_as_float((e + 127) << 23) * unit;
+  return fminf(fmaxf(f, 1e-37f), 3e38f);
+}
+
 // fp16 index (from the tile's 16 D bytes of codes on) of each scale and bias
 template <int D>
 struct Meta {

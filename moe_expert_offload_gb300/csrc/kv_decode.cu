@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
         qs[0] = t == 0 ? pack_h2(hi[0], hi[1]) : t == 1 ? pack_h2(hi[2], hi[3]) : 0u;
         qs[1] = t == 0 ? pack_h2(lo[0], lo[1]) : t == 1 ? pack_h2(lo[2], lo[3]) : 0u;
         // score = fac * accumulated, in units of log2; per C-fragment column 2t, 2t+1
-        const float f = a.scale * 1477.3197218702985f * pow2(e);  // log2(e) 2^24 2^(e-14)
+        const float f = score_factor(a.scale, 1477.3197218702985f, e);  // log2(e) 2^24 2^(e-14)
         fac[0] = __shfl_sync(~0u, f, 8 * t);
         fac[1] = __shfl_sync(~0u, f, 8 * t + 4);
 #pragma unroll

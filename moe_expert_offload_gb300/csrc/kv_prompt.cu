@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
                make_uint4(pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]),
                           pack_h2(x[3], x[7])));
         // score = fac * accumulated, in units of log2
-        if (col8 == 0) s_fac[qr] = a.scale * 8.8054160e-05f * pow2(e);  // log2(e) 2^-14 2^e
+        if (col8 == 0) s_fac[qr] = score_factor(a.scale, 8.8054160e-05f, e);  // log2(e) 2^-14 2^e
       }
       fence_async();
       __syncwarp();

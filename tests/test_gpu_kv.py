@@ -579,6 +579,33 @@ def test_attention_of_small_values_under_one_large_weight(B, n, D, size):
     assert np.all(off <= tol), (float((off / tol).max()), float(off.max()))
 
 
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-20, 1e-12, 1e38])
+@pytest.mark.parametrize("D,news", [(64, [1, 2, 1]), (128, [1, 4, 1]), (256, [1, 2, 1]),
+                                    (64, [140, 260, 33]), (128, [140, 260, 33]), (256, [140, 260, 33])])
+def test_attention_with_scales_at_the_ends(D, news, scale):
+    """A scale that takes the scores to nothing leaves the mean of what a token sees; a zero query
+    has that of any scale, and a large one with a large query no NaN."""
+    c = _attend_case(32, 1, D, 8, [500, 260, 33], news, 34)
+    c["scale"] = scale
+    q = c["q"].clone()
+    q[:, ::2] = 0
+    if scale > 1:
+        q[:, 1::4] = (q[:, 1::4].float() * 1e30).bfloat16()
+    out = _run_attend(c, q=q)
+    assert int(c["batch"].err[0]) == 0
+    got, pool, start = _f64(out)[:sum(news)], _np(c["kv"].pool), 0
+    assert np.all(np.isfinite(got))
+    zero = np.arange(8) % 2 == 0 if scale > 1 else np.ones(8, bool)
+    for b, (L, n) in enumerate(zip(c["lens"], news)):
+        j = np.arange(L)
+        k, v = ref.read_slots(pool, c["table"][b, j // 32] * 32 + j % 32, 1, 32, D)
+        qz = np.zeros((n, 8, D))
+        want = ref.attention(qz, k, v, 1.0, L - n)
+        tol = ref.attention_bound(qz, k, v, 1.0, want)
+        assert np.all((np.abs(got[start:start + n] - want) <= tol)[:, zero]), b
+        start += n
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("news", [[1, 1], [1, 150]])
 def test_attention_of_values_of_all_sizes(D, news):
