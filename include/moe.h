@@ -575,6 +575,8 @@ int moe_kv_reset(const moe_kv* kv, moe_stream_t stream);
  * All or nothing: when the free blocks, the table's width or max_tokens do
  * not suffice for every row, no row takes tokens (drops still happen), the
  * batch is empty (q_start = 0, slot = -1) and MOE_DERR_KV_FULL is set.
+ * A block id outside the pool in a table that the caller changed sets
+ * MOE_DERR_KV_INDEX when a plan meets it; its new tokens get slot INT32_MIN.
  * ------------------------------------------------------------------------ */
 int moe_kv_plan(const moe_kv* kv, const int32_t* new_len, int32_t rows, const moe_kv_batch* batch,
                 moe_stream_t stream);

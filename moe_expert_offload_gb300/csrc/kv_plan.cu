@@ -9,7 +9,9 @@
 // both ranked over all rows in (row, block) order: rank k goes to (comes from)
 // place count - 1 - k, so blocks given back come out again in the same order.
 // Exclusive scans over the rows give the ranks and q_start; token t of row b
-// sits at position kept + (t - q_start[b]).
+// sits at position kept + (t - q_start[b]).  Block ids are moved as they are; one
+// outside the pool (no plan writes such a table) is flagged when it is moved or
+// mapped, and its tokens get a slot that every reader of slots flags and skips.
 //
 // Bound by latency: one CTA scans the rows (1024 at a time: up to that many are
 // read once and kept in registers) and moves the blocks, a thread per block
@@ -18,6 +20,8 @@
 // over all SMs, whose CTAs search q_start in shared memory, four tokens a thread.
 // Measured: 64 rows, one token each, taken and dropped again (two calls) 7.1 us;
 // 256 rows with 90000 new tokens in 5600 blocks, and dropped again, 17.8 us.
+#include <climits>
+
 #include "kv_common.cuh"
 
 namespace moe {
@@ -104,8 +108,12 @@ __device__ __forceinline__ void map_token(const PlanArgs& a, int t, int row, int
                                           int len, int& slot, int& pos) {
   const int P = a.kv.block_tokens, p_shift = 31 - __clz(P);
   pos = len - (end - start) + (t - start);
-  slot = (a.kv.block_table[(int64_t)row * a.kv.max_blocks + (pos >> p_shift)] << p_shift) +
-         (pos & (P - 1));
+  const int block = a.kv.block_table[(int64_t)row * a.kv.max_blocks + (pos >> p_shift)];
+  slot = (block << p_shift) + (pos & (P - 1));
+  if ((unsigned)block >= (unsigned)a.kv.num_blocks) {
+    slot = INT_MIN;
+    atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
@@ -175,6 +183,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
       const long long from = carry[pass], to = carry[pass] + s_scan[pass][31];
       if (!(pass == 1 && refused)) {
         // four blocks of a thread on their way at a time
+        bool outside = false;
         for (int k0 = (int)from + tid; k0 < (int)to; k0 += 4 * kThreads) {
           int32_t *src[4], *dst[4], v[4];
 #pragma unroll
@@ -194,8 +203,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a) {
             if (k0 + j * kThreads < (int)to) {
               *dst[j] = v[j];
               if (pass == 0) *src[j] = -1;
+              outside |= (unsigned)v[j] >= (unsigned)a.kv.num_blocks;
             }
         }
+        if (outside) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
       }
       for (int i = 0; i < 3; ++i) carry[i] += s_scan[i][31];
     }

@@ -123,6 +123,45 @@ def test_plan_refuses_tables_that_are_not_its_own():
     assert int(kv.free_count[0]) == 5 and _np(batch.q_start).tolist() == [0, 0, 0]
 
 
+@pytest.mark.parametrize("bad", [-1, -5, 12, 1 << 28, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("max_tokens", [40, 5000])
+def test_plan_flags_block_ids_outside_the_pool(bad, max_tokens):
+    """A row whose held block has an id outside the pool: its new tokens get a slot that the store
+    flags and skips, padding among them nowhere, and the id is flagged again when it goes back to
+    the free list and when another row takes it."""
+    P, K, D = 16, 1, 64
+    kv = m.DeviceKv(3, 4, 12, P, K, D)
+    kv.pool.zero_()
+    batch = m.DeviceKvBatch(max_tokens, 3)
+
+    def plan(new):
+        m.moe_kv_plan(kv.c, _ints(new), 3, batch.c)
+        err = int(batch.err[0])
+        batch.err.zero_()
+        return err, _np(batch.slot)[:_np(batch.q_start)[3]]
+
+    assert plan([10, 20, 0])[0] == 0
+    kv.block_table[0, 0] = bad
+    err, slots = plan([6, 1, 0])  # positions 10 .. 15 of row 0, the last ones of its bad block
+    assert err == m.MOE_DERR_KV_INDEX
+    assert np.array_equal(slots[:6], np.full(6, -2 ** 31))
+    assert slots[6] == int(kv.block_table[1, 1]) * P + 4
+    x = torch.randn(7, 3, D, device=DEV).bfloat16()
+    q = torch.full((7, 1, D), 7.0, dtype=torch.bfloat16, device=DEV)
+    m.moe_qkv_store(kv.c, batch.c, None, m.make_qkv(x[:, :1], x[:, 1:2], x[:, 2:]), 7, None, q)
+    assert int(batch.err[0]) == m.MOE_DERR_KV_INDEX
+    batch.err.zero_()
+    assert torch.all(q[:6] == 7.0) and torch.equal(q[6:], x[6:, :1])
+    kk, _ = ref.read_slots(_np(kv.pool), np.setdiff1d(np.arange(12 * P), slots[6:]), K, P, D)
+    assert not kk.any()
+    assert plan([1, 0, 0])[0] == 0  # the row's next block is a good one
+    assert plan([-17, 0, 0])[0] == m.MOE_DERR_KV_INDEX
+    assert bad in _np(kv.free_list).tolist()
+    err, slots = plan([0, 0, 20])
+    assert err == m.MOE_DERR_KV_INDEX and kv.block_table[2, :2].tolist().count(bad) == 1
+    assert np.sum(slots == -2 ** 31) in (4, 16) and not np.any(slots == -1)
+
+
 # ------------------------------------------------------------------ store and load
 def _slots(rng, T, blocks, P):
     return _ints(rng.permutation(blocks * P)[:T])
