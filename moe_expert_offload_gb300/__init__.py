@@ -206,6 +206,23 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_BF16, _INT32 = [], []  # element types that the device reads as these: bf16 or its bits, int32
+
+
+def _array(t, kinds, least, name):
+    """_ptr of an array that the device reads as `least` contiguous entries of these kinds."""
+    if t is None or t.__class__ is int:
+        return t
+    if not kinds:
+        import torch
+
+        _BF16[:] = torch.bfloat16, torch.int16, torch.uint16
+        _INT32[:] = (torch.int32,)
+    if t.dtype not in kinds or t.numel() < least or not t.is_contiguous():
+        raise MoeError(MOE_EINVAL, f"{name} must be contiguous {kinds[0]} with at least {least} entries")
+    return t.data_ptr()
+
+
 def _stream(s):
     if s is None:
         import torch
@@ -357,10 +374,6 @@ def moe_layer_forward_prefill(spec, layer_experts, x, T, w_router, bias, shared,
                                                   _stream(stream)))
 
 
-def _ref(s):
-    return None if s is None else C.byref(s)
-
-
 def moe_kv_block_bytes(kv) -> int:
     return int(lib().moe_kv_block_bytes(C.byref(kv)))
 
@@ -370,29 +383,45 @@ def moe_kv_reset(kv, stream=None):
 
 
 def moe_kv_plan(kv, new_len, rows, batch, stream=None):
-    return _check(lib().moe_kv_plan(C.byref(kv), _ptr(new_len), rows, C.byref(batch),
-                                    _stream(stream)))
+    return _check(lib().moe_kv_plan(kv, _array(new_len, _INT32, rows, "new_len"), rows,
+                                    batch, _stream(stream)))
 
 
 def moe_qkv_store(kv, batch, rope, proj, T, positions, q_out, stream=None):
-    return _check(lib().moe_qkv_store(C.byref(kv), C.byref(batch), _ref(rope), C.byref(proj), T,
-                                      _ptr(positions), _ptr(q_out), _stream(stream)))
+    K, D, made = kv.kv_heads, kv.head_dim, getattr(proj, "made", None)
+    if made and (made[0] < T or made[1] != K or made[2] != D):
+        raise MoeError(MOE_EINVAL, f"proj has {made} tokens, kv heads and columns; the step and the "
+                       f"cache {(T, K, D)}")
+    if rope and rope.rotary_dim:
+        axes = rope.axes
+        if axes > 1 and getattr(positions, "ndim", 1) > 1 and positions.shape[-1] != T:
+            raise MoeError(MOE_EINVAL, "positions must be [axes][T]")
+        positions = _array(positions, _INT32, axes * T, "positions")
+    else:
+        positions = _ptr(positions)
+    return _check(lib().moe_qkv_store(kv, batch, rope, proj, T, positions,
+                                      _array(q_out, _BF16, T * proj.q_heads * D, "q_out"),
+                                      _stream(stream)))
 
 
 def moe_kv_load(kv, slots, T, k, v, err=None, stream=None):
-    return _check(lib().moe_kv_load(C.byref(kv), _ptr(slots), T, _ptr(k), _ptr(v), _ptr(err),
-                                    _stream(stream)))
+    n = T * kv.kv_heads * kv.head_dim
+    return _check(lib().moe_kv_load(kv, _array(slots, _INT32, T, "slots"), T,
+                                    _array(k, _BF16, n, "k"), _array(v, _BF16, n, "v"),
+                                    _ptr(err), _stream(stream)))
 
 
 def moe_kv_attention_workspace_bytes(kv, rows, T, heads, max_new) -> int:
-    return int(lib().moe_kv_attention_workspace_bytes(C.byref(kv), rows, T, heads, max_new))
+    return int(lib().moe_kv_attention_workspace_bytes(kv, rows, T, heads, max_new))
 
 
 def moe_kv_attention(kv, batch, rows, q, T, heads, max_new, scale, workspace, workspace_bytes,
                      out, stream=None):
-    return _check(lib().moe_kv_attention(C.byref(kv), C.byref(batch), rows, _ptr(q), T, heads,
-                                         max_new, scale, _ptr(workspace), workspace_bytes,
-                                         _ptr(out), _stream(stream)))
+    n = T * heads * kv.head_dim
+    return _check(lib().moe_kv_attention(kv, batch, rows,
+                                         _array(q, _BF16, n, "q"), T, heads, max_new, scale,
+                                         _ptr(workspace), workspace_bytes,
+                                         _array(out, _BF16, n, "out"), _stream(stream)))
 
 
 # ------------------------------------------------- device memory (plumbing)
@@ -568,4 +597,5 @@ def make_qkv(q, k, v, q_norm=None, k_norm=None, eps=1e-6) -> MoeQkv:
     p = MoeQkv(_ptr(q), _ptr(k), _ptr(v), q.stride(0), q.stride(1), k.stride(0), k.stride(1),
                v.stride(0), v.stride(1), q.shape[1], eps, _ptr(q_norm), _ptr(k_norm))
     p.tensors = (q, k, v, q_norm, k_norm)
+    p.made = (k.shape[0], k.shape[1], k.shape[2])
     return p

@@ -216,6 +216,46 @@ def test_binding_refusals():
             m.make_qkv(*a)
 
 
+def test_binding_checks_arrays():
+    """Arrays of another type, too short or not contiguous are refused before the library sees
+    them; so is a projection that is not the cache's."""
+    import torch
+
+    def refused(*words):
+        return lambda call: _refused(m.MOE_EINVAL, call, *words)
+
+    kv, b, T = _kv(), _batch(), 5
+    for t in (torch.ones(4, dtype=torch.int64), torch.ones(3, dtype=torch.int32),
+              torch.ones(8, dtype=torch.int32)[::2], torch.ones(4)):
+        refused("new_len")(lambda: m.moe_kv_plan(kv, t, 4, b, 0))
+        refused("slots")(lambda: m.moe_kv_load(kv, t, 4, PTR, PTR, None, 0))
+    x = torch.zeros(T, 12, 128, dtype=torch.bfloat16)
+    q, out = x[:, :8].contiguous(), torch.zeros(T, 8, 128, dtype=torch.bfloat16)
+    proj = m.make_qkv(x[:, :8], x[:, 8:10], x[:, 10:])
+    for t in (x[:, :8], q[:4], q.half(), q.transpose(0, 1)):
+        refused("q")(lambda: _attend(q=t, T=T))
+        refused("out")(lambda: _attend(out=t, T=T))
+        refused("q_out")(lambda: _store(proj=proj, T=T, q_out=t))
+    for t in (q[:, :1], q[:4, :2].contiguous(), q[:, :2].float()):
+        refused("k")(lambda: m.moe_kv_load(kv, PTR, T, t, PTR, None, 0))
+        refused("v")(lambda: m.moe_kv_load(kv, PTR, T, PTR, t, None, 0))
+    for args in (dict(T=6), dict(T=T, kv=_kv(kv_heads=4)), dict(T=T, kv=_kv(kv_heads=1)),
+                 dict(T=T, kv=_kv(head_dim=64)), dict(T=T, kv=_kv(head_dim=256))):
+        refused("proj")(lambda: _store(proj=proj, **args))
+    rope = _rope(axes=3)
+    for t in (torch.zeros(3, T, dtype=torch.int64), torch.zeros(2, T, dtype=torch.int32),
+              torch.zeros(3, T + 1, dtype=torch.int32), torch.zeros(T, 3, dtype=torch.int32).t()):
+        refused("positions")(lambda: _store(proj=proj, T=T, rope=rope, positions=t, q_out=out))
+    refused("positions")(lambda: _store(proj=proj, T=T, positions=torch.zeros(T), q_out=out))
+    # what fits goes on to the library's own checks
+    fits = torch.zeros(3, T, dtype=torch.int32)
+    _refused(m.MOE_EINVAL, lambda: _store(proj=proj, T=T, rope=_rope(axes=3, max_pos=0),
+                                          positions=fits, q_out=out), "max_pos")
+    _refused(m.MOE_EINVAL, lambda: _store(proj=proj, T=T, rope=_rope(rotary_dim=0), positions=x,
+                                          q_out=PTR + 8), "q_out")  # nothing turns: not looked at
+    _refused(m.MOE_EINVAL, lambda: _attend(q=q, out=out.view(torch.int16), T=T, scale=0.0), "scale")
+
+
 def test_binding_helpers():
     import torch
 
