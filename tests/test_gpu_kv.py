@@ -850,6 +850,80 @@ def test_far_blocks_of_a_large_pool(news):
         start += t
 
 
+def _long_case(P, K, D, r, lens, news, cycle, climb, seed):
+    """Rows that all read one context, whose blocks come again after `cycle` of them, so that long
+    contexts need a small pool.  climb: the scores rise by about so much (log2) along the cycle."""
+    c = _attend_case(P, K, D, r, [cycle * P] + [1] * (len(lens) - 1), news, seed)
+    order = c["table"][0, :cycle]
+    width = -(-max(lens) // P)
+    c["table"] = np.tile(order[np.arange(width) % cycle], (len(lens), 1))
+    kv = c["kv"]
+    kv.block_table = _ints(c["table"])
+    kv.c.block_table, kv.c.max_blocks = kv.block_table.data_ptr(), width
+    c["lens"] = lens
+    c["batch"].kv_len.copy_(_ints(lens))
+    if climb:  # every query has a part along the ones, and a key's part along them rises
+        c["q"] += 0.5
+        up = climb * np.log(2) / (0.5 * D ** 0.5) * torch.arange(cycle, device=DEV) / cycle
+        meta = kv.pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16).view(-1, K * P // 16, 4, D // 4)
+        meta[torch.tensor(order, device=DEV), :, 1] += up.half()[:, None, None]
+    return c
+
+
+def _check_long(c, out):
+    """_check_attend in 64 bits on the GPU, of a context that all rows share."""
+    P, K, D, r = c["P"], c["K"], c["D"], c["H"] // c["K"]
+    slots = np.arange(c["kv"].pool.shape[0] * P)
+    k_all, v_all = (torch.tensor(x, device=DEV) for x in
+                    ref.read_slots(_np(c["kv"].pool), slots, K, P, D))
+    j = torch.arange(max(c["lens"]), device=DEV)
+    at = torch.tensor(c["table"][0], device=DEV)[j // P] * P + j % P
+    big = v_all.abs().amax(0).view(K, -1, 64).amax(-1).repeat_interleave(64, 1)  # [K, D]
+    start, wrong, size = 0, 0.0, 0.0
+    for L, n in zip(c["lens"], c["news"]):
+        seen = j[None, :L] <= L - n + torch.arange(n, device=DEV)[:, None]
+        for h in range(K):
+            k, v = k_all[at[:L], h], v_all[at[:L], h]
+            q = c["q"][start:start + n, h * r:(h + 1) * r].double()  # [n, r, D]
+            x = (q @ k.T * c["scale"]).masked_fill(~seen[:, None], -np.inf)
+            want = torch.softmax(x, -1) @ v
+            spread = c["scale"] * (q.square() @ k.square().T).amax(-1, True).sqrt() * 2.0 ** -11
+            tol = (want.abs() * 2.0 ** -8 + 1e-6
+                   + 2 * big[h] * (4 * 2.0 ** -11 + 2 * 8 * spread / 3 ** 0.5))
+            got = out[start:start + n, h * r:(h + 1) * r].double()
+            off = (got - want).abs()
+            assert bool((off <= tol).all()), (L, n, h, float((off / tol).max()))
+            wrong, size = wrong + float(off.square().sum()), size + float(want.square().sum())
+        start += n
+    assert (wrong / size) ** 0.5 <= ref.ATTENTION_REL
+    assert torch.all(out[start:] == 5.0)
+
+
+@pytest.mark.parametrize("climb", [0, 60])
+@pytest.mark.parametrize("P,K,D,r,B,least,most,n,cycle", [
+    # key tiles of a warp (its share of all units' tiles): 55, 107, 54, 61
+    (64, 8, 128, 4, 64, 150, 8191, 1, 128),
+    (16, 2, 256, 8, 8, 129000, 131071, 1, 300),
+    (32, 4, 64, 3, 40, 4000, 9000, 3, 282),
+    (128, 2, 128, 16, 12, 20000, 30001, 2, 40),
+    # key blocks of a CTA (128 keys): 75, 105, 74
+    (64, 2, 256, 8, 2, 9000, 9400, 600, 148),
+    (64, 4, 128, 8, 1, 13001, 13001, 1200, 210),
+    (16, 8, 64, 1, 5, 8000, 9000, 1000, 563),
+])
+def test_attention_of_long_shares(P, K, D, r, B, least, most, n, cycle, climb):
+    """Work enough that every warp (CTA) turns its buffers many times over, moves its means and its
+    window of the block table, and cuts few units: long contexts, with references that keep
+    growing on the way too."""
+    rng = np.random.default_rng(P + D)
+    lens = rng.integers(least, most + 1, B).tolist()
+    c = _long_case(P, K, D, r, lens, [n] * B, cycle, climb, 35)
+    out = _run_attend(c)
+    assert int(c["batch"].err[0]) == 0
+    _check_long(c, out)
+    assert torch.equal(_run_attend(c), out)
+
+
 def test_two_graphs_share_a_workspace():
     """Two captured calls of different shapes over one workspace, replayed one after the other."""
     a = _attend_case(64, 2, 128, 8, [900, 30], [1, 1], 28)
