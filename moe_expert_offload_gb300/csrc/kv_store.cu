@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(128) store_kernel(StoreArgs a, int parts) {
   bool bad = false;
   if (turns) {
     const int first = a.rope.adjacent ? sub * 4 : sub * 8 < half ? sub * 8 : sub * 8 - half;
-    if (a.rope.axes == 1 && half % 4 == 0) {
+    if (a.rope.axes == 1) {
       // one position: the pairs lie side by side in the table
       const int p = a.positions[t];
       bad = p < 0 || p >= a.rope.max_pos;
