@@ -666,9 +666,15 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
  *   workspace  device, >= moe_kv_attention_workspace_bytes for the same
  *              arguments, 256-byte aligned, any contents; calls whose
  *              execution overlaps need one each
- * Scores, maxima, sums and accumulators are fp32; the weights enter the second
- * product in fp16.  Results do not depend on the order in which the GPU runs
- * its blocks.  Cache entries that no token sees (the rest of a last block,
+ * Scores, maxima, sums and accumulators are fp32, and finite queries, keys and
+ * values give finite results however large the scores are.  The weights enter the second product in fp16 (2^-11 of themselves; those
+ * below 2^-18 of a row's largest lose bits).  Which kernel takes a row depends on
+ * its number of new tokens: with up to 64 queries per kv head (32 at head_dim
+ * 256) codes are multiplied as they are and a weight's product with a value's
+ * scale is rounded to fp16 once more; with more, keys and values are formed in
+ * fp16 first (2^-11 of scale * code + bias), so a token's result may differ by
+ * these roundings with the step that it comes in.  Results do not depend on the
+ * order in which the GPU runs its blocks.  Cache entries that no token sees (the rest of a last block,
  * free blocks) may hold anything, NaN included; a NaN or an infinity among the
  * values that one of a row's new tokens sees may reach the results of the row's
  * other new tokens in the same call, but of no other row.

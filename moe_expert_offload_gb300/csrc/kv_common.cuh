@@ -26,12 +26,15 @@ constexpr int kGrid = 152; // CTAs of the attention kernels: one per SM
 // go through the decode kernel, longer ones through the prompt kernel
 // (microseconds, decode | prompt, 8 query heads on a kv head; 1 and 16 rows of
 // 2000 to 4000 keys, 4 of 30000 to 60000):
-//   head_dim 256, 32 queries  13 | 26   35 | 37    86 |  82
-//                 48          15 | 27   43 | 38   123 |  85
-//   head_dim 128, 64          15 | 29   54 | 53   154 | 112
-//                 96          17 | 31   80 | 57   240 | 116
-//   head_dim 64,  64          13 | 24   36 | 43    97 |  92
-//                 96          14 | 25   48 | 42   149 |  98
+//   head_dim 256, 32 queries  13 | 24   32 | 33    84 |  76
+//                 48          14 | 26   43 | 35   120 |  80
+//   head_dim 128, 64          14 | 25   54 | 47   155 | 100
+//                 96          16 | 26   80 | 48   242 | 106
+//   head_dim 64,  64          13 | 22   36 | 38    99 |  86
+//                 96          13 | 22   48 | 37   152 |  91
+// A compromise: a lone short row is faster in the decode kernel at every number
+// of columns (its units are smaller), many or long ones in the prompt kernel
+// from about these numbers on; the rule does not look at the lengths.
 __host__ __device__ constexpr int decode_cols(int D) { return D == 256 ? 32 : 64; }
 
 __host__ __device__ constexpr int tile_bytes(int D) { return 18 * D; }

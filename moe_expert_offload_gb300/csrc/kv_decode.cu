@@ -27,19 +27,24 @@
 // (exact but for columns 2^-29 below the largest).  p is rounded to fp16 with
 // its largest value between 2^7 and 2^15, and its product with the values' scale (after a
 // power of two that brings the largest scale to between 2^-3 and 1) once more: 2^-11 each
-// against the output's 2^-8; where both are not the largest, products below 2^-21 of the
-// largest weight lose that precision to fp16's subnormals.  The maximum that p refers to follows the scores only when they
-// pass it by 2^8, so it rarely moves.  Codes are positive and the bias takes
+// against the output's 2^-8; products below 2^-18 of the largest weight and scale lose
+// that precision to fp16's subnormals.  The maximum that p refers to, a raw score, follows
+// the scores only when they pass it by 2^8, so it rarely moves.  Codes are positive and the bias takes
 // their mean back, so the accumulators would grow far past the result and lose
 // it to the MMA's truncating sums (measured at 128k keys: 2.1e-3 from fp64
 // against 1.6e-3 for bf16 rounding alone): every 16 tiles each group's mean is
 // moved from them into a rounded fp32 sum of its own.
 //
-// Measured: 64 rows of 150 to 8191 keys, 32 query heads on 8 of 128 (330 MB): 75.6 us,
-// 4.4 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 112 us, 5.3 TB/s.
-// The stream alone takes 54.7 and 88 us; the rest is instruction issue, 316 and
-// 400 per tile, most of them unpacking codes.  Few keys are latency: 1000 keys of
-// one row 11.3 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
+// Measured: 64 rows of 150 to 8191 keys, 32 query heads on 8 of 128 (330 MB): 76.8 us,
+// 4.3 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 111.5 us, 5.4 TB/s.
+// The stream alone takes 54.7 and 88 us.  A tile takes 321 and 409 instructions: 80
+// and 160 unpack codes (four masks per product of them, and shifts), 18 and 34 are
+// MMAs, the rest is what a stage and a tile cost besides (the copies' bookkeeping,
+// the scan over the values' scales, the growth test, scales and biases).  Neither
+// the issue slots (57 and 43%) nor the ALU pipe (53 and 46%) are full: every warp is
+// one serial chain, and 16 (8) of them on an SM do not cover it.  Spilled: 20, 44 and
+// 56 bytes a thread at head_dim 64, 128 and 256.  Few keys are latency: 1000 keys of
+// one row 11.6 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
 #include <type_traits>
 
 #include "kv_common.cuh"

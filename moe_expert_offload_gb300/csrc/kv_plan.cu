@@ -18,8 +18,8 @@
 // wherever its row is (binary search in the shared ranks).  The slot map of up
 // to kInline tokens follows in the same kernel, a longer one in a second kernel
 // over all SMs, whose CTAs search q_start in shared memory, four tokens a thread.
-// Measured: 64 rows, one token each, taken and dropped again (two calls) 7.1 us;
-// 256 rows with 90000 new tokens in 5600 blocks, and dropped again, 17.8 us.
+// Measured: 64 rows, one token each, taken and dropped again (two calls) 7.3 us;
+// 256 rows with 90000 new tokens in 5600 blocks, and dropped again, 18.0 us.
 #include <climits>
 
 #include "kv_common.cuh"

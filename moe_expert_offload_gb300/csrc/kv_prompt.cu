@@ -27,18 +27,21 @@
 // order in which one LOP3 yields pairs): the queries are laid out alike, and the
 // result is put in order when it is stored.
 // fp16 roundings: keys and values 2^-11 once, weights 2^-11 once (2^7 for the
-// maximum that they refer to, so that small ones keep their bits); queries are
-// scaled by a power of two per row.  That maximum follows the scores only when
-// weights may pass fp16's range (a score 2^3 to 2^9 above it), so the accumulator in
-// TMEM is rarely rescaled.
+// maximum that they refer to, so that small ones keep their bits; at head_dim 64
+// and 128 twice more for the first half of a block whose second half moves that
+// maximum, by the factor's rounding and the product's); queries are scaled by a
+// power of two per row.  That maximum follows the scores only when weights may pass
+// fp16's range (a score 2^3 to 2^9 above it), so the accumulator in TMEM is rarely
+// rescaled.
 //
-// Measured: 8192 tokens, 16 query heads on 2 of 256: 508 us, 1082 TFLOP/s (56% of a
-// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 790 us,
-// 1316 TFLOP/s (68%).  Bound by the chain of a block: at head_dim 64 and 128 scores,
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 499 us, 1102 TFLOP/s (57% of a
+// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 787 us,
+// 1321 TFLOP/s (68%).  The compiler spills 400 to 430 bytes a thread
+// (stack 72 to 120).  Bound by the chain of a block: at head_dim 64 and 128 scores,
 // TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
 // takes all the shared memory there is, values freed, dequantised (1400 cycles),
 // fenced (570), seen by the issuer (350) and multiplied (1500).  The tensor pipe is
-// busy 57% (128) and 47% (256) of the time, the issue slots 58 and 60%.  Measured and
+// busy 57% (128) and 49% (256) of the time, the issue slots 57 and 59%.  Measured and
 // dropped: two tiles with the next scores in halves of 64 keys, the first before
 // the product (975 us then against 876), a warp of its own that issues for each
 // tile (1046); one tile with keys and values handed over by halves of the columns
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           tm_st16(s_tm + wg * 32, p);
           tm_st16(s_tm + wg * 32 + 16, p + 16);
         } else {
-          // 64 columns at a time (2048 tokens on 30000 of head_dim 128: 790 us, 863 with 32 at a
+          // 64 columns at a time (2048 tokens on 30000 of head_dim 128, at the time: 790 us, 863 with 32 at a
           // time, 926 with loads under way one part ahead, whose registers spill)
 #pragma unroll(D == 128 ? 2 : 1)
           for (int c = 0; c < 2; ++c) {
