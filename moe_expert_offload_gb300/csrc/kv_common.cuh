@@ -44,12 +44,12 @@ __device__ __forceinline__ int swizzle(int r) {
   return D == 256 ? (r & 7) : D == 128 ? ((r >> 1) & 3) : ((r >> 2) & 1);
 }
 
-// scale * unit * 2^e, kept positive and finite: a hidden key's -inf stays one (times 0 it would be
-// NaN), and a score's distance of 0 stays 0.  At either end it makes no difference to the weights:
-// distances of raw scores are 0 or between 2^-80 and 2^40.
+// scale * unit * 2^e, kept between 1e-37 and 2^88: a hidden key's -inf stays one (times 0 it would
+// be NaN), and no score overflows (raw ones are below 2^39).  It changes no weight: distances of
+// raw scores are 0 or between 2^-80 and 2^40, which times either end is nothing or past 2^7.
 __device__ __forceinline__ float score_factor(float scale, float unit, int e) {
   const float f = scale * __int_as_float((e + 127) << 23) * unit;
-  return fminf(fmaxf(f, 1e-37f), 3e38f);
+  return fminf(fmaxf(f, 1e-37f), 0x1p88f);
 }
 
 // fp16 index (from the tile's 16 D bytes of codes on) of each scale and bias

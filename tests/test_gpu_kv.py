@@ -645,6 +645,43 @@ def test_attention_with_scales_at_the_ends(D, news, scale):
         start += n
 
 
+@pytest.mark.parametrize("scale", [1e4, 1e10, 1e30, 1e38])
+@pytest.mark.parametrize("D,news", [(D, n) for D in (64, 128, 256) for n in ([1, 2, 1], [130, 260, 33])])
+def test_attention_of_scores_below_fp32(D, news, scale):
+    """Scores that all lie below fp32's range, queries of 1e35 against keys of one value each (the
+    same in every column, so a raw score is exact but for its sum's 2^-16): the key nearest to zero
+    takes all the weight, a token's only key too.  Keys differ by 2^-8 of themselves at least."""
+    lens, P = [500, 260, 33], 32
+    c = _attend_case(P, 1, D, 8, lens, news, 36)
+    c["scale"] = scale
+    G = D // 64
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16).view(-1, 4, 16 * G)
+    key = torch.zeros(meta.shape[0], 16)
+    rng = np.random.default_rng(37)
+    near = []
+    for b, L in enumerate(lens):
+        j = np.arange(L)
+        size = 1 + rng.permutation(L) / 128  # one value a key
+        tile = c["table"][b, j // P] * (P // 16) + j % P // 16
+        key[tile, j % 16] = torch.tensor(size, dtype=torch.float32)
+        near.append(size)
+    meta[:, 0] = 0
+    meta[:, 1] = key.repeat_interleave(G, 1).half().to(DEV)
+    q = torch.full_like(c["q"], -1e35)
+    out = _run_attend(c, q=q)
+    assert int(c["batch"].err[0]) == 0
+    got, pool, start = _f64(out), _np(c["kv"].pool), 0
+    for b, (L, n) in enumerate(zip(lens, news)):
+        j = np.arange(L)
+        _, v = ref.read_slots(pool, c["table"][b, j // P] * P + j % P, 1, P, D)
+        top = np.array([near[b][:L - n + i + 1].argmin() for i in range(n)])
+        want = v[top, 0][:, None]
+        big = np.abs(v).max((0, 1)).reshape(-1, 64).max(-1).repeat(64)
+        tol = np.abs(want) * 2.0 ** -8 + 2 * big * 3 * 2.0 ** -11
+        assert np.all(np.abs(got[start:start + n] - want) <= tol), b
+        start += n
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("news", [[1, 1], [1, 150]])
 def test_attention_of_values_of_all_sizes(D, news):
