@@ -37,6 +37,11 @@
  *   moe_qkv_store      query/key norms, rotation and the 4-bit store
  *   moe_kv_load        slots read back
  *   moe_kv_attention   attention over the cache (decode and prompt chunks)
+ *   moe_kv_attention_view  the same through a sliding window, and for trees of
+ *                      drafted tokens
+ *   moe_kv_tree_plan, moe_kv_tree_accept, moe_kv_tree_keep
+ *                      what a tree's tokens see, the path that a check keeps,
+ *                      and its keys and values moved into place
  *
  * Conventions shared by every entry point
  *   Memory   Every pointer named *device* must point to device memory that
@@ -686,6 +691,123 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
 int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, const void* q,
                      int32_t T, int32_t heads, int32_t max_new, float scale, void* workspace,
                      size_t workspace_bytes, void* out, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Trees of drafted tokens, and sliding windows.
+ *
+ * A step's new tokens of a row are a chain (each follows the one before it) or a
+ * tree: parent[t] of the row's token t - q_start[b] = i is the index within the
+ * row, below i, of the token that it follows, or -1: it follows the cached
+ * tokens.  MOE_KV_CHAIN as the parent of a row's first token: the row is a chain
+ * (a prompt chunk, a single token), its other parents are not read.  A token's
+ * depth is its number of ancestors among the new tokens, its position kv_len - n
+ * + depth; a chain's depths are 0, 1, 2, ...
+ *
+ * One step, for all layers: moe_kv_plan (a place for every new token),
+ * moe_kv_tree_plan (which also turns batch->pos into the tree's positions);
+ * in each layer moe_qkv_store and moe_kv_attention_view; then the model's choice
+ * behind every new token, moe_kv_tree_accept, moe_kv_tree_keep, and moe_kv_plan
+ * with `drop` as new_len, which gives back the places of the tokens not kept.
+ * ------------------------------------------------------------------------ */
+#define MOE_KV_MAX_TREE 256 /* tokens of a row's tree */
+#define MOE_KV_CHAIN (-2)   /* parent[q_start[b]]: row b's new tokens are a chain */
+
+typedef struct moe_kv_tree {
+  int32_t max_new;       /* upper bound of a tree's tokens, 1..MOE_KV_MAX_TREE; rows of more
+                            new tokens must be chains */
+  const int32_t* parent; /* device [max_tokens of the batch] */
+  uint32_t* seen;        /* device [max_tokens][moe_kv_tree_words(max_new)]: per token its depth,
+                            then bit i % 32 of word 1 + i / 32: it sees the row's new token i
+                            (moe_kv_tree_plan writes it; not read for rows of more than max_new
+                            new tokens; moe_kv_tree_accept needs none) */
+} moe_kv_tree;
+
+/* What a token at position p sees of its row: of the keys before it and its own
+ * (a tree's token: of the cached keys, its ancestors and itself) those at positions
+ * p - window + 1 .. p and those at positions below `sinks`. */
+typedef struct moe_kv_view {
+  int32_t window;          /* >= 1, or 0: all positions (sinks then change nothing) */
+  int32_t sinks;           /* >= 0: first positions that stay visible */
+  const moe_kv_tree* tree; /* host; NULL: every row is a chain */
+} moe_kv_view;
+
+/* Words of one token in moe_kv_tree.seen: 1 + ceil(max_new / 32); 0 for a
+ * max_new outside 1..MOE_KV_MAX_TREE. */
+int32_t moe_kv_tree_words(int32_t max_new);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_tree_plan -- what the new tokens of a step see of each other through
+ * `view`, and their positions.  Once per step for all layers of one window; a
+ * model that alternates windows keeps a moe_kv_tree (with its own `seen` and the
+ * same `parent`) for each.
+ *   view   with a tree, whose seen is written for the rows of at most max_new
+ *          new tokens (and batch->pos, for the same rows)
+ *   rows, T  rows and tokens of the step (T >= q_start[rows]); what lies behind
+ *          the last row's tokens stays as it was
+ * A parent that is not below its token's index, or below -1, counts as -1, a
+ * longer row that is no chain as one, and a row whose bounds are not consistent
+ * is skipped; each sets MOE_DERR_KV_INDEX.
+ * ------------------------------------------------------------------------ */
+int moe_kv_tree_plan(const moe_kv_batch* batch, const moe_kv_view* view, int32_t rows, int32_t T,
+                     moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_attention_view -- moe_kv_attention where a token sees what `view` leaves
+ * it.  All arguments, types, bounds, the workspace (moe_kv_attention_workspace_bytes)
+ * and the errors are moe_kv_attention's; rows that are trees, chains and prompt
+ * chunks mix in one call.  With a tree, moe_kv_tree_plan has been called for this
+ * step with this view's window and sinks.
+ * Only the tiles of 16 keys that some new token of the row sees are read: the
+ * work goes with the window, not with the context.  Keys and values that no new
+ * token of the row sees may hold anything, and the table may hold any id for the
+ * blocks of which none is seen (moe_kv_plan still gives a dropped row's ids back
+ * as they stand there).
+ * ------------------------------------------------------------------------ */
+int moe_kv_attention_view(const moe_kv* kv, const moe_kv_batch* batch, const moe_kv_view* view,
+                          int32_t rows, const void* q, int32_t T, int32_t heads, int32_t max_new,
+                          float scale, void* workspace, size_t workspace_bytes, void* out,
+                          moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_tree_accept -- the path that a check of a step's trees keeps.  A row's
+ * first new token (the one that the step before chose) is kept; behind a kept
+ * token i comes the child of lowest index whose `token` is next[i], if any.  A
+ * chain (MOE_KV_CHAIN) is kept whole.
+ *   token  device int32 [T]: the drafted tokens
+ *   next   device int32 [T]: the model's choice behind each of them
+ *   path   device int32 [T] out: row b's kept tokens, as indexes within the row,
+ *          from path[q_start[b]] on, ascending; -1 behind them
+ *   kept   device int32 [rows] out: their number (0: a row without new tokens)
+ *   drop   device int32 [rows] out: kept - n, moe_kv_plan's new_len afterwards
+ *   last   device int32 [rows] out: next of the last kept token: the token that
+ *          the row goes on with; -1 for a row without new tokens
+ * path must not overlap the inputs.  Entries behind the last row's tokens stay
+ * as they were.  Errors are moe_kv_tree_plan's; a child whose parent is not
+ * valid is never kept, and of a row that is skipped nothing is (0, 0, -1; its
+ * path stays as it was).
+ * ------------------------------------------------------------------------ */
+int moe_kv_tree_accept(const moe_kv_batch* batch, const moe_kv_tree* tree, int32_t rows, int32_t T,
+                       const int32_t* token, const int32_t* next, int32_t* path, int32_t* kept,
+                       int32_t* drop, int32_t* last, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_kv_tree_keep -- keys and values of each row's kept tokens moved to the first
+ * places of the row's new tokens, as they are held (codes, scales, biases), in
+ * all layers: the new token path[q_start[b] + i] goes where token i lies, i <
+ * kept[b].  (A key's rotation is that of its position, kv_len - n + depth, which
+ * is where it goes.)  Places behind the kept ones keep what they hold.
+ *   kv     HOST array of `layers` structs, one per layer, of one shape; their
+ *          pools differ (two of one pool are not defined)
+ *   path, kept  device int32, as moe_kv_tree_accept writes them (or a caller's
+ *          own choice: any ascending path)
+ * Before the moe_kv_plan that drops the other tokens, with the step's batch.  Up
+ * to 128 layers are one launch.  A row whose bounds are not consistent, whose
+ * path does not ascend within it or whose kept lies outside 0 .. n is left as it
+ * is, and a token whose slot (or whose place's) lies outside the pool is not
+ * moved; each sets MOE_DERR_KV_INDEX.  A row with kept = n is left as it is.
+ * ------------------------------------------------------------------------ */
+int moe_kv_tree_keep(const moe_kv* kv, int32_t layers, const moe_kv_batch* batch, int32_t rows,
+                     int32_t T, const int32_t* path, const int32_t* kept, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

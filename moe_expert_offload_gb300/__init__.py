@@ -38,7 +38,8 @@ EXPORTED = (
     "moe_layer_prefetch", "moe_expert_ffn_prefill", "moe_layer_forward_prefill",
     "moe_slots_for_budget", "moe_cache_resize_workspace_bytes", "moe_cache_resize",
     "moe_kv_block_bytes", "moe_kv_reset", "moe_kv_plan", "moe_qkv_store", "moe_kv_load",
-    "moe_kv_attention_workspace_bytes", "moe_kv_attention",
+    "moe_kv_attention_workspace_bytes", "moe_kv_attention", "moe_kv_attention_view",
+    "moe_kv_tree_words", "moe_kv_tree_plan", "moe_kv_tree_accept", "moe_kv_tree_keep",
 )
 MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -109,6 +110,18 @@ class MoeQkv(C.Structure):
                 ("q_heads", C.c_int32), ("eps", C.c_float), ("q_norm", C.c_void_p),
                 ("k_norm", C.c_void_p)]
 
+
+class MoeKvTree(C.Structure):
+    _fields_ = [("max_new", C.c_int32), ("parent", C.c_void_p), ("seen", C.c_void_p)]
+
+
+class MoeKvView(C.Structure):
+    _fields_ = [("window", C.c_int32), ("sinks", C.c_int32), ("tree", C.POINTER(MoeKvTree))]
+
+
+# trees of drafted tokens (include/moe.h)
+MOE_KV_MAX_TREE = 256
+MOE_KV_CHAIN = -2
 
 _lib = None
 
@@ -193,6 +206,18 @@ def lib():
         L.moe_kv_attention_workspace_bytes.argtypes = [kp, i32, i32, i32, i32]
         L.moe_kv_attention.restype = C.c_int
         L.moe_kv_attention.argtypes = [kp, bp, i32, vp, i32, i32, i32, C.c_float, vp, sz, vp, vp]
+        tp, wp = C.POINTER(MoeKvTree), C.POINTER(MoeKvView)
+        L.moe_kv_attention_view.restype = C.c_int
+        L.moe_kv_attention_view.argtypes = [kp, bp, wp, i32, vp, i32, i32, i32, C.c_float, vp, sz,
+                                            vp, vp]
+        L.moe_kv_tree_words.restype = i32
+        L.moe_kv_tree_words.argtypes = [i32]
+        L.moe_kv_tree_plan.restype = C.c_int
+        L.moe_kv_tree_plan.argtypes = [bp, wp, i32, i32, vp]
+        L.moe_kv_tree_accept.restype = C.c_int
+        L.moe_kv_tree_accept.argtypes = [bp, tp, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_kv_tree_keep.restype = C.c_int
+        L.moe_kv_tree_keep.argtypes = [kp, i32, bp, i32, i32, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -424,6 +449,50 @@ def moe_kv_attention(kv, batch, rows, q, T, heads, max_new, scale, workspace, wo
                                          _array(out, _BF16, n, "out"), _stream(stream)))
 
 
+def moe_kv_attention_view(kv, batch, view, rows, q, T, heads, max_new, scale, workspace,
+                          workspace_bytes, out, stream=None):
+    _tree_holds(getattr(view, "made", None), T)
+    n = T * heads * kv.head_dim
+    return _check(lib().moe_kv_attention_view(kv, batch, view, rows, _array(q, _BF16, n, "q"), T,
+                                              heads, max_new, scale, _ptr(workspace),
+                                              workspace_bytes, _array(out, _BF16, n, "out"),
+                                              _stream(stream)))
+
+
+def _tree_holds(made, T):
+    if made and made < T:
+        raise MoeError(MOE_EINVAL, f"the tree was made for {made} tokens, the step has {T}")
+
+
+def moe_kv_tree_words(max_new) -> int:
+    return int(lib().moe_kv_tree_words(max_new))
+
+
+def moe_kv_tree_plan(batch, view, rows, T, stream=None):
+    _tree_holds(getattr(view, "made", None), T)
+    return _check(lib().moe_kv_tree_plan(batch, view, rows, T, _stream(stream)))
+
+
+def moe_kv_tree_accept(batch, tree, rows, T, token, next_token, path, kept, drop, last,
+                       stream=None):
+    _tree_holds(getattr(tree, "made", None), T)
+    return _check(lib().moe_kv_tree_accept(batch, tree, rows, T, _array(token, _INT32, T, "token"),
+                                           _array(next_token, _INT32, T, "next_token"),
+                                           _array(path, _INT32, T, "path"),
+                                           _array(kept, _INT32, rows, "kept"),
+                                           _array(drop, _INT32, rows, "drop"),
+                                           _array(last, _INT32, rows, "last"), _stream(stream)))
+
+
+def moe_kv_tree_keep(layers, batch, rows, T, path, kept, stream=None):
+    """layers: DeviceKv.layers, or any sequence of MoeKv of one shape."""
+    if not isinstance(layers, C.Array):
+        layers = (MoeKv * len(layers))(*layers)
+    return _check(lib().moe_kv_tree_keep(layers, len(layers), batch, rows, T,
+                                         _array(path, _INT32, T, "path"),
+                                         _array(kept, _INT32, rows, "kept"), _stream(stream)))
+
+
 # ------------------------------------------------- device memory (plumbing)
 def make_spec(num_layers, hidden, inter, num_experts, top_k, router="softmax", n_groups=1,
               topk_groups=1, routed_scale=1.0, has_shared=False, shared_inter=None,
@@ -535,7 +604,7 @@ class DeviceKv:
         self.pools = [torch.empty((num_blocks, n), dtype=torch.uint8, device=device)
                       if with_pool else None for _ in range(layers)]
         self.pool = self.pools[0]
-        self.layers = [struct(p) for p in self.pools]
+        self.layers = (MoeKv * layers)(*(struct(p) for p in self.pools))
         self.c = self.layers[0]
 
 
@@ -552,6 +621,38 @@ class DeviceKvBatch:
         self.slot, self.pos, self.err = ints(max_tokens, -1), ints(max_tokens), ints(1)
         self.c = MoeKvBatch(max_tokens, max_rows, _ptr(self.q_start), _ptr(self.kv_len),
                             _ptr(self.slot), _ptr(self.pos), _ptr(self.err))
+
+
+class DeviceKvTree:
+    """A step's drafted trees in device memory + the C struct: `parent` comes from the drafter,
+    `seen` from moe_kv_tree_plan, the others from moe_kv_tree_accept.  A model that alternates
+    windows makes one for each, with the first one's `parent`."""
+
+    def __init__(self, max_tokens, max_rows, max_new, device="cuda", parent=None):
+        import torch
+
+        words = moe_kv_tree_words(max_new)
+        if words == 0:
+            raise MoeError(MOE_EINVAL, f"max_new must be in 1..{MOE_KV_MAX_TREE}")
+
+        def ints(*shape):
+            return torch.zeros(shape, dtype=torch.int32, device=device)
+
+        self.parent = ints(max_tokens) if parent is None else parent
+        self.seen = ints(max_tokens, words)
+        self.path, self.kept = ints(max_tokens), ints(max_rows)
+        self.drop, self.last = ints(max_rows), ints(max_rows)
+        self.c = MoeKvTree(max_new, _array(self.parent, _INT32, max_tokens, "parent"),
+                           _ptr(self.seen))
+        self.c.made = max_tokens
+
+
+def make_view(window=0, sinks=0, tree=None) -> MoeKvView:
+    """What a token sees: its last `window` positions (0: all) and those below `sinks`; tree: a
+    DeviceKvTree for a step with trees."""
+    v = MoeKvView(window, sinks, C.pointer(tree.c) if tree else None)
+    v.held, v.made = tree, tree.c.made if tree else None
+    return v
 
 
 def rope_table(max_pos, rotary_dim, base=10000.0, device="cuda"):

@@ -72,6 +72,34 @@ int check_tokens(const moe_kv_batch* b, int32_t T) {
   return MOE_OK;
 }
 
+int check_tree(const moe_kv_tree* t) {
+  if (t->max_new < 1 || t->max_new > MOE_KV_MAX_TREE)
+    return set_error(MOE_EINVAL, "tree max_new must be in 1..%d", MOE_KV_MAX_TREE);
+  if (!t->parent) return set_error(MOE_EINVAL, "tree parent is NULL");
+  return MOE_OK;
+}
+
+// a view and its tree's visibility of T tokens
+int check_view(const moe_kv_view* v, int32_t T) {
+  if (!v) return set_error(MOE_EINVAL, "view is NULL");
+  if (v->window < 0) return set_error(MOE_EINVAL, "window must be >= 0");
+  if (v->sinks < 0) return set_error(MOE_EINVAL, "sinks must be >= 0");
+  if (!v->tree) return MOE_OK;
+  const int rc = check_tree(v->tree);
+  if (rc) return rc;
+  if (!v->tree->seen) return set_error(MOE_EINVAL, "tree seen is NULL");
+  if ((int64_t)T * moe_kv_tree_words(v->tree->max_new) > 0x7fffffff)
+    return set_error(MOE_EUNSUPPORTED, "T * moe_kv_tree_words exceeds 2^31 - 1");
+  return MOE_OK;
+}
+
+int check_batch_rows(const moe_kv_batch* b, int32_t rows) {
+  if (rows < 1) return set_error(MOE_EINVAL, "rows must be >= 1");
+  if (rows > b->max_rows)
+    return set_error(MOE_ECAPACITY, "rows = %d exceeds the batch's %d", rows, b->max_rows);
+  return MOE_OK;
+}
+
 int check_strided(const char* what, const void* p, int64_t token_stride, int64_t head_stride) {
   if (!p) return set_error(MOE_EINVAL, "%s is NULL", what);
   if (!aligned(p, 16) || token_stride % 8 || head_stride % 8 || token_stride < 0 ||
@@ -209,15 +237,17 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
   return moe::kv::attn_workspace_bytes(*kv, rows, T, heads, max_new);
 }
 
-int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, const void* q,
-                     int32_t T, int32_t heads, int32_t max_new, float scale, void* workspace,
-                     size_t workspace_bytes, void* out, moe_stream_t stream) {
+static int attention(const moe_kv* kv, const moe_kv_batch* batch, const moe_kv_view* view,
+                     int32_t rows, const void* q, int32_t T, int32_t heads, int32_t max_new,
+                     float scale, void* workspace, size_t workspace_bytes, void* out,
+                     moe_stream_t stream) {
   int rc = check_tables(kv);
   if (!rc) rc = check_pool(kv);
   if (!rc) rc = check_batch(batch);
   if (!rc) rc = check_rows(kv, batch, rows);
   if (!rc) rc = check_tokens(batch, T);
   if (!rc) rc = check_heads(kv, heads, max_new);
+  if (!rc && view) rc = check_view(view, T);
   if (rc) return rc;
   if (T == 0) return set_ok();
   if (!q || !out || !workspace) return set_error(MOE_EINVAL, "moe_kv_attention: NULL argument");
@@ -228,7 +258,7 @@ int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, 
   const size_t need = moe::kv::attn_workspace_bytes(*kv, rows, T, heads, max_new);
   if (workspace_bytes < need)
     return set_error(MOE_ECAPACITY, "workspace %zu < %zu bytes", workspace_bytes, need);
-  moe::kv::AttnArgs a;
+  moe::kv::AttnArgs a = {};
   a.kv = *kv;
   a.batch = *batch;
   a.q = static_cast<const uint16_t*>(q);
@@ -239,8 +269,123 @@ int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, 
   a.heads = heads;
   a.max_new = max_new;
   a.scale = scale;
+  if (view) {
+    a.window = view->window;
+    a.sinks = view->window ? view->sinks : 0;
+    if (view->tree) {
+      a.tree = view->tree->seen;
+      a.tree_max = view->tree->max_new;
+      a.words = moe_kv_tree_words(a.tree_max);
+    }
+  }
   const cudaError_t e = moe::kv::launch_attention(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kv attention launch");
+  return set_ok();
+}
+
+int moe_kv_attention(const moe_kv* kv, const moe_kv_batch* batch, int32_t rows, const void* q,
+                     int32_t T, int32_t heads, int32_t max_new, float scale, void* workspace,
+                     size_t workspace_bytes, void* out, moe_stream_t stream) {
+  return attention(kv, batch, nullptr, rows, q, T, heads, max_new, scale, workspace,
+                   workspace_bytes, out, stream);
+}
+
+int moe_kv_attention_view(const moe_kv* kv, const moe_kv_batch* batch, const moe_kv_view* view,
+                          int32_t rows, const void* q, int32_t T, int32_t heads, int32_t max_new,
+                          float scale, void* workspace, size_t workspace_bytes, void* out,
+                          moe_stream_t stream) {
+  if (!view) return set_error(MOE_EINVAL, "view is NULL");
+  return attention(kv, batch, view, rows, q, T, heads, max_new, scale, workspace, workspace_bytes,
+                   out, stream);
+}
+
+int32_t moe_kv_tree_words(int32_t max_new) {
+  return max_new < 1 || max_new > MOE_KV_MAX_TREE ? 0 : 1 + (max_new + 31) / 32;
+}
+
+int moe_kv_tree_plan(const moe_kv_batch* batch, const moe_kv_view* view, int32_t rows, int32_t T,
+                     moe_stream_t stream) {
+  int rc = check_batch(batch);
+  if (!rc) rc = check_batch_rows(batch, rows);
+  if (!rc) rc = check_tokens(batch, T);
+  if (!rc) rc = check_view(view, T);
+  if (rc) return rc;
+  if (!view->tree) return set_error(MOE_EINVAL, "moe_kv_tree_plan: the view has no tree");
+  if (T == 0) return set_ok();
+  moe::kv::TreePlanArgs a;
+  a.batch = *batch;
+  a.parent = view->tree->parent;
+  a.seen = view->tree->seen;
+  a.rows = rows;
+  a.T = T;
+  a.max_new = view->tree->max_new;
+  a.words = moe_kv_tree_words(a.max_new);
+  a.window = view->window;
+  a.sinks = view->sinks;
+  const cudaError_t e = moe::kv::launch_tree_plan(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kv tree plan launch");
+  return set_ok();
+}
+
+int moe_kv_tree_accept(const moe_kv_batch* batch, const moe_kv_tree* tree, int32_t rows, int32_t T,
+                       const int32_t* token, const int32_t* next, int32_t* path, int32_t* kept,
+                       int32_t* drop, int32_t* last, moe_stream_t stream) {
+  int rc = check_batch(batch);
+  if (!rc) rc = check_batch_rows(batch, rows);
+  if (!rc) rc = check_tokens(batch, T);
+  if (!rc) rc = tree ? check_tree(tree) : set_error(MOE_EINVAL, "tree is NULL");
+  if (rc) return rc;
+  if (!kept || !drop || !last || (T && (!token || !next || !path)))
+    return set_error(MOE_EINVAL, "moe_kv_tree_accept: NULL argument");
+  moe::kv::TreeAcceptArgs a;
+  a.batch = *batch;
+  a.parent = tree->parent;
+  a.token = token;
+  a.next = next;
+  a.path = path;
+  a.kept = kept;
+  a.drop = drop;
+  a.last = last;
+  a.rows = rows;
+  a.T = T;
+  a.max_new = tree->max_new;
+  const cudaError_t e = moe::kv::launch_tree_accept(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kv tree accept launch");
+  return set_ok();
+}
+
+int moe_kv_tree_keep(const moe_kv* kv, int32_t layers, const moe_kv_batch* batch, int32_t rows,
+                     int32_t T, const int32_t* path, const int32_t* kept, moe_stream_t stream) {
+  if (layers < 1) return set_error(MOE_EINVAL, "layers must be >= 1");
+  for (int l = 0; l < (kv ? layers : 1); ++l) {
+    int rc = check_shape(kv ? kv + l : nullptr);
+    if (!rc) rc = check_pool(kv + l);
+    if (rc) return rc;
+    if (kv[l].num_blocks != kv->num_blocks || kv[l].block_tokens != kv->block_tokens ||
+        kv[l].kv_heads != kv->kv_heads || kv[l].head_dim != kv->head_dim)
+      return set_error(MOE_EINVAL, "layer %d's pool has another shape than the first one's", l);
+  }
+  int rc = check_batch(batch);
+  if (!rc) rc = check_batch_rows(batch, rows);
+  if (!rc) rc = check_tokens(batch, T);
+  if (rc) return rc;
+  if (T == 0) return set_ok();
+  if (!path || !kept) return set_error(MOE_EINVAL, "moe_kv_tree_keep: NULL argument");
+  moe::kv::TreeKeepArgs a;
+  a.batch = *batch;
+  a.path = path;
+  a.kept = kept;
+  a.rows = rows;
+  a.T = T;
+  a.num_blocks = kv->num_blocks;
+  a.block_tokens = kv->block_tokens;
+  a.kv_heads = kv->kv_heads;
+  for (int at = 0; at < layers; at += a.layers) {
+    a.layers = layers - at < moe::kv::kKeepLayers ? layers - at : moe::kv::kKeepLayers;
+    for (int l = 0; l < a.layers; ++l) a.pool[l] = static_cast<uint8_t*>(kv[at + l].pool);
+    const cudaError_t e = moe::kv::launch_tree_keep(a, kv->head_dim, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "kv tree keep launch");
+  }
   return set_ok();
 }
 

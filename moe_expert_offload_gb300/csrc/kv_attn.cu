@@ -1,10 +1,10 @@
 // Attention over the 4-bit key/value cache: which kernel takes which rows.
 //
 // Rows of up to decode_cols queries per kv head go through the decode kernel
-// (kv_decode.cu), longer ones through the prompt kernel (kv_prompt.cu).  The
+// (kv_decode.cuh), longer ones through the prompt kernel (kv_prompt.cuh).  The
 // rows' lengths are on the device, so both look at every row and leave the
 // other's alone; the prompt kernel is launched only where max_new allows a long
-// row.
+// row.  Both exist twice: for causal attention, and with windows and trees (View).
 #include "kv_common.cuh"
 
 namespace moe {
@@ -20,11 +20,12 @@ size_t attn_workspace_bytes(const moe_kv& kv, int, int, int heads, int max_new) 
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
-  const cudaError_t e = launch_decode(a, st);
+  const bool view = a.window > 0 || a.tree;
+  const cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
   if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new)) return e;
   AttnArgs p = a;
   p.ws = static_cast<char*>(a.ws) + decode_workspace_bytes(a.kv.head_dim);
-  return launch_prompt(p, st);
+  return view ? launch_prompt_view(p, st) : launch_prompt(p, st);
 }
 
 }  // namespace kv

@@ -100,13 +100,63 @@ struct AttnArgs {
   void* ws;
   int rows, T, heads, max_new;
   float scale;
+  // what a token sees (the kernels with View): the last `window` positions (0: all) and those
+  // below `sinks`; the visibility of trees of up to tree_max tokens, `words` of a token
+  int window, sinks, tree_max, words;
+  const uint32_t* tree;
 };
+
+// What a row's new tokens see of its keys, in whole tiles: the first sink_tiles tiles, then those
+// from the first position of the window on.  The kernels walk a row without the gap between
+// them: tile t of the walk is the row's tile t, or t + gap behind the sinks.
+struct Sight {
+  int sink_tiles, gap;
+  __device__ __forceinline__ int tile(int t) const { return t < sink_tiles ? t : t + gap; }
+};
+// first: the first position that the window leaves to any of the tokens (below 0: all of them)
+__device__ __forceinline__ Sight sight_of(const AttnArgs& a, int first) {
+  Sight s;
+  s.sink_tiles = a.sinks / kTile + (a.sinks % kTile != 0);
+  s.gap = max(0, max(first, 0) / kTile - s.sink_tiles);
+  return s;
+}
+// of 16 keys, those below the x-th
+__device__ __forceinline__ uint32_t below16(int x) {
+  return x >= 16 ? 0xFFFFu : x <= 0 ? 0u : (1u << x) - 1u;
+}
 size_t attn_workspace_bytes(const moe_kv& kv, int rows, int T, int heads, int max_new);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
 size_t decode_workspace_bytes(int D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_decode_view(const AttnArgs& a, cudaStream_t st);
 size_t prompt_workspace_bytes(int D);
 cudaError_t launch_prompt(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_prompt_view(const AttnArgs& a, cudaStream_t st);
+
+struct TreePlanArgs {
+  moe_kv_batch batch;
+  const int32_t* parent;
+  uint32_t* seen;
+  int rows, T, max_new, words, window, sinks;
+};
+cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t st);
+
+struct TreeAcceptArgs {
+  moe_kv_batch batch;
+  const int32_t *parent, *token, *next;
+  int32_t *path, *kept, *drop, *last;
+  int rows, T, max_new;
+};
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st);
+
+constexpr int kKeepLayers = 128;  // layers of one launch: their pools go by value
+struct TreeKeepArgs {
+  moe_kv_batch batch;
+  const int32_t *path, *kept;
+  int rows, T, num_blocks, block_tokens, kv_heads, layers;
+  uint8_t* pool[kKeepLayers];
+};
+cudaError_t launch_tree_keep(const TreeKeepArgs& a, int head_dim, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace moe
