@@ -81,9 +81,7 @@ struct Cfg {
   // 256, 16 heads on 2, from 512 on 278, 285, 296)
   static constexpr int kUnitKeys = D == 128 ? 768 : 512;
   static constexpr int kBlockBytes = kKeys * D * 2;  // one block of keys (or values, or queries)
-  // results on their way out: each softmax warp's 32 rows of 64 bytes, 80 apart
-  static constexpr int kOutBytes = kSoftWarps * 32 * 80;
-  static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes + kOutBytes;
+  static constexpr size_t kSmem = 1024 + (size_t)(kTiles + 2 * kStages) * kBlockBytes;
   static constexpr int kPartial = kRows * (D + 3);  // floats: o [row][D], top, l, fac [row]
   static constexpr uint32_t kIdescS = (1u << 4) | ((kKeys >> 3) << 17) | ((128u >> 4) << 24);
   static constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
@@ -98,7 +96,7 @@ struct Cfg {
 
 // The unit that a CTA began and did not end: the last CTA with a part of it (-1: there is none).
 struct Cut {
-  int last, start, n, tok0, kvh, pad[3];
+  int last, start, end, tok0, kvh, pad[3];  // tokens tok0 .. end - 1
 };
 constexpr size_t kCutBytes = (kGrid * sizeof(Cut) + 255) / 256 * 256;
 
@@ -126,6 +124,7 @@ __device__ __forceinline__ long long most_keys(const AttnArgs& a, const Row& i, 
   return (long long)a.window + a.sinks + (by_tree<View>(a, i) ? i.n : tok) + 2 * kTile;
 }
 
+template <bool View>
 __device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok) {
   Row i;
   i.start = a.batch.q_start[b];
@@ -141,54 +140,87 @@ __device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok
   return i;
 }
 
-// Cost of the first j units of a head of the row: each its keys (taking every
-// tile for a full one) and a fixed part.
-template <int D, bool View>
-__device__ __forceinline__ long long cost_before(const AttnArgs& a, const Row& i, int tok, long long j) {
-  if constexpr (View) {  // the first units by their keys, the others by the window
-    const long long most = most_keys<View>(a, i, tok), base = i.len - i.n;
-    const long long k = most < base ? 0 : min(j, (most - base) / tok);
-    return j * Cfg<D>::kUnitKeys + k * base + (long long)tok * (k * (k + 1) / 2) + (j - k) * most;
+// Costs of a row's units: each its keys (taking every tile for a full one; with a window `most` at
+// most, which the units from `full` on have) and a fixed part.
+struct Costs {
+  long long base, most;
+  int tok, full;
+};
+template <bool View>
+__device__ __forceinline__ Costs costs_of(const AttnArgs& a, const Row& i, int tok) {
+  Costs c = {i.len - i.n, 0, tok, INT_MAX};
+  if constexpr (View) {
+    c.most = most_keys<View>(a, i, tok);
+    if (a.window > 0) {
+      const long long more = c.most - c.base;
+      c.full = more < 0 ? 0 : more > INT_MAX ? INT_MAX : (int)more / tok;
+    }
   }
-  return j * (i.len - i.n + Cfg<D>::kUnitKeys) + (long long)tok * (j * (j + 1) / 2);
+  return c;
+}
+template <int D, bool View>
+__device__ __forceinline__ long long cost_of(const Costs& c, int j) {
+  const long long keys = c.base + (long long)(j + 1) * c.tok;
+  return (View && j >= c.full ? c.most : keys) + Cfg<D>::kUnitKeys;
+}
+// of the first j of them
+template <int D, bool View>
+__device__ __forceinline__ long long cost_before(const Costs& c, int j) {
+  const long long k = View ? min(j, c.full) : j;
+  long long x = (long long)j * Cfg<D>::kUnitKeys + k * c.base + (long long)c.tok * (k * (k + 1) / 2);
+  if constexpr (View)
+    if (k < j) x += (j - k) * c.most;
+  return x;
 }
 
-struct Unit {
-  int kvh, tok0;     // kv head, first token
-  int blk0, blk1;    // key blocks of this share
-  int blocks;        // key blocks of the unit
-  int low;           // View: the first position that the window leaves to any of its tokens
-  long long rest;    // cost behind this share's end that still holds blocks
+// A unit, or a CTA's share of one, as it is handed to the roles.
+struct Job {
+  int more;                // 0: there are no more units
+  int b, start, n, len;    // its row
+  int kvh, tok0;           // kv head, first token
+  int blk0, blk1, blocks;  // key blocks of this share, and of the unit
+  int low, gap;            // View: the first position that the window leaves to any of its tokens,
+                           // and the tiles between the sinks' and that one's
+  int last;                // the last CTA with a part of a unit that is begun here and not ended
 };
+constexpr int kJobs = 4;
+constexpr int kTakers = kSoftWarps + 2 * kSideWarps + 1;  // warps that take jobs
 
-// The walk over a CTA's share; every role runs it for itself.
+// The walk over a CTA's share.
 struct Walk {
   int b, kvh, j;
-  long long at, left;  // offset in unit (kvh, j) where the share goes on; what is left of it
+  long long at, left, share;  // offset in unit (kvh, j) where the share goes on; what is left of it
   Row row;
+  Costs costs;
 };
 
 template <int D, bool View>
-__device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int tok, Unit& u) {
+__device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int tok, Job& u) {
   constexpr int kUnitKeys = Cfg<D>::kUnitKeys;
   while (w.left > 0) {
-    if (w.row.tiles == 0 || w.kvh >= a.kv.kv_heads) {
+    if (w.kvh >= a.kv.kv_heads) {
       do {
         if (++w.b >= a.rows) return false;
-        w.row = row_info(a, w.b, r, tok);
+        w.row = row_info<View>(a, w.b, r, tok);
       } while (w.row.tiles == 0);
+      w.costs = costs_of<View>(a, w.row, tok);
       w.kvh = w.j = 0;
       w.at = 0;
     }
     const int seen = w.row.len - w.row.n + min(w.row.n, (w.j + 1) * tok);
-    long long cost = w.row.len - w.row.n + kUnitKeys + (long long)(w.j + 1) * tok;
+    const long long cost = cost_of<D, View>(w.costs, w.j);
+    u.b = w.b;
+    u.start = w.row.start;
+    u.n = w.row.n;
+    u.len = w.row.len;
     u.kvh = w.kvh;
     u.tok0 = w.j * tok;
     u.blocks = (seen + kKeys - 1) / kKeys;
+    u.low = u.gap = 0;
     if constexpr (View) {
-      cost = min(cost, most_keys<View>(a, w.row, tok) + kUnitKeys);
       u.low = first_seen<View>(a, w.row, u.tok0);
-      u.blocks = (seen - sight_of(a, u.low).gap * kTile + kKeys - 1) / kKeys;
+      u.gap = sight_of(a, u.low).gap;
+      u.blocks = (seen - u.gap * kTile + kKeys - 1) / kKeys;
     }
     // both ends of a share fall on the same block for the CTAs on either side
     auto block_at = [&](long long x) {
@@ -198,7 +230,13 @@ __device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int
     u.blk0 = block_at(w.at);
     const bool whole = w.left >= cost - w.at;
     u.blk1 = whole ? u.blocks : block_at(w.at + w.left);
-    u.rest = min(cost, kUnitKeys + (long long)u.blocks * kKeys - kKeys / 2) - (w.at + w.left);
+    u.last = -1;
+    if (u.blk0 == 0 && u.blk1 < u.blocks) {
+      // it goes on at the next share's start: what of its cost behind there still holds blocks
+      const long long rest =
+          min(cost, kUnitKeys + (long long)u.blocks * kKeys - kKeys / 2) - (w.at + w.left);
+      u.last = (int)(blockIdx.x + (rest + w.share - 1) / w.share);
+    }
     if (whole) {
       w.left -= cost - w.at;
       w.at = 0;
@@ -391,7 +429,15 @@ __device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
                : "memory");
 }
 
-template <int D, bool View>
+// 32 bytes, a whole sector
+__device__ __forceinline__ void stg256(void* to, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Split: a unit is one tile of queries, whose key blocks two tiles take in turn.
+template <int D, bool View, bool Split>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   using C = Cfg<D>;
   constexpr int NT = C::kTiles, S = C::kStages;
@@ -400,20 +446,32 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   // the block's parity: a buffer's next block waits for the scores (products) of the block that
   // it replaces, which are never more than one phase of that barrier ago.
   __shared__ __align__(8) uint64_t k_full[S], v_full[S], p_full[NT][2];
-  __shared__ __align__(8) uint64_t s_full[NT][2], o_done[NT][2], q_full, drained;
+  __shared__ __align__(8) uint64_t s_full[NT][2], o_done[NT][2], drained;
+  // a unit's queries are there; by the unit's parity: those of the next one may come before the
+  // softmax has looked for these
+  __shared__ __align__(8) uint64_t q_full[2];
+  __shared__ __align__(8) uint64_t k_free[S], v_free[S], q_free;  // nothing reads the buffer any more
+  __shared__ __align__(8) uint64_t job_full[kJobs], job_free[kJobs];
+  __shared__ Job s_job[kJobs];
   __shared__ uint32_t tmem_slot;
-  __shared__ long long s_scan[kThreads / 32], s_at, s_share;
+  __shared__ long long s_scan[kThreads / 32], s_at;
   __shared__ int s_row;
   __shared__ volatile int s_stop;  // a wait ran out
-  __shared__ float s_fac[C::kRows], s_max[2][128], s_sum[2][128];
+  // factors of the rows' scores, of this unit and the next
+  __shared__ float s_fac[2][C::kRows], s_max[2][128], s_sum[2][128];
+  // key tiles of a block that are missing (a block id outside the pool): two bits of each byte, of
+  // the last four blocks (the softmax reads a block's before the keys' side writes the fourth
+  // behind it, which waits for scores that come after this block's weights)
+  __shared__ uint32_t s_miss[4];
   const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
   const int K = a.kv.kv_heads, r = a.heads / K, P = a.kv.block_tokens;
   const int p_shift = 31 - __clz(P);
-  const int per_tile = 128 / r, tok = per_tile * NT;  // tokens of a tile, of a unit
+  static_assert(NT == 2 || !Split, "two tiles");
+  constexpr int kUnitTiles = Split ? 1 : NT;
+  const int per_tile = 128 / r, tok = per_tile * kUnitTiles;  // tokens of a tile, of a unit
   const uint32_t r_inv = (65536 + r - 1) / r;         // x * r_inv >> 16 = x / r for x < 128
   const uint32_t base = (su32(smem_raw) + 1023u) & ~1023u;
   const uint32_t q_at = base, k_at = q_at + NT * C::kBlockBytes, v_at = k_at + S * C::kBlockBytes;
-  const uint32_t out_at = v_at + S * C::kBlockBytes;
 
   if (wid == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -426,13 +484,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     for (int i = 0; i < S; ++i) {
       bar_init(su32(&k_full[i]), kSideWarps);
       bar_init(su32(&v_full[i]), kSideWarps);
+      bar_init(su32(&k_free[i]), 1);
+      bar_init(su32(&v_free[i]), 1);
     }
     for (int i = 0; i < 2 * NT; ++i) {
       bar_init(su32(&s_full[0][0] + i), 1);
       bar_init(su32(&o_done[0][0] + i), 1);
       bar_init(su32(&p_full[0][0] + i), kSoftWarps / NT);
     }
-    bar_init(su32(&q_full), kSoftWarps);
+    for (int i = 0; i < kJobs; ++i) {
+      bar_init(su32(&job_full[i]), 1);
+      bar_init(su32(&job_free[i]), kTakers);
+    }
+    bar_init(su32(&q_full[0]), kSoftWarps);
+    bar_init(su32(&q_full[1]), kSoftWarps);
+    bar_init(su32(&q_free), 1);
     bar_init(su32(&drained), 1);
     s_row = -1;
     s_stop = 0;
@@ -440,42 +506,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   }
   __syncwarp();
   griddep_wait();
+  Cut* cuts = static_cast<Cut*>(a.ws);
+  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kCutBytes);
+  if (tid == 0) cuts[blockIdx.x].last = -1;
 
   // ------------------------------------------------------- this CTA's share
   long long total = 0;
   auto share_of = [&] { return max((total + kGrid - 1) / kGrid, 2ll * kKeys); };
-  if (a.rows <= 32) {
-    // every warp for itself, a lane per row (7 short prompts: 48.8 us, 52.0 the other way)
-    long long cost = 0;
-    if (lane < a.rows) {
-      const Row i = row_info(a, lane, r, tok);
-      if (i.tiles) cost = K * cost_before<D, View>(a, i, tok, i.tiles);
-    }
-    long long v = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(~0u, v, o);
-      if (lane >= o) v += u;
-    }
-    total = __shfl_sync(~0u, v, 31);
-    const long long share = share_of(), x0 = blockIdx.x * share;
-    if (wid == 0 && x0 < v && x0 >= v - cost) {
-      s_row = lane;
-      s_at = x0 - (v - cost);
-    }
-    if (tid == 0) s_share = share;
-  }
+  auto row_cost = [&](const Row& i) {
+    return i.tiles ? K * cost_before<D, View>(costs_of<View>(a, i, tok), i.tiles) : 0ll;
+  };
   const int chunks = (a.rows + kThreads - 1) / kThreads;
-  // more: chunks of kThreads rows, twice over when there is more than one (the total comes first)
+  // Up to 32 rows are the walking warp's own business, a lane per row (below).  More: chunks of
+  // kThreads rows, twice over when there is more than one (the total comes first)
   for (int pass = a.rows <= 32 ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
     long long carry = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
       long long cost = 0;
-      if (b < a.rows) {
-        const Row i = row_info(a, b, r, tok);
-        if (i.tiles) cost = K * cost_before<D, View>(a, i, tok, i.tiles);
-      }
+      if (b < a.rows) cost = row_cost(row_info<View>(a, b, r, tok));
       long long v = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -492,13 +541,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       }
       if (pass == 0 || chunks == 1) total = carry + sum;
       if (pass == 1) {
-        const long long share = share_of();
-        const long long pre = before + v - cost, x0 = blockIdx.x * share;
+        const long long pre = before + v - cost, x0 = blockIdx.x * share_of();
         if (x0 < total && x0 >= pre && x0 < pre + cost) {
           s_row = b;
           s_at = x0 - pre;
         }
-        if (tid == 0) s_share = share;
       }
       carry += sum;
     }
@@ -507,59 +554,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   __syncthreads();
   tc_after();
   const uint32_t tmem = tmem_slot;
-  Cut* cuts = static_cast<Cut*>(a.ws);
-  float* parts = reinterpret_cast<float*>(static_cast<char*>(a.ws) + kCutBytes);
-  if (tid == 0) cuts[blockIdx.x].last = -1;
-
-  Walk walk;
-  walk.left = 0;
-  if (s_row >= 0) {
-    walk.b = s_row;
-    walk.row = row_info(a, walk.b, r, tok);
-    walk.left = min(s_share, total - blockIdx.x * s_share);
-    const long long per_head = cost_before<D, View>(a, walk.row, tok, walk.row.tiles);
-    long long x = s_at;
-    walk.kvh = (int)(x / per_head);
-    x -= walk.kvh * per_head;
-    int lo = 0, hi = walk.row.tiles;  // the last unit whose cost_before is <= x
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (cost_before<D, View>(a, walk.row, tok, mid) <= x) lo = mid;
-      else hi = mid;
-    }
-    walk.j = lo;
-    walk.at = x - cost_before<D, View>(a, walk.row, tok, lo);
-  }
-  Unit u;
-
-  if (wid < kSoftWarps) {
-    // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
-    const int wg = wid >> 2, row = (wid & 3) * 32 + lane;  // TMEM lane
-    const int tile = NT == 1 ? 0 : wg;
-    const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
-    const uint32_t o_tm = tmem + lanes + tile * C::kO;
-    uint32_t n = 0;  // blocks seen
-    // A unit's queries: a warp's rows, 8 columns a lane, all loads under way at once.  The
-    // buffer is free once the last block's scores of the unit before are there.
-    auto load_queries = [&](const Row& w_row, const Unit& u) {
-      constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = C::kRows / kSoftWarps / kAtOnce;
-      constexpr uint32_t kGroup = kLanes == 32 ? ~0u : (1u << kLanes) - 1u;
-      const uint32_t group = kGroup << (lane / kLanes * kLanes);
-      uint4 raw[kRounds];
+  auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
+  // job k of this CTA: whether there is one; it stays in its place until the warp has given it back
+  auto take = [&](uint32_t k) {
+    wait_all(&job_full[k % kJobs], k / kJobs, s_stop);
+    return !stopped() && s_job[k % kJobs].more != 0;
+  };
+  auto give = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) sc::bar_arrive(su32(&job_free[k % kJobs]));
+  };
+  // the row's tile that a unit's walk has as its tile t
+  auto tile_of = [&](const Job& u, int t) {
+    return View && u.gap && t >= sight_of(a, 0).sink_tiles ? t + u.gap : t;
+  };
+  // A unit's queries by eight warps, of which this is one: a warp's rows, 8 columns a lane, some
+  // loads under way at a time.
+  auto load_queries = [&](auto at_once_tag, int warp, uint32_t n_u) {
+    constexpr int kWarps = kSoftWarps, kDeep = decltype(at_once_tag)::value;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 128 * kUnitTiles / kWarps / kAtOnce;
+    constexpr uint32_t kGroup = kLanes == 32 ? ~0u : (1u << kLanes) - 1u;
+    static_assert(kRounds % kDeep == 0, "whole batches");
+    const Job& u = s_job[n_u % kJobs];
+    const uint32_t group = kGroup << (lane / kLanes * kLanes);
+    const int col8 = lane % kLanes;
+    const int n = u.n, tok0 = u.tok0;
+    const uint16_t* src = a.q + ((int64_t)(u.start + tok0) * a.heads + u.kvh * r) * D + col8 * 8;
+    for (int i0 = 0; i0 < kRounds; i0 += kDeep) {
+      uint4 raw[kDeep];
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int qr = (wid * kRounds + i) * kAtOnce + lane / kLanes, in = qr & 127;
-        const int i_tok = (int)(in * r_inv >> 16), t = u.tok0 + (qr >> 7) * per_tile + i_tok;
+      for (int i = 0; i < kDeep; ++i) {
+        const int qr = (warp * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
+        const int i_tok = (int)(in * r_inv >> 16), t = (qr >> 7) * per_tile + i_tok;
         raw[i] = make_uint4(0, 0, 0, 0);
-        if (in < per_tile * r && t < w_row.n)
-          raw[i] = *reinterpret_cast<const uint4*>(
-              a.q + ((int64_t)(w_row.start + t) * a.heads + u.kvh * r + in - i_tok * r) * D +
-              lane % kLanes * 8);
+        if (in < per_tile * r && tok0 + t < n)
+          raw[i] = *reinterpret_cast<const uint4*>(src + ((int64_t)t * a.heads + in - i_tok * r) * D);
       }
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int qr = (wid * kRounds + i) * kAtOnce + lane / kLanes, in = qr & 127;
+      for (int i = 0; i < kDeep; ++i) {
+        const int qr = (warp * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
         const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
         uint32_t big = 0;
 #pragma unroll
@@ -573,65 +606,57 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           x[2 * k] = __uint_as_float(w[k] << 16) * up;
           x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u) * up;
         }
-        const int col8 = lane % kLanes;
         sts128(q_at + (qr >> 7) * C::kBlockBytes + (col8 >> 3) * (kKeys * 128) + in * 128 +
                    (((col8 & 7) ^ (in & 7)) << 4),
                make_uint4(pack_h2(x[0], x[4]), pack_h2(x[1], x[5]), pack_h2(x[2], x[6]),
                           pack_h2(x[3], x[7])));
         // score = fac * accumulated, in units of log2
-        if (col8 == 0) s_fac[qr] = score_factor(a.scale, 8.8054160e-05f, e);  // log2(e) 2^-14 2^e
+        if (col8 == 0)
+          s_fac[n_u & 1u][qr] = score_factor(a.scale, 8.8054160e-05f, e);  // log2(e) 2^-14 2^e
       }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) sc::bar_arrive(su32(&q_full));
+    }
+    fence_async();
+    __syncwarp();
+    if (lane == 0) sc::bar_arrive(su32(&q_full[n_u & 1u]));
+  };
+
+  if (wid < kSoftWarps) {
+    // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
+    const int wg = wid >> 2, row = (wid & 3) * 32 + lane;  // TMEM lane
+    const int tile = NT == 1 ? 0 : wg;
+    const uint32_t lanes = (uint32_t)((wid & 3) * 32) << 16;
+    const uint32_t o_tm = tmem + lanes + tile * C::kO;
+    uint32_t n = 0;  // blocks seen
+    auto is_tree = [&](const Job& u) { return View && a.tree && u.n <= a.tree_max; };
+    // View: where the window of the unit's last token begins
+    auto last_low = [&](const Job& u) {
+      if (!View || a.window <= 0) return 0;
+      return u.len - u.n + (is_tree(u) ? u.n : min(u.n, u.tok0 + tok)) - a.window;
     };
-    bool have = next_unit<D, View>(walk, a, r, tok, u);
-    if (have) load_queries(walk.row, u);
-    while (have) {
-      const Row ri = walk.row;
-      const int b = walk.b;
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // s_fac of all rows
-      const float fac = s_fac[tile * 128 + row];
-      {
-        // the next unit's queries come to L2 meanwhile: a row of queries a thread
-        Walk ahead = walk;
-        Unit un;
-        if (next_unit<D, View>(ahead, a, r, tok, un) && tid < C::kRows) {
-          const int in = tid & 127, i_tok = (int)(in * r_inv >> 16);
-          const int t = un.tok0 + (tid >> 7) * per_tile + i_tok;
-          if (in < per_tile * r && t < ahead.row.n) {
-            const uint16_t* src =
-                a.q + ((int64_t)(ahead.row.start + t) * a.heads + un.kvh * r + in - i_tok * r) * D;
-#pragma unroll
-            for (int k = 0; k < D; k += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + k));
-          }
-        }
-      }
-      const int row_tok = (int)(row * r_inv >> 16), row_h = row - row_tok * r;
-      const int t = u.tok0 + tile * per_tile + row_tok;
-      const bool live = row < per_tile * r && t < ri.n;
-      int lim = ri.len - ri.n + min(t, ri.n - 1);            // last key that the row sees
-      int open = ri.len - ri.n + u.tok0 + tile * per_tile;   // all rows see the keys up to it
-      // View: where the row's window begins, and the last one of the tile's; a tree's first key and
-      // the bits of the row's token
-      int low = 0, last_low = 0, tree0 = INT_MAX;
-      const uint32_t* bits = nullptr;
-      Sight sight = {};
+    // the token of this thread's row
+    auto token_of = [&](const Job& u, int q_tile) {
+      return u.tok0 + q_tile * per_tile + (int)(row * r_inv >> 16);
+    };
+    uint32_t n_u = 0;
+    [[maybe_unused]] uint32_t n_blocks = 0;  // of the units before
+    bool have = take(0);
+    // (idle as yet, these warps bring the first unit's queries)
+    if (have) load_queries(std::integral_constant<int, D == 64 ? 4 : 8>{}, wid, 0);
+    // (every softmax warp leaves at the same unit: they meet at barriers on the way)
+    for (; !any_of_256(!have); ++n_u) {
+      const Job& u = s_job[n_u % kJobs];
+      const int q_tile = Split ? 0 : tile;  // the tile of the queries
+      wait_all(&q_full[n_u & 1u], n_u >> 1, s_stop);
+      const float fac = s_fac[n_u & 1u][q_tile * 128 + row];
+      // Blocks of which every row of the tile sees every key.
+      const int base0 = u.len - u.n, open = is_tree(u) ? base0 : base0 + u.tok0 + q_tile * per_tile + 1;
+      int free0 = 0, free1 = open / kKeys;
       if constexpr (View) {
-        sight = sight_of(a, u.low);
-        const int base = ri.len - ri.n;
-        int depth = min(t, ri.n - 1);
-        if (by_tree<View>(a, ri)) {
-          tree0 = base;
-          open = base - 1;
-          lim = ri.len - 1;
-          bits = a.tree + (size_t)(ri.start + depth) * a.words + 1;
-          depth = (int)bits[-1];
-        }
-        if (a.window > 0) {
-          low = base + depth - a.window + 1;
-          last_low = base + (tree0 == base ? ri.n : min(ri.n, u.tok0 + tok)) - a.window;
-        }
+        constexpr int kTiles = kKeys / kTile;
+        // (both ends lie behind the gap)
+        free0 = (max(0, (max(last_low(u), 0) + kTile - 1) / kTile - u.gap) + kTiles - 1) / kTiles;
+        free1 = (open / kTile - u.gap) / kTiles;
       }
       // The row's reference, a raw score; a score x weighs 2^(x fac + off), off = 7 - top fac.
       // Where that is far from zero every visible score shall weigh too much (an infinite query's
@@ -642,54 +667,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         if (fabsf(off) > kFar && top < -kNone) off = 3e38f;
       };
       set_off();
-      // the tiles of a block that are missing (a block id outside the pool), looked up a block ahead
-      auto block_of = [&](int i) {
-        int at = i * (kKeys / kTile) + lane;
-        if constexpr (View) at = sight.tile(at);
-        return lane < kKeys / kTile && at * kTile < ri.len
-                   ? a.kv.block_table[(int64_t)b * a.kv.max_blocks + ((at * kTile) >> p_shift)] : 0;
-      };
-      int block = block_of(u.blk0);
-      for (int i = u.blk0; i < u.blk1; ++i) {
+      constexpr int by = Split ? 2 : 1;
+      const int i0 = u.blk0 + (Split ? tile : 0), i1 = u.blk1;
+      for (int i = i0; i < i1; i += by) {
         const int slot = NT == 1 ? (int)(n & 1u) : tile;
-        const uint32_t miss = __ballot_sync(~0u, (unsigned)block >= (unsigned)a.kv.num_blocks);
-        block = block_of(i + 1);
         wait_all(&s_full[tile][n & 1u], n >> 1, s_stop);
         tc_after();
         const uint32_t s_tm = tmem + lanes + C::kS + slot * 128;
-        const int key0 = i * kKeys;
-        bool edge = key0 + kKeys > open + 1 || miss != 0;
-        if constexpr (View) {
-          const int from = sight.tile(i * (kKeys / kTile)) * kTile;
-          const int to = sight.tile(i * (kKeys / kTile) + kKeys / kTile - 1) * kTile + kTile;
-          edge = to > open + 1 || miss != 0 || (from < last_low && to > a.sinks);
-        }
-        // 16 columns (a key tile) from column c * 16 on: what the row does not see
-        auto hide = [&](uint32_t* v, int c) {
+        const uint32_t miss = s_miss[(Split ? n_blocks + i - u.blk0 : n) & 3u];
+        const bool edge = (View && i < free0) || i >= free1 || miss != 0;
+        // 64 columns (four key tiles) from column c * 16 on: what the row does not see is taken out.
+        // (All of it is found again from the job: kept, it would take registers from the others.)
+        auto is_missing = [&](int c) { return (miss >> (c / 2 * 8 + c % 2) & 1u) != 0; };
+        auto hide = [&](uint32_t* v, int c0) {
+          const int t = min(token_of(u, q_tile), u.n - 1), base = u.len - u.n;
           if constexpr (View) {
-            if (edge) {
-              const int key = sight.tile(i * (kKeys / kTile) + c) * kTile;
+            const bool tree = is_tree(u);
+            const int tree0 = tree ? base : INT_MAX, lim = tree ? u.len - 1 : base + t;
+            const int open = tree ? base : base + u.tok0 + q_tile * per_tile + 1, shut = last_low(u);
+            const uint32_t* bits = a.tree + (size_t)(u.start + t) * a.words + 1;
+            const int low = a.window > 0 ? base + (tree ? (int)bits[-1] : t) - a.window + 1 : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int key = tile_of(u, i * (kKeys / kTile) + c0 + q) * kTile;
+              if (key + kTile <= open && !is_missing(c0 + q) &&
+                  (key >= shut || key + kTile <= a.sinks))
+                continue;
               uint32_t see = below16(lim - key + 1);
               if (key + kTile > tree0) {
                 const int at = key - tree0;  // -15 and on: the first -at keys are cached ones
                 const int w = max(at, 0) >> 5, words = a.words - 1;
                 const uint32_t lo = w < words ? bits[w] : 0u, hi = w + 1 < words ? bits[w + 1] : 0u;
-                const uint32_t own = at < 0 ? lo << -at | ((1u << -at) - 1u)
-                                            : __funnelshift_r(lo, hi, at & 31);
-                see &= own;
+                see &= at < 0 ? lo << -at | ((1u << -at) - 1u) : __funnelshift_r(lo, hi, at & 31);
               }
               // (a tree's key lies at its depth, not at its place: its bits know of the window)
-              const uint32_t far = below16(min(low, tree0) - key) & ~below16(a.sinks - key);
-              see = (miss >> c) & 1u ? 0u : see & ~far;
+              see &= ~(below16(min(low, tree0) - key) & ~below16(a.sinks - key));
+              if (is_missing(c0 + q)) see = 0u;
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                if (!((see >> k) & 1u)) v[k] = 0xFF800000u;
+                if (!((see >> k) & 1u)) v[16 * q + k] = 0xFF800000u;
             }
-          } else if (edge) {
-            const int last = (miss >> c) & 1u ? -1 : lim - key0 - c * 16;
+          } else {
+            const int lim = base + t - i * kKeys;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (k > last) v[k] = 0xFF800000u;
+            for (int q = 0; q < 4; ++q) {
+              const int last = is_missing(c0 + q) ? -1 : lim - (c0 + q) * 16;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (k > last) v[16 * q + k] = 0xFF800000u;
+            }
           }
         };
         // The weights relative to the maximum so far, 2^7 above it.  While a part's sum is below
@@ -722,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           top = to;
           set_off();
           l *= f;
-          if (i > u.blk0 && __any_sync(~0u, f != 1.0f)) {
+          if (i > i0 && __any_sync(~0u, f != 1.0f)) {
             wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
             tc_after();
             constexpr int kCols = NT == 1 ? D / 2 : D;
@@ -746,8 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             tm_ld32(s_tm + wg * 64, v);
             tm_ld32(s_tm + wg * 64 + 32, v + 32);
             tm_wait_regs(v);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) hide(v + 16 * c, wg * 4 + c);
+            if (edge) hide(v, wg * 4);
             if constexpr (decltype(apart_tag)::value) {
               float seen = kNone;
 #pragma unroll
@@ -763,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           // Both halves of the rows agree on whether the reference follows, which it does once at
           // most.  Every score has been read by the barrier on the way: the weights may go over
           // the scores.
-          bool follow = i == u.blk0;
+          bool follow = i == i0;
           if (!follow) {
             attempt(Fused{});
             follow = any_of_256(sum.x + sum.y > kMost);
@@ -781,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             tm_ld32(s_tm + c * 64, x);
             tm_ld32(s_tm + c * 64 + 32, x + 32);
             tm_wait_regs(x);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) hide(x + 16 * q, 4 * c + q);
+            if (edge) hide(x, 4 * c);
             sum = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) weights(Fused{}, x + 16 * q, p + 8 * q);
@@ -818,91 +842,104 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         if (lane == 0) sc::bar_arrive(su32(&p_full[tile][n & 1u]));
         ++n;
       }
-      // the next unit's queries come while the last product runs
-      const Unit done = u;
-      have = next_unit<D, View>(walk, a, r, tok, u);
-      if (have) load_queries(walk.row, u);
       // ---- the unit's end (here): a result, or a part of one
-      wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
+      if (i0 < i1) wait_all(&o_done[tile][(n - 1) & 1u], (n - 1) >> 1, s_stop);
       tc_after();
-      if constexpr (NT == 1) {
+      float f_mine = 1.0f, f_other = 0.0f;
+      if (NT == 1 || Split) {
+        const int other = wg ^ 1;
         s_sum[wg][row] = l;
+        if (NT == 2) s_max[wg][row] = top;
+        tc_before();
         asm volatile("bar.sync 1, 256;" ::: "memory");
-        l += s_sum[wg ^ 1][row];
-      }
-      const bool whole = done.blk0 == 0 && done.blk1 == done.blocks;
-      const float inv = l > 0.0f ? 1.0f / l : l;
-      // A lane holds a row's columns; through shared memory four lanes get 64 bytes of a row each
-      // time, so that stores fill sectors (a row per lane: 2.5 times as long).
-      const long long out_row =
-          live ? (long long)(ri.start + t) * a.heads + done.kvh * r + row_h : -1ll;
-      float* part = parts + ((size_t)blockIdx.x * 2 + (done.blk0 == 0 ? 1 : 0)) * C::kPartial;
-      const int pr = tile * 128 + row;
-      constexpr int kCols = NT == 1 ? D / 2 : D;
-      const int c_at = NT == 1 ? wg * (D / 2) : 0;
-      const uint32_t stage = out_at + wid * (32 * 80), mine = stage + lane * 80;
-      auto flush = [&](auto&& store) {  // store(row of the warp, its output row, 16-byte piece, data)
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2);
-          const long long to = __shfl_sync(~0u, out_row, rr);
-          uint4 d;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w)
-                       : "r"(stage + rr * 80 + (lane & 3) * 16)
-                       : "memory");
-          if (to >= 0) store(rr, to, lane & 3, d);
+        tc_after();
+        if constexpr (NT == 1) {
+          l += s_sum[other][row];
+        } else {
+          // both tiles' results of the same queries
+          const float top_o = s_max[other][row], both = fmaxf(top, top_o);
+          f_mine = ex2((top - both) * fac);
+          f_other = ex2((top_o - both) * fac);
+          l = l * f_mine + s_sum[other][row] * f_other;
+          top = both;
         }
-        __syncwarp();
-      };
+      }
+      // (a tile that had no block of it has no result either)
+      const bool mine = i0 < i1, others = u.blk0 + (tile ^ 1) < i1;
+      const bool whole = u.blk0 == 0 && u.blk1 == u.blocks;
+      const float inv = whole ? (l > 0.0f ? 1.0f / l : l) : 1.0f;
+      f_mine *= inv;
+      f_other *= inv;
+      const int t = token_of(u, q_tile);
+      const bool live = row < per_tile * r && t < u.n;
+      uint16_t* dst = a.out + ((int64_t)(u.start + t) * a.heads + u.kvh * r + row - (int)(row * r_inv >> 16) * r) * D;
+      float* part = parts + ((size_t)blockIdx.x * 2 + (u.blk0 == 0 ? 1 : 0)) * C::kPartial;
+      const int pr = q_tile * 128 + row;
+      have = take(n_u + 1);
+      // A lane holds a row's columns: 32 at a time, in whole sectors.  (Where `out` is not aligned
+      // to them, half sectors.)
+      constexpr bool halves = NT == 1 || Split;  // of the columns, one for either tile (warp group)
+      const int c_at = halves ? wg * (D / 2) : 0, c_end = halves ? c_at + D / 2 : D;
+      const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
+      for (int c = c_at; c < c_end; c += 32) {
         uint32_t v[32];
-        tm_ld32(o_tm + c_at + c, v);
-        tm_wait_regs(v);
+        if constexpr (Split) {
+          uint32_t w[32];
+          tm_ld32(tmem + lanes + wg * C::kO + c, v);
+          tm_ld32(tmem + lanes + (wg ^ 1) * C::kO + c, w);
+          tm_wait_regs(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            asm volatile("" : "+r"(w[k]));
+            const float x = mine ? __uint_as_float(v[k]) * f_mine : 0.0f;
+            v[k] = __float_as_uint(others ? fmaf(__uint_as_float(w[k]), f_other, x) : x);
+          }
+        } else {
+          tm_ld32(o_tm + c, v);
+          tm_wait_regs(v);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * f_mine);
+        }
         // columns in order: 0,4,1,5,2,6,3,7 -> 0..7
-        auto y = [&](int k) { return __uint_as_float(v[(k & ~7) + (k & 3) * 2 + ((k >> 2) & 1)]); };
+        auto y = [&](int k) { return v[(k & ~7) + (k & 3) * 2 + ((k >> 2) & 1)]; };
         if (whole) {
+          uint32_t h[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(__uint_as_float(y(2 * k)),
+                                                           __uint_as_float(y(2 * k + 1)));
+            h[k] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          if (live) {
+            if (wide) {
+              stg256(dst + c, h);
+              stg256(dst + c + 16, h + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; k += 4)
+                *reinterpret_cast<uint4*>(dst + c + 2 * k) =
+                    make_uint4(h[k], h[k + 1], h[k + 2], h[k + 3]);
+            }
+          }
+        } else if (live) {
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
-            uint32_t h[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const __nv_bfloat162 x =
-                  __floats2bfloat162_rn(y(k + 2 * q) * inv, y(k + 2 * q + 1) * inv);
-              h[q] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            sts128(mine + k * 2, make_uint4(h[0], h[1], h[2], h[3]));
-          }
-          flush([&](int, long long to, int piece, uint4 d) {
-            *reinterpret_cast<uint4*>(a.out + to * D + c_at + c + piece * 8) = d;
-          });
-        } else {
-#pragma unroll
-          for (int half = 0; half < 32; half += 16) {
-#pragma unroll
-            for (int k = half; k < half + 16; k += 4)
-              sts128(mine + (k - half) * 4,
-                     make_uint4(__float_as_uint(y(k)), __float_as_uint(y(k + 1)),
-                                __float_as_uint(y(k + 2)), __float_as_uint(y(k + 3))));
-            flush([&](int rr, long long, int piece, uint4 d) {
-              *reinterpret_cast<uint4*>(part + (size_t)(pr - lane + rr) * D + c_at + c + half +
-                                        piece * 4) = d;
-            });
+            const uint32_t h[8] = {y(k), y(k + 1), y(k + 2), y(k + 3), y(k + 4), y(k + 5), y(k + 6), y(k + 7)};
+            stg256(part + (size_t)pr * D + c + k, h);
           }
         }
       }
-      if (!whole && (NT == 2 || wg == 0)) {
+      if (!whole && (halves ? wg == 0 : true)) {
         part[(size_t)C::kRows * D + pr] = top;
         part[(size_t)C::kRows * (D + 1) + pr] = l;
         part[(size_t)C::kRows * (D + 2) + pr] = fac;
       }
-      if (done.blk0 == 0 && !whole && tid == 0)  // begun here; it goes on at the next share's start
-        cuts[blockIdx.x] = Cut{(int)(blockIdx.x + (done.rest + s_share - 1) / s_share), ri.start, ri.n,
-                               done.tok0, done.kvh, {}};
+      n_blocks += u.blk1 - u.blk0;
+      if (u.last >= 0 && tid == 0)
+        cuts[blockIdx.x] = Cut{u.last, u.start, min(u.n, u.tok0 + tok), u.tok0, u.kvh, {}};
       tc_before();
-      __syncwarp();
+      give(n_u);
     }
   } else if (wid < kMmaWarp) {
     // ------------- keys (warps 8-15) and values (16-23): a thread per key and half of the columns
@@ -919,23 +956,31 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       uint4 code[KC];
       uint32_t meta[KG];  // scale | bias << 16
       uint32_t n = 0;     // blocks written
-      while (next_unit<D, View>(walk, a, r, tok, u)) {
-        const int len = walk.row.len;
-        Sight sight = {};
-        if constexpr (View) sight = sight_of(a, u.low);
-        const int32_t* table = a.kv.block_table + (int64_t)walk.b * a.kv.max_blocks;
+      for (uint32_t n_u = 0; take(n_u); ++n_u) {
+        const Job& u = s_job[n_u % kJobs];
+        const int len = u.len, blk0 = u.blk0, blk1 = u.blk1, low = u.low;
+        [[maybe_unused]] int sink_keys = 0, gap_keys = 0;
+        if constexpr (View) {
+          sink_keys = u.gap ? sight_of(a, 0).sink_tiles * kTile : 0;
+          gap_keys = u.gap * kTile;
+        }
+        const int32_t* table = a.kv.block_table + (int64_t)u.b * a.kv.max_blocks;
         const uint8_t* pool = static_cast<const uint8_t*>(a.kv.pool) +
                               (int64_t)u.kvh * (P / kTile) * tile_bytes(D);
         const int64_t stride = (int64_t)K * (P / kTile) * tile_bytes(D);
+        bool lost = false;  // what tile_at found last: the tile's block id lies outside the pool
         auto tile_at = [&](int i) -> const uint8_t* {  // the key's tile; null: it is not there
+          lost = false;
           int j = i * kKeys + key;
-          if constexpr (View) j = sight.tile(j / kTile) * kTile + in_tile;
-          if (i >= u.blk1 || j >= len) return nullptr;
+          if constexpr (View)
+            if (j >= sink_keys) j += gap_keys;
+          if (i >= blk1 || j >= len) return nullptr;
           // (the window's begin within a tile, and behind the sinks: nothing is read there)
-          if (View && j < u.low && j >= a.sinks) return nullptr;
+          if (View && j < low && j >= a.sinks) return nullptr;
           const int block = table[j >> p_shift];
           if ((unsigned)block >= (unsigned)a.kv.num_blocks) {
             if (!kValues) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
+            lost = true;
             return nullptr;
           }
           return pool + block * stride + (j & (P - 1)) / kTile * tile_bytes(D);
@@ -956,11 +1001,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             }
           }
         };
-        load(tile_at(u.blk0));
-        const uint8_t* next = tile_at(u.blk0 + 1);
-        for (int i = u.blk0; i < u.blk1; ++i) {
-          if (n >= S) wait_all(&freed[(n - S) & 1u], (n - S) >> 1, s_stop);
-          const uint32_t to = room + n % S * C::kBlockBytes + key * 128;
+        // The values' side, which is the last to be needed, brings the queries of the units behind
+        // the first one: their buffer is free once the last scores of the unit before are there.
+        if (kValues && n_u > 0) {
+          wait_all(&q_free, n_u - 1, s_stop);
+          load_queries(std::integral_constant<int, 4>{}, wid - kSoftWarps - kSideWarps, n_u);
+        }
+        load(tile_at(blk0));
+        bool lost_now = lost;
+        const uint8_t* next = tile_at(blk0 + 1);
+        for (int i = blk0; i < blk1; ++i) {
+          const int st = n % S;
+          if (n >= S) wait_all(&freed[st], n / S - 1, s_stop);
+          const uint32_t to = room + st * C::kBlockBytes + key * 128;
 #pragma unroll
           for (int c = 0; c < KC; ++c) {
             const int chunk = half * KC + c, g = D == 256 ? c / 2 : 0;
@@ -972,39 +1025,49 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             for (int k = 0; k < 4; ++k)
               sts128(at + ((((chunk & 1) * 4 + k) ^ (key & 7)) << 4), dequant8(w[k], sc, bi));
           }
+          if (!kValues && half == 0) {
+            const uint32_t gone = __ballot_sync(~0u, lost_now);
+            if (lane == 0)
+              reinterpret_cast<uint8_t*>(&s_miss[n & 3u])[key >> 5] = (uint8_t)((gone & 1u) | (gone >> 15 & 2u));
+          }
           fence_async();
           __syncwarp();
-          if (lane == 0) sc::bar_arrive(su32(&full[n % S]));
+          if (lane == 0) sc::bar_arrive(su32(&full[st]));
           ++n;
+          lost_now = lost;
           // (not before the fence, which would wait for them)
           load(next);
           next = tile_at(i + 2);
         }
+        give(n_u);
       }
     };
-    // a buffer is free when the scores (the product) of its block are over
+    // (a buffer is free when the scores, or the products, of its block are over)
     if (wid < kSoftWarps + kSideWarps)
-      side(std::false_type{}, k_at, k_full, s_full[NT - 1]);
+      side(std::false_type{}, k_at, k_full, k_free);
     else
-      side(std::true_type{}, v_at, v_full, o_done[NT - 1]);
+      side(std::true_type{}, v_at, v_full, v_free);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
     if (wid == kMmaWarp) {
       // -------------------------------------------------------------------- MMAs
-      uint32_t n_u = 0, n_k = 0, n_p = 0;  // units; blocks scored, and multiplied
+      uint32_t n_k = 0, n_v = 0;                  // blocks of keys and values used
+      uint32_t n_s[NT] = {}, n_p[NT] = {};        // each tile's scores and products
       const bool leader = elect_one();
       // descriptors: a byte offset moves them by a sixteenth
       const uint64_t dq = smem_desc(q_at, 16), dk = smem_desc(k_at, 16);
       const uint64_t dv = smem_desc(v_at, kKeys * 128);
-      // A tile's scores of block n_k go where the weights of the block before (two blocks before,
-      // with one tile) were: their product has to be over, as MMAs of other accumulators are not
-      // ordered by themselves.
-      auto scores = [&](int tile) {
-        const int slot = NT == 1 ? (int)(n_k & 1u) : tile, st = n_k % S;
-        const uint64_t da = dq + tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
+      // A tile's scores go where the weights of its block before (two blocks before, with one
+      // tile) were: their product has to be over, as MMAs of other accumulators are not ordered by
+      // themselves.
+      // (first, last: of the tiles that use the block; end: of the unit's scores)
+      auto scores = [&](auto tile_tag, int q_tile, bool first, bool last, bool end) {
+        constexpr int tile = decltype(tile_tag)::value;
+        const int slot = NT == 1 ? (int)(n_s[tile] & 1u) : tile, st = n_k % S;
+        const uint64_t da = dq + q_tile * (C::kBlockBytes / 16), db = dk + st * (C::kBlockBytes / 16);
         // (the wait that is over first comes first: it is not on the way then)
-        if (tile == 0) wait_all(&k_full[st], n_k / S, s_stop);
-        if (n_p > 0) wait_all(&o_done[tile][(n_p - 1) & 1u], (n_p - 1) >> 1, s_stop);
+        if (first) wait_all(&k_full[st], n_k / S, s_stop);
+        if (n_p[tile] > 0) wait_all(&o_done[tile][(n_p[tile] - 1) & 1u], (n_p[tile] - 1) >> 1, s_stop);
         tc_after();
         if (leader) {
 #pragma unroll
@@ -1012,14 +1075,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             const int off = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) / 16;
             mma_ss(tmem + C::kS + slot * 128, da + off, db + off, C::kIdescS, k > 0);
           }
-          commit(su32(&s_full[tile][n_k & 1u]));
+          commit(su32(&s_full[tile][n_s[tile] & 1u]));
+          if (last) commit(su32(&k_free[st]));
+          if (end) commit(su32(&q_free));
         }
         __syncwarp();
+        ++n_s[tile];
+        n_k += last;
       };
-      auto product = [&](int tile, uint32_t n, bool more) {
-        const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n % S;
+      auto product = [&](auto tile_tag, bool first, bool last, bool more) {
+        constexpr int tile = decltype(tile_tag)::value;
+        const uint32_t n = n_p[tile];
+        const int slot = NT == 1 ? (int)(n & 1u) : tile, st = n_v % S;
         const uint64_t db = dv + st * (C::kBlockBytes / 16);
-        if (tile == 0) wait_all(&v_full[st], n / S, s_stop);
+        if (first) wait_all(&v_full[st], n_v / S, s_stop);
         wait_all(&p_full[tile][n & 1u], n >> 1, s_stop);
         tc_after();
         if (leader) {
@@ -1028,41 +1097,101 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             mma_ts(tmem + tile * C::kO, tmem + C::kS + slot * 128 + k * 8, db + k * (2048 / 16),
                    C::kIdescO, more || k > 0);
           commit(su32(&o_done[tile][n & 1u]));
+          if (last) commit(su32(&v_free[st]));
         }
         __syncwarp();
+        ++n_p[tile];
+        n_v += last;
       };
-      auto stopped = [&] { return __any_sync(~0u, s_stop) != 0; };
-      while (next_unit<D, View>(walk, a, r, tok, u)) {
-        wait_all(&q_full, n_u++, s_stop);
+      using T0 = std::integral_constant<int, 0>;
+      using T1 = std::integral_constant<int, NT - 1>;
+      for (uint32_t n_u = 0; take(n_u); ++n_u) {
+        const Job& u = s_job[n_u % kJobs];
         const int nb = u.blk1 - u.blk0;
+        wait_all(&q_full[n_u & 1u], n_u >> 1, s_stop);
         if constexpr (NT == 1) {
           for (int i = 0; i <= nb && !stopped(); ++i) {
-            if (i < nb) {
-              scores(0);
-              ++n_k;
-            }
-            if (i > 0) product(0, n_p++, i > 1);
+            if (i < nb) scores(T0{}, 0, true, true, i + 1 == nb);
+            if (i > 0) product(T0{}, true, true, i > 1);
           }
         } else {
-          scores(0);
-          scores(1);
-          ++n_k;
-          for (int i = 0; i < nb && !stopped(); ++i) {
-            product(0, n_p, i > 0);
-            ++n_p;
-            if (i + 1 < nb) scores(0);
-            product(1, n_p - 1, i > 0);
-            if (i + 1 < nb) {
-              scores(1);
-              ++n_k;
-            }
+          // the tiles in turn, each its scores two steps ahead of the other's product
+          const int steps = Split ? nb : 2 * nb;
+          scores(T0{}, 0, true, Split, steps == 1);
+          if (steps > 1) scores(T1{}, Split ? 0 : 1, Split, true, steps == 2);
+          for (int i = 0; i < steps && !stopped(); i += 2) {
+            product(T0{}, true, Split, i > 0);
+            if (i + 2 < steps) scores(T0{}, 0, true, Split, i + 3 == steps);
+            if (i + 1 < steps) product(T1{}, Split, true, i > 0);
+            if (i + 3 < steps) scores(T1{}, Split ? 0 : 1, Split, true, i + 4 == steps);
           }
         }
-        if (stopped()) break;
+        give(n_u);
       }
       if (leader) commit(su32(&drained));  // nothing is under way when TMEM goes back
       __syncwarp();
       if (!__all_sync(~0u, bar_wait(su32(&drained), 0))) s_stop = 1;
+    } else if (wid == kMmaWarp + 1) {
+      // ----------------------------------------------------- the walk, a job ahead of the others
+      Walk w;
+      w.left = 0;
+      if (a.rows <= 32) {  // a lane per row
+        long long cost = 0;
+        if (lane < a.rows) cost = row_cost(row_info<View>(a, lane, r, tok));
+        long long v = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(~0u, v, o);
+          if (lane >= o) v += x;
+        }
+        total = __shfl_sync(~0u, v, 31);
+        const long long x0 = blockIdx.x * share_of();
+        if (x0 < v && x0 >= v - cost) {
+          s_row = lane;
+          s_at = x0 - (v - cost);
+        }
+        __syncwarp();
+      }
+      if (s_row >= 0) {
+        w.share = share_of();
+        w.b = s_row;
+        w.row = row_info<View>(a, w.b, r, tok);
+        w.costs = costs_of<View>(a, w.row, tok);
+        w.left = min(w.share, total - blockIdx.x * w.share);
+        const long long per_head = cost_before<D, View>(w.costs, w.row.tiles);
+        long long x = s_at;
+        w.kvh = (x | per_head) >> 31 ? (int)(x / per_head) : (int)x / (int)per_head;
+        x -= w.kvh * per_head;
+        // the last unit whose cost_before is <= x, a lane per candidate
+        int lo = 0, count = w.row.tiles;
+        while (count > 1) {
+          const int step = (count + 31) / 32, j = lo + lane * step;
+          const bool fits = lane * step < count && cost_before<D, View>(w.costs, j) <= x;
+          const int k = 31 - __clz(__ballot_sync(~0u, fits));
+          lo += k * step;
+          count = min(step, count - k * step);
+        }
+        w.j = lo;
+        w.at = x - cost_before<D, View>(w.costs, lo);
+      }
+      for (uint32_t k = 0;; ++k) {
+        Job u = {};
+        u.more = next_unit<D, View>(w, a, r, tok, u) ? 1 : 0;
+        if (k >= kJobs) wait_all(&job_free[k % kJobs], k / kJobs - 1, s_stop);
+        if (lane == 0) {
+          s_job[k % kJobs] = u;
+          sc::bar_arrive(su32(&job_full[k % kJobs]));
+        }
+        __syncwarp();
+        if (!u.more || stopped()) break;
+        // its queries come to L2
+        const int tokens = min(tok, u.n - u.tok0);
+        for (int i = lane; i < tokens * (r * D / 64); i += 32) {
+          const int t = i / (r * D / 64), c = i % (r * D / 64);
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(
+              a.q + ((int64_t)(u.start + u.tok0 + t) * a.heads + u.kvh * r) * D + c * 64));
+        }
+      }
     }
   }
   tc_before();
@@ -1089,7 +1218,7 @@ __global__ void __launch_bounds__(512) combine_kernel(AttnArgs a) {
   if (cut.last <= first) return;
   const int r = a.heads / a.kv.kv_heads, per_tile = 128 / r, in = row & 127;
   const int t = cut.tok0 + (row >> 7) * per_tile + in / r;
-  if (in >= per_tile * r || t >= cut.n) return;
+  if (in >= per_tile * r || t >= cut.end) return;
   const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kCutBytes);
   float m = kNone, l = 0.0f;  // (raw scores, as the parts have them)
   const float fac = parts[((size_t)first * 2 + 1) * C::kPartial + (size_t)C::kRows * (D + 2) + row];
@@ -1115,15 +1244,22 @@ __global__ void __launch_bounds__(512) combine_kernel(AttnArgs a) {
                                             *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <int D, bool View>
-cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+template <int D, bool View, bool Split>
+cudaError_t launch_kernel(const AttnArgs& a, cudaStream_t st) {
   using C = Cfg<D>;
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, View>,
+  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, View, Split>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e == cudaSuccess)
-    e = launch_pdl(prompt_kernel<D, View>, dim3(kGrid), dim3(kThreads), C::kSmem, st, a);
+    e = launch_pdl(prompt_kernel<D, View, Split>, dim3(kGrid), dim3(kThreads), C::kSmem, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(combine_kernel<D>, dim3(kGrid, C::kRows * D / 2048), dim3(512), 0, st, a);
+}
+
+template <int D, bool View>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  if constexpr (View && Cfg<D>::kTiles == 2)
+    if ((int64_t)a.max_new * (a.heads / a.kv.kv_heads) <= 128) return launch_kernel<D, View, true>(a, st);
+  return launch_kernel<D, View, false>(a, st);
 }
 
 template <int D>
