@@ -234,7 +234,7 @@ size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t 
     set_error(MOE_EINVAL, "rows must be >= 1 and T >= 0");
     return 0;
   }
-  return moe::kv::attn_workspace_bytes(*kv, rows, T, heads, max_new);
+  return moe::kv::attn_workspace_bytes(*kv, heads, max_new, true);
 }
 
 static int attention(const moe_kv* kv, const moe_kv_batch* batch, const moe_kv_view* view,
@@ -255,7 +255,7 @@ static int attention(const moe_kv* kv, const moe_kv_batch* batch, const moe_kv_v
     return set_error(MOE_EINVAL, "q and out (16 B) and workspace (256 B) alignment");
   if (!(scale > 0.0f) || scale > 3.0e38f)
     return set_error(MOE_EINVAL, "scale must be finite and > 0");
-  const size_t need = moe::kv::attn_workspace_bytes(*kv, rows, T, heads, max_new);
+  const size_t need = moe::kv::attn_workspace_bytes(*kv, heads, max_new, view != nullptr);
   if (workspace_bytes < need)
     return set_error(MOE_ECAPACITY, "workspace %zu < %zu bytes", workspace_bytes, need);
   moe::kv::AttnArgs a = {};

@@ -1,8 +1,8 @@
 // Attention over the 4-bit key/value cache: which kernel takes which rows.
 //
-// Rows of up to decode_cols queries per kv head go through the decode kernel
-// (kv_decode.cuh), longer ones through the prompt kernel (kv_prompt.cuh).  The
-// rows' lengths are on the device, so both look at every row and leave the
+// Rows of few queries per kv head (causal: up to decode_cols; with windows and
+// trees: view_decode) go through the decode kernel (kv_decode.cuh), the others
+// through the prompt kernel (kv_prompt.cuh).  The rows' lengths are on the device, so both look at every row and leave the
 // other's alone; the prompt kernel is launched only where max_new allows a long
 // row.  Both exist twice: for causal attention, and with windows and trees (View).
 #include "kv_common.cuh"
@@ -10,19 +10,26 @@
 namespace moe {
 namespace kv {
 
-static bool may_have_prompts(const moe_kv& kv, int heads, int max_new) {
-  return (int64_t)max_new * (heads / kv.kv_heads) > decode_cols(kv.head_dim);
+static bool may_have_prompts(const moe_kv& kv, int heads, int max_new, bool view) {
+  return (int64_t)max_new * (heads / kv.kv_heads) > (view ? view_cols(kv.head_dim) : decode_cols(kv.head_dim));
 }
 
-size_t attn_workspace_bytes(const moe_kv& kv, int, int, int heads, int max_new) {
+size_t attn_workspace_bytes(const moe_kv& kv, int heads, int max_new, bool view) {
   return decode_workspace_bytes(kv.head_dim) +
-         (may_have_prompts(kv, heads, max_new) ? prompt_workspace_bytes(kv.head_dim) : 0);
+         (may_have_prompts(kv, heads, max_new, view) ? prompt_workspace_bytes(kv.head_dim) : 0);
 }
 
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
   const bool view = a.window > 0 || a.tree;
   const cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
-  if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new)) return e;
+  if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new, view)) return e;
+  if (view) {
+    // where the longest row that there can be is the decode kernel's, every row is
+    int64_t tiles = (int64_t)a.kv.max_blocks * (a.kv.block_tokens / kTile);
+    if (a.window > 0) tiles = min(tiles, ((int64_t)a.window + a.max_new + a.sinks) / kTile + 3);
+    const int64_t cols = (int64_t)a.max_new * (a.heads / a.kv.kv_heads);
+    if (view_decode(a.kv.head_dim, a.kv.kv_heads, a.rows, cols, tiles)) return e;
+  }
   AttnArgs p = a;
   p.ws = static_cast<char*>(a.ws) + decode_workspace_bytes(a.kv.head_dim);
   return view ? launch_prompt_view(p, st) : launch_prompt(p, st);

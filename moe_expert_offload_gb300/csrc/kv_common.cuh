@@ -120,11 +120,51 @@ __device__ __forceinline__ Sight sight_of(const AttnArgs& a, int first) {
   s.gap = max(0, max(first, 0) / kTile - s.sink_tiles);
   return s;
 }
+// Key tiles that the decode kernel walks over for a row in all, its units' fixed cost among them.
+__host__ __device__ constexpr int decode_warps(int D) { return D == 256 ? 8 : 16; }
+__host__ __device__ constexpr int decode_unit_cost(int D) { return D == 64 ? 8 : 4; }
+__host__ __device__ inline long long decode_work(int D, int kv_heads, long long cols, long long tiles) {
+  return kv_heads * ((cols + 7) / 8) * (tiles + decode_unit_cost(D));
+}
+// With windows and trees, by both numbers: rows of up to view_cols columns go through the decode
+// kernel, and longer ones where a batch of such rows is little work, up to view_tiles key tiles for
+// each of its warps (microseconds, decode | prompt; trees without a window, rows x keys):
+//   head_dim 256, 8 heads on one of 2    16 columns   24        64        256
+//     1 x 2000                          14 | 22   14 | 23    15 | 25   22 | 28
+//     16 x 1000                         17 | 26   19 | 26    32 | 28  100 | 37
+//     64 x 4000                         66 | 89   90 | 89   205 | 93  743 | 162
+//   head_dim 128, 8 on one of 4
+//     1 x 2000                          16 | 20   16 | 20    17 | 23   22 | 29
+//     16 x 1000                         19 | 28   20 | 28    33 | 29   88 | 40
+//     64 x 4000                         70 | 113  96 | 112  222 | 116 794 | 148
+//   head_dim 64, 8 on one of 8
+//     1 x 2000                          14 | 20   15 | 20    15 | 21   24 | 26
+//     16 x 1000                         19 | 28   23 | 27    39 | 29  105 | 39
+//     64 x 4000                         79 | 139 108 | 138  246 | 141 883 | 203
+__host__ __device__ constexpr int view_cols(int D) { return D == 256 ? 16 : D == 128 ? 24 : 32; }
+__host__ __device__ constexpr int view_tiles(int D) { return D == 256 ? 10 : D == 128 ? 8 : 12; }
+__host__ __device__ inline bool view_decode(int D, int kv_heads, int rows, long long cols,
+                                            long long tiles) {
+  return cols <= view_cols(D) || decode_work(D, kv_heads, cols, tiles) * rows <=
+                                     (long long)view_tiles(D) * kGrid * decode_warps(D);
+}
+
+// Whether a row of n new tokens is the decode kernel's.
+template <bool View>
+__device__ __forceinline__ bool takes_decode(const AttnArgs& a, int n, int len, int r) {
+  if constexpr (View) {
+    const int gap = a.window > 0 ? sight_of(a, len - n - a.window + 1).gap : 0;
+    return view_decode(a.kv.head_dim, a.kv.kv_heads, a.rows, (long long)n * r, (len + kTile - 1) / kTile - gap);
+  }
+  return (long long)n * r <= decode_cols(a.kv.head_dim);
+}
+
 // of 16 keys, those below the x-th
 __device__ __forceinline__ uint32_t below16(int x) {
   return x >= 16 ? 0xFFFFu : x <= 0 ? 0u : (1u << x) - 1u;
 }
-size_t attn_workspace_bytes(const moe_kv& kv, int rows, int T, int heads, int max_new);
+// for either kind of call, or (view false) for causal ones
+size_t attn_workspace_bytes(const moe_kv& kv, int heads, int max_new, bool view);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
 size_t decode_workspace_bytes(int D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st);

@@ -66,7 +66,7 @@ using sc::warp_wait;
 // head_dim 128, 96 at 256).
 template <int D>
 struct Cfg {
-  static constexpr int kWarps = D == 256 ? 8 : 16;
+  static constexpr int kWarps = decode_warps(D);
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kTiles = D == 64 ? 4 : 2;  // key tiles of a stage
   static constexpr int kStageBytes = kTiles * tile_bytes(D);
@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr int kPartial = kCols * (D + 3);  // floats: o [col][D], m, l, fac [col]
   // a unit's fixed cost, in key tiles (100 rows of up to 1000 keys, us at half of it, at it and at
   // twice: head_dim 64 16.9, 16.5, 16.5; 128 30.8, 29.0, 29.0; 256 25.2, 22.3, 22.9)
-  static constexpr int kUnitCost = D == 64 ? 8 : 4;
+  static constexpr int kUnitCost = decode_unit_cost(D);
   static constexpr int kCentre = 16 / kTiles;       // stages between two moves of the mean
   static constexpr size_t kSmem = (size_t)kWarps * kWarpBytes + 128;
   static_assert(kPartial * 4 <= kStages * kStageBytes, "a partial fits its warp's ring");
@@ -125,7 +125,7 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int b, int r, int
     return i;
   }
   set_tiles<View>(a, i);
-  if (i.n * r <= decode_cols(a.kv.head_dim)) i.ntb = (i.n * r + cols - 1) / cols;
+  if (takes_decode<View>(a, i.n, i.len, r)) i.ntb = (i.n * r + cols - 1) / cols;
   return i;
 }
 

@@ -134,7 +134,7 @@ __device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok
   // (the decode kernel, which sees every row, reports what does not fit)
   if (i.n <= 0 || i.start < 0 || i.n > a.max_new || i.n > i.len ||
       (long long)i.len > (long long)a.kv.max_blocks * a.kv.block_tokens ||
-      (long long)i.start + i.n > a.T || (long long)i.n * r <= decode_cols(a.kv.head_dim))
+      (long long)i.start + i.n > a.T || takes_decode<View>(a, i.n, i.len, r))
     return i;
   i.tiles = (i.n + tok - 1) / tok;
   return i;
@@ -174,7 +174,7 @@ __device__ __forceinline__ long long cost_before(const Costs& c, int j) {
 }
 
 // A unit, or a CTA's share of one, as it is handed to the roles.
-struct Job {
+struct __align__(16) Job {
   int more;                // 0: there are no more units
   int b, start, n, len;    // its row
   int kvh, tok0;           // kv head, first token
@@ -570,13 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   };
   // A unit's queries by eight warps, of which this is one: a warp's rows, 8 columns a lane, some
   // loads under way at a time.
-  auto load_queries = [&](auto at_once_tag, int warp, uint32_t n_u) {
-    constexpr int kWarps = kSoftWarps, kDeep = decltype(at_once_tag)::value;
+  auto load_queries = [&](auto deep_tag, int warp, uint32_t n_u) {
+    constexpr int kWarps = kSoftWarps;
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kRounds = 128 * kUnitTiles / kWarps / kAtOnce;
-    constexpr uint32_t kGroup = kLanes == 32 ? ~0u : (1u << kLanes) - 1u;
+    constexpr int kMost = decltype(deep_tag)::value, kDeep = kRounds < kMost ? kRounds : kMost;
     static_assert(kRounds % kDeep == 0, "whole batches");
     const Job& u = s_job[n_u % kJobs];
-    const uint32_t group = kGroup << (lane / kLanes * kLanes);
     const int col8 = lane % kLanes;
     const int n = u.n, tok0 = u.tok0;
     const uint16_t* src = a.q + ((int64_t)(u.start + tok0) * a.heads + u.kvh * r) * D + col8 * 8;
@@ -590,6 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         if (in < per_tile * r && tok0 + t < n)
           raw[i] = *reinterpret_cast<const uint4*>(src + ((int64_t)t * a.heads + in - i_tok * r) * D);
       }
+      // (the buffer is free once the last scores of the unit before are there)
+      if (i0 == 0 && n_u > 0) wait_all(&q_free, n_u - 1, s_stop);
 #pragma unroll
       for (int i = 0; i < kDeep; ++i) {
         const int qr = (warp * kRounds + i0 + i) * kAtOnce + lane / kLanes, in = qr & 127;
@@ -597,7 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         uint32_t big = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) big = __vmaxu2(big, w[k] & 0x7FFF7FFFu);
-        big = __reduce_max_sync(group, max(big & 0xFFFFu, big >> 16));
+        big = max(big & 0xFFFFu, big >> 16);
+        if constexpr (kLanes == 32) {
+          big = __reduce_max_sync(~0u, big);
+        } else {
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(~0u, big, o));
+        }
         const int e = max((int)(big >> 7) - 127, -100);  // 2^e <= largest < 2^(e+1)
         const float up = pow2(14 - e);
         float x[8];
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     [[maybe_unused]] uint32_t n_blocks = 0;  // of the units before
     bool have = take(0);
     // (idle as yet, these warps bring the first unit's queries)
-    if (have) load_queries(std::integral_constant<int, D == 64 ? 4 : 8>{}, wid, 0);
+    if (have) load_queries(std::integral_constant<int, 8>{}, wid, 0);
     // (every softmax warp leaves at the same unit: they meet at barriers on the way)
     for (; !any_of_256(!have); ++n_u) {
       const Job& u = s_job[n_u % kJobs];
@@ -1001,12 +1008,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             }
           }
         };
-        // The values' side, which is the last to be needed, brings the queries of the units behind
-        // the first one: their buffer is free once the last scores of the unit before are there.
-        if (kValues && n_u > 0) {
-          wait_all(&q_free, n_u - 1, s_stop);
+        // (the values' side, which is the last to be needed, brings the queries of the units
+        // behind the first one)
+        // (eight loads under way spill what its loop over the blocks needs: 853 us instead of 779 for
+        // 2048 tokens on 30000 of head_dim 128)
+        if (kValues && n_u > 0)
           load_queries(std::integral_constant<int, 4>{}, wid - kSoftWarps - kSideWarps, n_u);
-        }
         load(tile_at(blk0));
         bool lost_now = lost;
         const uint8_t* next = tile_at(blk0 + 1);
@@ -1135,34 +1142,43 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       // ----------------------------------------------------- the walk, a job ahead of the others
       Walk w;
       w.left = 0;
+      long long x = 0;  // where the share begins, as a cost within its row
+      w.b = -1;
       if (a.rows <= 32) {  // a lane per row
-        long long cost = 0;
-        if (lane < a.rows) cost = row_cost(row_info<View>(a, lane, r, tok));
+        Row i = {};
+        if (lane < a.rows) i = row_info<View>(a, lane, r, tok);
+        const long long cost = row_cost(i);
         long long v = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long x = __shfl_up_sync(~0u, v, o);
-          if (lane >= o) v += x;
+          const long long y = __shfl_up_sync(~0u, v, o);
+          if (lane >= o) v += y;
         }
         total = __shfl_sync(~0u, v, 31);
         const long long x0 = blockIdx.x * share_of();
-        if (x0 < v && x0 >= v - cost) {
-          s_row = lane;
-          s_at = x0 - (v - cost);
+        const uint32_t here = __ballot_sync(~0u, x0 < v && x0 >= v - cost);
+        if (here) {
+          w.b = __ffs(here) - 1;
+          x = __shfl_sync(~0u, x0 - (v - cost), w.b);
+          w.row.start = __shfl_sync(~0u, i.start, w.b);
+          w.row.n = __shfl_sync(~0u, i.n, w.b);
+          w.row.len = __shfl_sync(~0u, i.len, w.b);
+          w.row.tiles = __shfl_sync(~0u, i.tiles, w.b);
         }
-        __syncwarp();
-      }
-      if (s_row >= 0) {
-        w.share = share_of();
+      } else if (s_row >= 0) {
         w.b = s_row;
+        x = s_at;
         w.row = row_info<View>(a, w.b, r, tok);
+      }
+      if (w.b >= 0) {
+        w.share = share_of();
         w.costs = costs_of<View>(a, w.row, tok);
         w.left = min(w.share, total - blockIdx.x * w.share);
+        // the kv head and the unit that hold it, a lane per candidate
         const long long per_head = cost_before<D, View>(w.costs, w.row.tiles);
-        long long x = s_at;
-        w.kvh = (x | per_head) >> 31 ? (int)(x / per_head) : (int)x / (int)per_head;
+        w.kvh = 0;
+        for (int h = 1; h < K; h += 32) w.kvh += __popc(__ballot_sync(~0u, h + lane < K && (h + lane) * per_head <= x));
         x -= w.kvh * per_head;
-        // the last unit whose cost_before is <= x, a lane per candidate
         int lo = 0, count = w.row.tiles;
         while (count > 1) {
           const int step = (count + 31) / 32, j = lo + lane * step;
@@ -1174,6 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         w.j = lo;
         w.at = x - cost_before<D, View>(w.costs, lo);
       }
+      const int lines = r * D / 64;  // 128 bytes each, of a token's queries
       for (uint32_t k = 0;; ++k) {
         Job u = {};
         u.more = next_unit<D, View>(w, a, r, tok, u) ? 1 : 0;
@@ -1184,12 +1201,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         }
         __syncwarp();
         if (!u.more || stopped()) break;
+        if (k == 0) continue;  // (the first one's are on their way)
         // its queries come to L2
         const int tokens = min(tok, u.n - u.tok0);
-        for (int i = lane; i < tokens * (r * D / 64); i += 32) {
-          const int t = i / (r * D / 64), c = i % (r * D / 64);
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(
-              a.q + ((int64_t)(u.start + u.tok0 + t) * a.heads + u.kvh * r) * D + c * 64));
+        int t = lane / lines, c = lane - t * lines;
+        const int dt = 32 / lines, dc = 32 - dt * lines;
+        const uint16_t* src = a.q + ((int64_t)(u.start + u.tok0) * a.heads + u.kvh * r) * D;
+        while (t < tokens) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(src + (int64_t)t * a.heads * D + c * 64));
+          t += dt;
+          c += dc;
+          if (c >= lines) {
+            c -= lines;
+            ++t;
+          }
         }
       }
     }
