@@ -1,7 +1,7 @@
 // Attention over the 4-bit key/value cache: which kernel takes which rows.
 //
 // Rows of few queries per kv head (causal: up to decode_cols; with windows and
-// trees: view_decode) go through the decode kernel (kv_decode.cuh), the others
+// trees: by the batch's work) go through the decode kernel (kv_decode.cuh), the others
 // through the prompt kernel (kv_prompt.cuh).  The rows' lengths are on the device, so both look at every row and leave the
 // other's alone; the prompt kernel is launched only where max_new allows a long
 // row.  Both exist twice: for causal attention, and with windows and trees (View).
@@ -24,11 +24,13 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
   const cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
   if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new, view)) return e;
   if (view) {
-    // where the longest row that there can be is the decode kernel's, every row is
+    // where rows as long as there can be take less than the prompt kernel's fixed part, all rows
+    // are the decode kernel's
     int64_t tiles = (int64_t)a.kv.max_blocks * (a.kv.block_tokens / kTile);
     if (a.window > 0) tiles = min(tiles, ((int64_t)a.window + a.max_new + a.sinks) / kTile + 3);
     const int64_t cols = (int64_t)a.max_new * (a.heads / a.kv.kv_heads);
-    if (view_decode(a.kv.head_dim, a.kv.kv_heads, a.rows, cols, tiles)) return e;
+    if (kDecodeFixed + a.rows * decode_cost(a.kv.head_dim, a.kv.kv_heads, cols, tiles) <= kPromptFixed)
+      return e;
   }
   AttnArgs p = a;
   p.ws = static_cast<char*>(a.ws) + decode_workspace_bytes(a.kv.head_dim);

@@ -120,15 +120,30 @@ __device__ __forceinline__ Sight sight_of(const AttnArgs& a, int first) {
   s.gap = max(0, max(first, 0) / kTile - s.sink_tiles);
   return s;
 }
-// Key tiles that the decode kernel walks over for a row in all, its units' fixed cost among them.
 __host__ __device__ constexpr int decode_warps(int D) { return D == 256 ? 8 : 16; }
 __host__ __device__ constexpr int decode_unit_cost(int D) { return D == 64 ? 8 : 4; }
-__host__ __device__ inline long long decode_work(int D, int kv_heads, long long cols, long long tiles) {
-  return kv_heads * ((cols + 7) / 8) * (tiles + decode_unit_cost(D));
+
+// A row's new tokens and keys, if its bounds are consistent.
+struct RowBounds {
+  int start, n, len;
+  bool ok;
+};
+__device__ __forceinline__ RowBounds row_bounds(const AttnArgs& a, int b) {
+  RowBounds i;
+  i.start = a.batch.q_start[b];
+  i.n = a.batch.q_start[b + 1] - i.start;
+  i.len = a.batch.kv_len[b];
+  i.ok = i.start >= 0 && i.n > 0 && i.n <= a.max_new && i.n <= i.len &&
+         (long long)i.len <= (long long)a.kv.max_blocks * a.kv.block_tokens &&
+         (long long)i.start + i.n <= a.T;
+  return i;
 }
-// With windows and trees, by both numbers: rows of up to view_cols columns go through the decode
-// kernel, and longer ones where a batch of such rows is little work, up to view_tiles key tiles for
-// each of its warps (microseconds, decode | prompt; trees without a window, rows x keys):
+
+// With windows and trees, which kernel takes which rows goes by the whole batch: all rows through
+// the decode kernel, all through the prompt kernel, or those of up to view_cols columns and the
+// others, by what takes least time.  Times are modelled (10 ps a key tile of a unit, a fixed part),
+// with the numbers that choose best among the measured shapes (microseconds, decode | prompt; trees
+// without a window, rows x keys; 224 shapes: 0.5% above the faster one on average, 17% at most):
 //   head_dim 256, 8 heads on one of 2    16 columns   24        64        256
 //     1 x 2000                          14 | 22   14 | 23    15 | 25   22 | 28
 //     16 x 1000                         17 | 26   19 | 26    32 | 28  100 | 37
@@ -142,20 +157,86 @@ __host__ __device__ inline long long decode_work(int D, int kv_heads, long long 
 //     16 x 1000                         19 | 28   23 | 27    39 | 29  105 | 39
 //     64 x 4000                         79 | 139 108 | 138  246 | 141 883 | 203
 __host__ __device__ constexpr int view_cols(int D) { return D == 256 ? 16 : D == 128 ? 24 : 32; }
-__host__ __device__ constexpr int view_tiles(int D) { return D == 256 ? 10 : D == 128 ? 8 : 12; }
-__host__ __device__ inline bool view_decode(int D, int kv_heads, int rows, long long cols,
-                                            long long tiles) {
-  return cols <= view_cols(D) || decode_work(D, kv_heads, cols, tiles) * rows <=
-                                     (long long)view_tiles(D) * kGrid * decode_warps(D);
+__host__ __device__ constexpr long long decode_tile_cost(int D) { return D == 256 ? 55 : D == 128 ? 35 : 30; }
+constexpr long long kPromptTileCost = 90;
+__host__ __device__ constexpr int prompt_unit_tiles(int D) { return D == 128 ? 48 : 32; }
+constexpr long long kDecodeFixed = 1750000, kPromptFixed = 2200000, kBothFixed = 900000;
+enum RowsMode { kByColumns, kAllDecode, kAllPrompt };
+
+__host__ __device__ inline long long decode_cost(int D, int kv_heads, long long cols, long long tiles) {
+  return decode_tile_cost(D) * kv_heads * ((cols + 7) / 8) * (tiles + decode_unit_cost(D));
+}
+
+struct BatchCost {
+  long long decode, columns, prompt;  // all rows through one kernel, by columns, through the other
+  bool few, many;                     // rows of up to view_cols columns, of more
+};
+__device__ __forceinline__ void add_row(const AttnArgs& a, const RowBounds& i, int r, BatchCost& c) {
+  if (!i.ok) return;
+  const int D = a.kv.head_dim, K = a.kv.kv_heads;
+  const int gap = a.window > 0 ? sight_of(a, i.len - i.n - a.window + 1).gap : 0;
+  const long long tiles = (i.len + kTile - 1) / kTile - gap, cols = (long long)i.n * r;
+  const int per_tile = 128 / r, tok = D == 256 || a.max_new * (long long)r <= 128 ? per_tile : 2 * per_tile;
+  const long long d = decode_cost(D, K, cols, tiles);
+  const long long p = kPromptTileCost * K * ((i.n + tok - 1) / tok) * (tiles + prompt_unit_tiles(D));
+  const bool few = cols <= view_cols(D);
+  c.decode += d;
+  c.prompt += p;
+  c.columns += few ? d : p;
+  c.few |= few;
+  c.many |= !few;
+}
+__device__ __forceinline__ int mode_of(const BatchCost& c) {
+  if (!c.many) return kAllDecode;
+  const long long d = kDecodeFixed + c.decode, p = kPromptFixed + c.prompt;
+  const long long m = kPromptFixed + (c.few ? kBothFixed : 0) + c.columns;
+  return d <= p && d <= m ? kAllDecode : m <= p ? kByColumns : kAllPrompt;
+}
+// over a warp's rows, one a lane
+__device__ __forceinline__ BatchCost warp_sum(BatchCost c) {
+  c.many = __any_sync(~0u, c.many);
+  if (!c.many) return c;
+  c.few = __any_sync(~0u, c.few);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    c.decode += __shfl_xor_sync(~0u, c.decode, o);
+    c.columns += __shfl_xor_sync(~0u, c.columns, o);
+    c.prompt += __shfl_xor_sync(~0u, c.prompt, o);
+  }
+  return c;
+}
+// of up to 32 rows, for a warp (i: its lane's row); of more, for a CTA
+__device__ __forceinline__ int warp_mode(const AttnArgs& a, const RowBounds& i, int r) {
+  BatchCost c = {};
+  add_row(a, i, r, c);
+  return mode_of(warp_sum(c));
+}
+__device__ __forceinline__ int block_mode(const AttnArgs& a, int r) {
+  __shared__ unsigned long long s_cost[3];
+  BatchCost c = {};
+  for (int b = threadIdx.x; b < a.rows; b += blockDim.x) add_row(a, row_bounds(a, b), r, c);
+  if (threadIdx.x < 3) s_cost[threadIdx.x] = 0;
+  c.many = __syncthreads_or(c.many) != 0;
+  if (!c.many) return kAllDecode;
+  c.few = __syncthreads_or(c.few) != 0;
+  c = warp_sum(c);
+  if ((threadIdx.x & 31) == 0) {
+    atomicAdd(&s_cost[0], (unsigned long long)c.decode);
+    atomicAdd(&s_cost[1], (unsigned long long)c.columns);
+    atomicAdd(&s_cost[2], (unsigned long long)c.prompt);
+  }
+  __syncthreads();
+  c.decode = (long long)s_cost[0];
+  c.columns = (long long)s_cost[1];
+  c.prompt = (long long)s_cost[2];
+  return mode_of(c);
 }
 
 // Whether a row of n new tokens is the decode kernel's.
 template <bool View>
-__device__ __forceinline__ bool takes_decode(const AttnArgs& a, int n, int len, int r) {
-  if constexpr (View) {
-    const int gap = a.window > 0 ? sight_of(a, len - n - a.window + 1).gap : 0;
-    return view_decode(a.kv.head_dim, a.kv.kv_heads, a.rows, (long long)n * r, (len + kTile - 1) / kTile - gap);
-  }
+__device__ __forceinline__ bool takes_decode(const AttnArgs& a, int n, int r, int mode) {
+  if constexpr (View)
+    return mode == kAllDecode || (mode == kByColumns && (long long)n * r <= view_cols(a.kv.head_dim));
   return (long long)n * r <= decode_cols(a.kv.head_dim);
 }
 

@@ -112,20 +112,18 @@ __device__ __forceinline__ void set_tiles(const AttnArgs& a, RowInfo& i) {
 
 // Row b's bounds, checked; flag: report what does not fit.
 template <bool View>
-__device__ __forceinline__ RowInfo row_info(const AttnArgs& a, int b, int r, int cols, bool flag) {
+__device__ __forceinline__ RowInfo row_info(const AttnArgs& a, const RowBounds& w, int r, int cols,
+                                            int mode, bool flag) {
   RowInfo i = {};
-  i.start = a.batch.q_start[b];
-  i.n = a.batch.q_start[b + 1] - i.start;
-  i.len = a.batch.kv_len[b];
-  if (i.n == 0) return i;
-  if (i.start < 0 || i.n < 0 || i.n > a.max_new || i.n > i.len ||
-      (long long)i.len > (long long)a.kv.max_blocks * a.kv.block_tokens ||
-      (long long)i.start + i.n > a.T) {
-    if (flag) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
+  i.start = w.start;
+  i.n = w.n;
+  i.len = w.len;
+  if (!w.ok) {
+    if (flag && w.n != 0) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);
     return i;
   }
   set_tiles<View>(a, i);
-  if (takes_decode<View>(a, i.n, i.len, r)) i.ntb = (i.n * r + cols - 1) / cols;
+  if (takes_decode<View>(a, i.n, r, mode)) i.ntb = (i.n * r + cols - 1) / cols;
   return i;
 }
 
@@ -263,14 +261,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
   // cost of the rows before each row
   long long total = 0, share = 0;
   const int chunks = (a.rows + C::kThreads - 1) / C::kThreads;
+  [[maybe_unused]] int mode = kByColumns;
+  if (View && a.rows > 32) mode = block_mode(a, r);
   auto share_of = [&] {
     return max((total + (long long)kGrid * W - 1) / ((long long)kGrid * W), (long long)TS);
   };
   if (a.rows <= 32) {
     // up to 32 rows: every warp for itself, a lane per row (1000 keys of one row: 11.4 us, 11.8
     // the other way)
-    RowInfo i = {};
-    if (lane < a.rows) i = row_info<View>(a, lane, r, C::kCols, blockIdx.x == 0 && wid == 0);
+    RowBounds w = {};
+    if (lane < a.rows) w = row_bounds(a, lane);
+    if constexpr (View) mode = warp_mode(a, w, r);
+    const RowInfo i = row_info<View>(a, w, r, C::kCols, mode, blockIdx.x == 0 && wid == 0);
     const long long cost = (long long)K * i.ntb * (i.tiles + C0);
     if (wid == 0) {
       s_rows[0][lane] = i.start;
@@ -299,7 +301,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
       const int b = c * C::kThreads + tid;
       long long cost = 0;
       if (b < a.rows) {
-        const RowInfo i = row_info<View>(a, b, r, C::kCols, pass == 1 && blockIdx.x == 0);
+        const RowInfo i =
+            row_info<View>(a, row_bounds(a, b), r, C::kCols, mode, pass == 1 && blockIdx.x == 0);
         cost = (long long)K * i.ntb * (i.tiles + C0);
         if (chunks == 1) {
           s_rows[0][tid] = i.start;
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     // ---- the walk: units in order, each unit's tiles in stages that end at multiples of the stage
     auto row_of = [&](int b) {
       RowInfo i;
-      if (chunks > 1) return row_info<View>(a, b, r, C::kCols, false);
+      if (chunks > 1) return row_info<View>(a, row_bounds(a, b), r, C::kCols, mode, false);
       i.start = s_rows[0][b];
       i.n = s_rows[1][b];
       i.len = s_rows[2][b];

@@ -124,19 +124,11 @@ __device__ __forceinline__ long long most_keys(const AttnArgs& a, const Row& i, 
   return (long long)a.window + a.sinks + (by_tree<View>(a, i) ? i.n : tok) + 2 * kTile;
 }
 
+// (the decode kernel, which sees every row, reports what does not fit)
 template <bool View>
-__device__ __forceinline__ Row row_info(const AttnArgs& a, int b, int r, int tok) {
-  Row i;
-  i.start = a.batch.q_start[b];
-  i.n = a.batch.q_start[b + 1] - i.start;
-  i.len = a.batch.kv_len[b];
-  i.tiles = 0;
-  // (the decode kernel, which sees every row, reports what does not fit)
-  if (i.n <= 0 || i.start < 0 || i.n > a.max_new || i.n > i.len ||
-      (long long)i.len > (long long)a.kv.max_blocks * a.kv.block_tokens ||
-      (long long)i.start + i.n > a.T || takes_decode<View>(a, i.n, i.len, r))
-    return i;
-  i.tiles = (i.n + tok - 1) / tok;
+__device__ __forceinline__ Row row_info(const AttnArgs& a, const RowBounds& w, int r, int tok, int mode) {
+  Row i = {w.start, w.n, w.len, 0};
+  if (w.ok && !takes_decode<View>(a, w.n, r, mode)) i.tiles = (i.n + tok - 1) / tok;
   return i;
 }
 
@@ -190,6 +182,7 @@ constexpr int kTakers = kSoftWarps + 2 * kSideWarps + 1;  // warps that take job
 struct Walk {
   int b, kvh, j;
   long long at, left, share;  // offset in unit (kvh, j) where the share goes on; what is left of it
+  int mode;
   Row row;
   Costs costs;
 };
@@ -201,7 +194,7 @@ __device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int
     if (w.kvh >= a.kv.kv_heads) {
       do {
         if (++w.b >= a.rows) return false;
-        w.row = row_info<View>(a, w.b, r, tok);
+        w.row = row_info<View>(a, row_bounds(a, w.b), r, tok, w.mode);
       } while (w.row.tiles == 0);
       w.costs = costs_of<View>(a, w.row, tok);
       w.kvh = w.j = 0;
@@ -517,6 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     return i.tiles ? K * cost_before<D, View>(costs_of<View>(a, i, tok), i.tiles) : 0ll;
   };
   const int chunks = (a.rows + kThreads - 1) / kThreads;
+  int mode = kByColumns;
+  if (View && a.rows > 32) mode = block_mode(a, r);
   // Up to 32 rows are the walking warp's own business, a lane per row (below).  More: chunks of
   // kThreads rows, twice over when there is more than one (the total comes first)
   for (int pass = a.rows <= 32 ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
@@ -524,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
       long long cost = 0;
-      if (b < a.rows) cost = row_cost(row_info<View>(a, b, r, tok));
+      if (b < a.rows) cost = row_cost(row_info<View>(a, row_bounds(a, b), r, tok, mode));
       long long v = cost;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -1145,8 +1140,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       long long x = 0;  // where the share begins, as a cost within its row
       w.b = -1;
       if (a.rows <= 32) {  // a lane per row
-        Row i = {};
-        if (lane < a.rows) i = row_info<View>(a, lane, r, tok);
+        RowBounds bounds = {};
+        if (lane < a.rows) bounds = row_bounds(a, lane);
+        if constexpr (View) mode = warp_mode(a, bounds, r);
+        const Row i = row_info<View>(a, bounds, r, tok, mode);
         const long long cost = row_cost(i);
         long long v = cost;
 #pragma unroll
@@ -1168,8 +1165,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       } else if (s_row >= 0) {
         w.b = s_row;
         x = s_at;
-        w.row = row_info<View>(a, w.b, r, tok);
+        w.row = row_info<View>(a, row_bounds(a, w.b), r, tok, mode);
       }
+      w.mode = mode;
       if (w.b >= 0) {
         w.share = share_of();
         w.costs = costs_of<View>(a, w.row, tok);
