@@ -19,7 +19,9 @@ size_t attn_workspace_bytes(const moe_kv& kv, int heads, int max_new, bool view)
          (may_have_prompts(kv, heads, max_new, view) ? prompt_workspace_bytes(kv.head_dim) : 0);
 }
 
-cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch_attention(const AttnArgs& args, cudaStream_t st) {
+  AttnArgs a = args;
+  a.mode = static_cast<int*>(a.ws) + kModeWord;
   const bool view = a.window > 0 || a.tree;
   const cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
   if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new, view)) return e;

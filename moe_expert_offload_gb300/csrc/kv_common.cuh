@@ -104,6 +104,7 @@ struct AttnArgs {
   // below `sinks`; the visibility of trees of up to tree_max tokens, `words` of a token
   int window, sinks, tree_max, words;
   const uint32_t* tree;
+  int* mode;  // which kernel takes which rows (RowsMode): the decode kernel finds it, the prompt kernel reads it
 };
 
 // What a row's new tokens see of its keys, in whole tiles: the first sink_tiles tiles, then those
@@ -122,6 +123,8 @@ __device__ __forceinline__ Sight sight_of(const AttnArgs& a, int first) {
 }
 __host__ __device__ constexpr int decode_warps(int D) { return D == 256 ? 8 : 16; }
 __host__ __device__ constexpr int decode_unit_cost(int D) { return D == 64 ? 8 : 4; }
+
+constexpr int kModeWord = 5;  // of the workspace: in the padding of the decode kernel's first Cut
 
 // A row's new tokens and keys, if its bounds are consistent.
 struct RowBounds {
@@ -207,12 +210,14 @@ __device__ __forceinline__ BatchCost warp_sum(BatchCost c) {
 }
 // of up to 32 rows, for a warp (i: its lane's row); of more, for a CTA
 __device__ __forceinline__ int warp_mode(const AttnArgs& a, const RowBounds& i, int r) {
+  if ((long long)a.max_new * r <= view_cols(a.kv.head_dim)) return kAllDecode;
   BatchCost c = {};
   add_row(a, i, r, c);
   return mode_of(warp_sum(c));
 }
 __device__ __forceinline__ int block_mode(const AttnArgs& a, int r) {
   __shared__ unsigned long long s_cost[3];
+  if ((long long)a.max_new * r <= view_cols(a.kv.head_dim)) return kAllDecode;
   BatchCost c = {};
   for (int b = threadIdx.x; b < a.rows; b += blockDim.x) add_row(a, row_bounds(a, b), r, c);
   if (threadIdx.x < 3) s_cost[threadIdx.x] = 0;

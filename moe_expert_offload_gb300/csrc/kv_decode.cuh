@@ -46,6 +46,7 @@
 // 56 bytes a thread at head_dim 64, 128 and 256.  Few keys are latency: 1000 keys of
 // one row 11.6 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
 #pragma once
+#include <cstddef>
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -88,8 +89,9 @@ constexpr float kNone = -1e30f;  // a maximum before the first key: finite, so t
 // The unit that a CTA began and did not end: the last CTA with a part of it
 // (-1: there is none).
 struct Cut {
-  int last, unit, start, n, ntb, pad[3];
+  int last, unit, start, n, ntb, mode, pad[2];  // (mode: RowsMode, for the prompt kernel)
 };
+static_assert(offsetof(Cut, mode) == kModeWord * sizeof(int), "where the prompt kernel reads it");
 constexpr size_t kCutBytes = (kGrid * sizeof(Cut) + 255) / 256 * 256;
 __host__ __device__ inline float* cta_parts(void* ws) {
   return reinterpret_cast<float*>(static_cast<char*>(ws) + kCutBytes);
@@ -236,6 +238,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
   __shared__ __align__(16) Stage s_stage[W][S];
   __shared__ int s_rows[3][C::kThreads];  // start, new tokens, length of the rows, if they fit
   __shared__ long long s_scan[W];
+  __shared__ int s_mode;
   __shared__ long long s_x[W];  // each warp's start: offset in the row
   __shared__ int s_row[W];      // and the row; -1: no work
   // the parts of units left by each warp, the head one (it ends a unit that an
@@ -262,7 +265,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
   long long total = 0, share = 0;
   const int chunks = (a.rows + C::kThreads - 1) / C::kThreads;
   [[maybe_unused]] int mode = kByColumns;
-  if (View && a.rows > 32) mode = block_mode(a, r);
+  if (View && a.rows > 32) {
+    mode = block_mode(a, r);
+    if (tid == 0) s_mode = mode;
+  }
   auto share_of = [&] {
     return max((total + (long long)kGrid * W - 1) / ((long long)kGrid * W), (long long)TS);
   };
@@ -271,7 +277,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     // the other way)
     RowBounds w = {};
     if (lane < a.rows) w = row_bounds(a, lane);
-    if constexpr (View) mode = warp_mode(a, w, r);
+    if constexpr (View) {
+      mode = warp_mode(a, w, r);
+      if (wid == 0) s_mode = mode;
+    }
     const RowInfo i = row_info<View>(a, w, r, C::kCols, mode, blockIdx.x == 0 && wid == 0);
     const long long cost = (long long)K * i.ntb * (i.tiles + C0);
     if (wid == 0) {
@@ -349,6 +358,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     }
   }
 
+  if (View && blockIdx.x == 0 && tid == 0) *a.mode = mode;
+
   bool failed = false;
   if (s_row[wid] >= 0) {
     constexpr int NK = D / 16;  // MMAs along a head
@@ -356,7 +367,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
     // ---- the walk: units in order, each unit's tiles in stages that end at multiples of the stage
     auto row_of = [&](int b) {
       RowInfo i;
-      if (chunks > 1) return row_info<View>(a, row_bounds(a, b), r, C::kCols, mode, false);
+      if (chunks > 1)
+        return row_info<View>(a, row_bounds(a, b), r, C::kCols, View ? s_mode : kByColumns, false);
       i.start = s_rows[0][b];
       i.n = s_rows[1][b];
       i.len = s_rows[2][b];
@@ -969,7 +981,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1) decode_kernel(AttnArgs a)
       if (tid == 0)
         static_cast<Cut*>(a.ws)[blockIdx.x] =
             Cut{begun ? (int)(blockIdx.x + (pt.left + per - 1) / per) : -1, pt.unit, pt.start, pt.n,
-                pt.ntb, {}};
+                pt.ntb, View ? s_mode : 0, {}};
       break;
     }
     from = to;

@@ -510,11 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     return i.tiles ? K * cost_before<D, View>(costs_of<View>(a, i, tok), i.tiles) : 0ll;
   };
   const int chunks = (a.rows + kThreads - 1) / kThreads;
-  int mode = kByColumns;
-  if (View && a.rows > 32) mode = block_mode(a, r);
+  const int mode = View ? *a.mode : kByColumns;
   // Up to 32 rows are the walking warp's own business, a lane per row (below).  More: chunks of
   // kThreads rows, twice over when there is more than one (the total comes first)
-  for (int pass = a.rows <= 32 ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
+  for (int pass = a.rows <= 32 || mode == kAllDecode ? 2 : chunks > 1 ? 0 : 1; pass < 2; ++pass) {
     long long carry = 0;
     for (int c = 0; c < chunks; ++c) {
       const int b = c * kThreads + tid;
@@ -1139,10 +1138,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       w.left = 0;
       long long x = 0;  // where the share begins, as a cost within its row
       w.b = -1;
-      if (a.rows <= 32) {  // a lane per row
+      if (mode == kAllDecode) {  // nothing to do
+      } else if (a.rows <= 32) {  // a lane per row
         RowBounds bounds = {};
         if (lane < a.rows) bounds = row_bounds(a, lane);
-        if constexpr (View) mode = warp_mode(a, bounds, r);
         const Row i = row_info<View>(a, bounds, r, tok, mode);
         const long long cost = row_cost(i);
         long long v = cost;
