@@ -23,20 +23,24 @@ cudaError_t launch_attention(const AttnArgs& args, cudaStream_t st) {
   AttnArgs a = args;
   a.mode = static_cast<int*>(a.ws) + kModeWord;
   const bool view = a.window > 0 || a.tree;
-  const cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
-  if (e != cudaSuccess || !may_have_prompts(a.kv, a.heads, a.max_new, view)) return e;
-  if (view) {
-    // where rows as long as there can be take less than the prompt kernel's fixed part, all rows
-    // are the decode kernel's
+  bool prompts = may_have_prompts(a.kv, a.heads, a.max_new, view);
+  if (view && prompts) {
+    // where rows as long as there can be take the decode kernel less than the prompt kernel's fixed
+    // part, all rows are its own
     int64_t tiles = (int64_t)a.kv.max_blocks * (a.kv.block_tokens / kTile);
     if (a.window > 0) tiles = min(tiles, ((int64_t)a.window + a.max_new + a.sinks) / kTile + 3);
-    const int64_t cols = (int64_t)a.max_new * (a.heads / a.kv.kv_heads);
-    if (kDecodeFixed + a.rows * decode_cost(a.kv.head_dim, a.kv.kv_heads, cols, tiles) <= kPromptFixed)
-      return e;
+    const int64_t r = a.heads / a.kv.kv_heads;
+    const int64_t units = min(a.rows * ((a.max_new * r + 7) / 8), (a.T * r + a.rows * (int64_t)7) / 8);
+    prompts = kDecodeAlone + decode_cost(a.kv.head_dim, a.kv.kv_heads, units, tiles) > kPromptFixed;
   }
+  a.prompts = prompts;
   AttnArgs p = a;
   p.ws = static_cast<char*>(a.ws) + decode_workspace_bytes(a.kv.head_dim);
-  return view ? launch_prompt_view(p, st) : launch_prompt(p, st);
+  cudaError_t e = view ? launch_decode_view(a, st) : launch_decode(a, st);
+  if (e == cudaSuccess && prompts) e = view ? launch_prompt_view(p, st) : launch_prompt(p, st);
+  if (e == cudaSuccess) e = launch_decode_join(a, st);
+  if (e == cudaSuccess && prompts) e = launch_prompt_join(p, st);
+  return e;
 }
 
 }  // namespace kv

@@ -104,6 +104,7 @@ struct AttnArgs {
   // below `sinks`; the visibility of trees of up to tree_max tokens, `words` of a token
   int window, sinks, tree_max, words;
   const uint32_t* tree;
+  int prompts;  // 0: all rows are the decode kernel's
   int* mode;  // which kernel takes which rows (RowsMode): the decode kernel finds it, the prompt kernel reads it
 };
 
@@ -163,11 +164,13 @@ __host__ __device__ constexpr int view_cols(int D) { return D == 256 ? 16 : D ==
 __host__ __device__ constexpr long long decode_tile_cost(int D) { return D == 256 ? 55 : D == 128 ? 35 : 30; }
 constexpr long long kPromptTileCost = 90;
 __host__ __device__ constexpr int prompt_unit_tiles(int D) { return D == 128 ? 48 : 32; }
-constexpr long long kDecodeFixed = 1750000, kPromptFixed = 2200000, kBothFixed = 900000;
+// (a call that launches the prompt kernel and has no row for it, and one that does not)
+constexpr long long kDecodeFixed = 1950000, kDecodeAlone = 1350000;
+constexpr long long kPromptFixed = 2200000, kBothFixed = 900000;
 enum RowsMode { kByColumns, kAllDecode, kAllPrompt };
 
-__host__ __device__ inline long long decode_cost(int D, int kv_heads, long long cols, long long tiles) {
-  return decode_tile_cost(D) * kv_heads * ((cols + 7) / 8) * (tiles + decode_unit_cost(D));
+__host__ __device__ inline long long decode_cost(int D, int kv_heads, long long units, long long tiles) {
+  return decode_tile_cost(D) * kv_heads * units * (tiles + decode_unit_cost(D));
 }
 
 struct BatchCost {
@@ -180,7 +183,7 @@ __device__ __forceinline__ void add_row(const AttnArgs& a, const RowBounds& i, i
   const int gap = a.window > 0 ? sight_of(a, i.len - i.n - a.window + 1).gap : 0;
   const long long tiles = (i.len + kTile - 1) / kTile - gap, cols = (long long)i.n * r;
   const int per_tile = 128 / r, tok = D == 256 || a.max_new * (long long)r <= 128 ? per_tile : 2 * per_tile;
-  const long long d = decode_cost(D, K, cols, tiles);
+  const long long d = decode_cost(D, K, (cols + 7) / 8, tiles);
   const long long p = kPromptTileCost * K * ((i.n + tok - 1) / tok) * (tiles + prompt_unit_tiles(D));
   const bool few = cols <= view_cols(D);
   c.decode += d;
@@ -210,14 +213,14 @@ __device__ __forceinline__ BatchCost warp_sum(BatchCost c) {
 }
 // of up to 32 rows, for a warp (i: its lane's row); of more, for a CTA
 __device__ __forceinline__ int warp_mode(const AttnArgs& a, const RowBounds& i, int r) {
-  if ((long long)a.max_new * r <= view_cols(a.kv.head_dim)) return kAllDecode;
+  if (!a.prompts) return kAllDecode;
   BatchCost c = {};
   add_row(a, i, r, c);
   return mode_of(warp_sum(c));
 }
 __device__ __forceinline__ int block_mode(const AttnArgs& a, int r) {
   __shared__ unsigned long long s_cost[3];
-  if ((long long)a.max_new * r <= view_cols(a.kv.head_dim)) return kAllDecode;
+  if (!a.prompts) return kAllDecode;
   BatchCost c = {};
   for (int b = threadIdx.x; b < a.rows; b += blockDim.x) add_row(a, row_bounds(a, b), r, c);
   if (threadIdx.x < 3) s_cost[threadIdx.x] = 0;
@@ -255,9 +258,11 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
 size_t decode_workspace_bytes(int D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_decode_view(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_decode_join(const AttnArgs& a, cudaStream_t st);  // of units cut between CTAs
 size_t prompt_workspace_bytes(int D);
 cudaError_t launch_prompt(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_prompt_view(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_prompt_join(const AttnArgs& a, cudaStream_t st);
 
 struct TreePlanArgs {
   moe_kv_batch batch;

@@ -15,5 +15,10 @@ cudaError_t launch_decode(const AttnArgs& a, cudaStream_t st) {
                   : D == 128 ? launch<128, false>(a, st) : launch<64, false>(a, st);
 }
 
+cudaError_t launch_decode_join(const AttnArgs& a, cudaStream_t st) {
+  const int D = a.kv.head_dim;
+  return D == 256 ? launch_join<256>(a, st) : D == 128 ? launch_join<128>(a, st) : launch_join<64>(a, st);
+}
+
 }  // namespace kv
 }  // namespace moe

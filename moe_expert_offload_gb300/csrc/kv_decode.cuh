@@ -1079,7 +1079,11 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e == cudaSuccess)
     e = launch_pdl(decode_kernel<D, View>, dim3(kGrid), dim3(C::kThreads), C::kSmem, st, a);
-  if (e != cudaSuccess) return e;
+  return e;
+}
+
+template <int D>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
   return launch_pdl(combine_kernel<D>, dim3(kGrid), dim3(1024), 0, st, a);
 }
 

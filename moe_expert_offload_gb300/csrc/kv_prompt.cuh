@@ -688,26 +688,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             const int open = tree ? base : base + u.tok0 + q_tile * per_tile + 1, shut = last_low(u);
             const uint32_t* bits = a.tree + (size_t)(u.start + t) * a.words + 1;
             const int low = a.window > 0 ? base + (tree ? (int)bits[-1] : t) - a.window + 1 : 0;
-#pragma unroll
+            uint32_t see[2] = {~0u, ~0u};
+#pragma unroll(D == 64 ? 4 : 1)
             for (int q = 0; q < 4; ++q) {
               const int key = tile_of(u, i * (kKeys / kTile) + c0 + q) * kTile;
               if (key + kTile <= open && !is_missing(c0 + q) &&
                   (key >= shut || key + kTile <= a.sinks))
                 continue;
-              uint32_t see = below16(lim - key + 1);
+              uint32_t x = below16(lim - key + 1);
               if (key + kTile > tree0) {
                 const int at = key - tree0;  // -15 and on: the first -at keys are cached ones
                 const int w = max(at, 0) >> 5, words = a.words - 1;
                 const uint32_t lo = w < words ? bits[w] : 0u, hi = w + 1 < words ? bits[w + 1] : 0u;
-                see &= at < 0 ? lo << -at | ((1u << -at) - 1u) : __funnelshift_r(lo, hi, at & 31);
+                x &= at < 0 ? lo << -at | ((1u << -at) - 1u) : __funnelshift_r(lo, hi, at & 31);
               }
               // (a tree's key lies at its depth, not at its place: its bits know of the window)
-              see &= ~(below16(min(low, tree0) - key) & ~below16(a.sinks - key));
-              if (is_missing(c0 + q)) see = 0u;
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (!((see >> k) & 1u)) v[16 * q + k] = 0xFF800000u;
+              x &= ~(below16(min(low, tree0) - key) & ~below16(a.sinks - key));
+              if (is_missing(c0 + q)) x = 0u;
+              const uint32_t gone = ~x & 0xFFFFu;
+              if (q & 2) see[1] &= ~(gone << (q * 16 & 31));
+              else see[0] &= ~(gone << (q * 16 & 31));
             }
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+              if (!((see[k >> 5] >> (k & 31)) & 1u)) v[k] = 0xFF800000u;
           } else {
             const int lim = base + t - i * kKeys;
 #pragma unroll
@@ -1005,9 +1009,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         // (the values' side, which is the last to be needed, brings the queries of the units
         // behind the first one)
         // (eight loads under way spill what its loop over the blocks needs: 853 us instead of 779 for
-        // 2048 tokens on 30000 of head_dim 128)
+        // 2048 tokens on 30000 of head_dim 128; split units, 32 trees of 32 tokens: 123 us with four)
         if (kValues && n_u > 0)
-          load_queries(std::integral_constant<int, 4>{}, wid - kSoftWarps - kSideWarps, n_u);
+          load_queries(std::integral_constant<int, Split ? 2 : 4>{}, wid - kSoftWarps - kSideWarps, n_u);
         load(tile_at(blk0));
         bool lost_now = lost;
         const uint8_t* next = tile_at(blk0 + 1);
@@ -1273,8 +1277,12 @@ cudaError_t launch_kernel(const AttnArgs& a, cudaStream_t st) {
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e == cudaSuccess)
     e = launch_pdl(prompt_kernel<D, View, Split>, dim3(kGrid), dim3(kThreads), C::kSmem, st, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D>, dim3(kGrid, C::kRows * D / 2048), dim3(512), 0, st, a);
+  return e;
+}
+
+template <int D>
+cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
+  return launch_pdl(combine_kernel<D>, dim3(kGrid, Cfg<D>::kRows * D / 2048), dim3(512), 0, st, a);
 }
 
 template <int D, bool View>
