@@ -25,13 +25,12 @@ cudaError_t launch_attention(const AttnArgs& args, cudaStream_t st) {
   const bool view = a.window > 0 || a.tree;
   bool prompts = may_have_prompts(a.kv, a.heads, a.max_new, view);
   if (view && prompts) {
-    // where rows as long as there can be take the decode kernel less than the prompt kernel's fixed
-    // part, all rows are its own
+    // where rows as long as there can be are little work, all rows are the decode kernel's
     int64_t tiles = (int64_t)a.kv.max_blocks * (a.kv.block_tokens / kTile);
     if (a.window > 0) tiles = min(tiles, ((int64_t)a.window + a.max_new + a.sinks) / kTile + 3);
     const int64_t r = a.heads / a.kv.kv_heads;
     const int64_t units = min(a.rows * ((a.max_new * r + 7) / 8), (a.T * r + a.rows * (int64_t)7) / 8);
-    prompts = kDecodeAlone + decode_cost(a.kv.head_dim, a.kv.kv_heads, units, tiles) > kPromptFixed;
+    prompts = decode_cost(a.kv.head_dim, a.kv.kv_heads, units, tiles) > kDecodeAlone;
   }
   a.prompts = prompts;
   AttnArgs p = a;

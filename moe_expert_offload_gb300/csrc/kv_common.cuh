@@ -164,8 +164,11 @@ __host__ __device__ constexpr int view_cols(int D) { return D == 256 ? 16 : D ==
 __host__ __device__ constexpr long long decode_tile_cost(int D) { return D == 256 ? 55 : D == 128 ? 35 : 30; }
 constexpr long long kPromptTileCost = 90;
 __host__ __device__ constexpr int prompt_unit_tiles(int D) { return D == 128 ? 48 : 32; }
-// (a call that launches the prompt kernel and has no row for it, and one that does not)
-constexpr long long kDecodeFixed = 1950000, kDecodeAlone = 1350000;
+constexpr long long kDecodeFixed = 1950000;
+// The host, which knows the rows' number and bounds but not their lengths, leaves the prompt kernel
+// out where the decode kernel's part of such rows is at most this: an idle launch of the prompt
+// kernel costs 6 to 8 us, rows that it would have taken sooner at most about 3.
+constexpr long long kDecodeAlone = 1200000;
 constexpr long long kPromptFixed = 2200000, kBothFixed = 900000;
 enum RowsMode { kByColumns, kAllDecode, kAllPrompt };
 
