@@ -648,7 +648,8 @@ int moe_qkv_store(const moe_kv* kv, const moe_kv_batch* batch, const moe_rope* r
 int moe_kv_load(const moe_kv* kv, const int32_t* slots, int32_t T, void* k, void* v, int32_t* err,
                 moe_stream_t stream);
 
-/* Scratch bytes moe_kv_attention needs; 0 for invalid arguments. */
+/* Scratch bytes moe_kv_attention and moe_kv_attention_view need; 0 for invalid
+ * arguments.  (A causal call of few queries per kv head needs less than this.) */
 size_t moe_kv_attention_workspace_bytes(const moe_kv* kv, int32_t rows, int32_t T, int32_t heads,
                                         int32_t max_new);
 
@@ -757,6 +758,9 @@ int moe_kv_tree_plan(const moe_kv_batch* batch, const moe_kv_view* view, int32_t
  * and the errors are moe_kv_attention's; rows that are trees, chains and prompt
  * chunks mix in one call.  With a tree, moe_kv_tree_plan has been called for this
  * step with this view's window and sinks.
+ * Which of the two kernels takes a row depends on the whole batch's lengths here,
+ * so a token's result may differ by their roundings with the rows that it shares
+ * a call with.
  * Only the tiles of 16 keys that some new token of the row sees are read: the
  * work goes with the window, not with the context.  Keys and values that no new
  * token of the row sees may hold anything, and the table may hold any id for the

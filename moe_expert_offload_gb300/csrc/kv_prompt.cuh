@@ -1140,14 +1140,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       // ----------------------------------------------------- the walk, a job ahead of the others
       Walk w;
       w.left = 0;
-      long long x = 0;  // where the share begins, as a cost within its row
+      long long x = 0, per_head = 0;  // where the share begins, as a cost within its row; one head's cost
       w.b = -1;
       if (mode == kAllDecode) {  // nothing to do
       } else if (a.rows <= 32) {  // a lane per row
         RowBounds bounds = {};
         if (lane < a.rows) bounds = row_bounds(a, lane);
         const Row i = row_info<View>(a, bounds, r, tok, mode);
-        const long long cost = row_cost(i);
+        const Costs costs = costs_of<View>(a, i, tok);
+        const long long head = i.tiles ? cost_before<D, View>(costs, i.tiles) : 0, cost = K * head;
         long long v = cost;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1164,32 +1165,37 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           w.row.n = __shfl_sync(~0u, i.n, w.b);
           w.row.len = __shfl_sync(~0u, i.len, w.b);
           w.row.tiles = __shfl_sync(~0u, i.tiles, w.b);
+          per_head = __shfl_sync(~0u, head, w.b);
+          w.costs = {w.row.len - w.row.n, __shfl_sync(~0u, costs.most, w.b), tok,
+                     __shfl_sync(~0u, costs.full, w.b)};
         }
       } else if (s_row >= 0) {
         w.b = s_row;
         x = s_at;
         w.row = row_info<View>(a, row_bounds(a, w.b), r, tok, mode);
+        w.costs = costs_of<View>(a, w.row, tok);
+        per_head = cost_before<D, View>(w.costs, w.row.tiles);
       }
       w.mode = mode;
       if (w.b >= 0) {
         w.share = share_of();
-        w.costs = costs_of<View>(a, w.row, tok);
         w.left = min(w.share, total - blockIdx.x * w.share);
         // the kv head and the unit that hold it, a lane per candidate
-        const long long per_head = cost_before<D, View>(w.costs, w.row.tiles);
         w.kvh = 0;
         for (int h = 1; h < K; h += 32) w.kvh += __popc(__ballot_sync(~0u, h + lane < K && (h + lane) * per_head <= x));
         x -= w.kvh * per_head;
+        long long before = 0;
         int lo = 0, count = w.row.tiles;
         while (count > 1) {
           const int step = (count + 31) / 32, j = lo + lane * step;
-          const bool fits = lane * step < count && cost_before<D, View>(w.costs, j) <= x;
-          const int k = 31 - __clz(__ballot_sync(~0u, fits));
+          const long long c = cost_before<D, View>(w.costs, j);
+          const int k = 31 - __clz(__ballot_sync(~0u, lane * step < count && c <= x));
+          before = __shfl_sync(~0u, c, k);
           lo += k * step;
           count = min(step, count - k * step);
         }
         w.j = lo;
-        w.at = x - cost_before<D, View>(w.costs, lo);
+        w.at = x - before;
       }
       const int lines = r * D / 64;  // 128 bytes each, of a token's queries
       for (uint32_t k = 0;; ++k) {

@@ -695,6 +695,36 @@ def test_views_on_two_streams_and_in_graphs():
             assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window,kinds", [(0, None), (100, ["any"])])
+def test_results_on_half_sectors(D, window, kinds):
+    """`out` aligned to 16 bytes but not to 32: the same results, and nothing beside them."""
+    c = _case(32, 2, D, 4, [700, 260, 33], [200, 130, 20], window, 4, kinds, 256, seed=41, heavy=14)
+    good = _run(c)
+    room = torch.full((c["q"].numel() + 16,), 5.0, dtype=torch.bfloat16, device=DEV)
+    for at in (8, 16):
+        room.fill_(5.0)
+        out = room[at:at + c["q"].numel()].view(c["q"].shape)
+        assert out.data_ptr() % 32 == (16 if at == 8 else 0)
+        assert torch.equal(_run(c, out=out), good)
+        assert torch.all(room[:at] == 5.0) and torch.all(room[at + c["q"].numel():] == 5.0)
+
+
+def test_steps_without_tokens():
+    """Rows without new tokens, and calls with T = 0 (whose token arrays may be missing)."""
+    c = _case(16, 2, 128, 4, [30, 0, 9], [0, 0, 0], 8, 1, ["any"], 8, seed=43)
+    assert torch.all(_run(c) == 5.0)
+    t = c["tree"]
+    for x in (t.kept, t.drop, t.last):
+        x.fill_(7)
+    none = dict(token=None, next_token=None, path=None)
+    m.moe_kv_tree_accept(c["batch"].c, t.c, 3, 0, kept=t.kept, drop=t.drop, last=t.last, **none)
+    assert [x[:3].tolist() for x in (t.kept, t.drop, t.last)] == [[0] * 3, [0] * 3, [-1] * 3]
+    before = c["kv"].pool.clone()
+    m.moe_kv_tree_keep(c["kv"].layers, c["batch"].c, 3, 2, t.path, t.kept)
+    assert torch.equal(c["kv"].pool, before) and int(c["batch"].err[0]) == 0
+
+
 @pytest.mark.parametrize("news", [[6, 2], [70, 90]])
 def test_views_far_into_a_large_pool(news):
     """A pool of over 4 GB whose last blocks are in use: attention through a view, and kept tokens."""
