@@ -1239,13 +1239,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
 }
 
 // Units that were cut between CTAs, each found at the CTA that began it: a
-// thread per query row and four columns, its parts in order.
+// thread per query row and 16 columns (four at a time, a quarter of the head apart), its parts in
+// order.
 template <int D>
 __global__ void __launch_bounds__(512) combine_kernel(AttnArgs a) {
   using C = Cfg<D>;
   griddep_wait();
   const int first = blockIdx.x, at = blockIdx.y * 512 + threadIdx.x;
-  const int row = at / (D / 4), c = at % (D / 4) * 4;
+  const int row = at / (D / 16), c = at % (D / 16) * 4;
   const Cut cut = static_cast<const Cut*>(a.ws)[first];
   if (cut.last <= first) return;
   const int r = a.heads / a.kv.kv_heads, per_tile = 128 / r, in = row & 127;
@@ -1254,26 +1255,35 @@ __global__ void __launch_bounds__(512) combine_kernel(AttnArgs a) {
   const float* parts = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + kCutBytes);
   float m = kNone, l = 0.0f;  // (raw scores, as the parts have them)
   const float fac = parts[((size_t)first * 2 + 1) * C::kPartial + (size_t)C::kRows * (D + 2) + row];
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+  float4 y[4] = {};
+#pragma unroll 2
   for (int k = first; k <= cut.last; ++k) {
     const float* src = parts + ((size_t)k * 2 + (k == first)) * C::kPartial;
     const float mk = src[(size_t)C::kRows * D + row], lk = src[(size_t)C::kRows * (D + 1) + row];
-    const float4 v = *reinterpret_cast<const float4*>(src + (size_t)row * D + c);
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = *reinterpret_cast<const float4*>(src + (size_t)row * D + c + i * (D / 4));
     const float mm = fmaxf(m, mk), f = ex2((m - mm) * fac), h = ex2((mk - mm) * fac);
     m = mm;
     l = l * f + lk * h;
-    y.x = y.x * f + v.x * h;
-    y.y = y.y * f + v.y * h;
-    y.z = y.z * f + v.z * h;
-    y.w = y.w * f + v.w * h;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i].x = y[i].x * f + v[i].x * h;
+      y[i].y = y[i].y * f + v[i].y * h;
+      y[i].z = y[i].z * f + v[i].z * h;
+      y[i].w = y[i].w * f + v[i].w * h;
+    }
   }
   const float inv = l > 0.0f ? 1.0f / l : l;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x * inv, y.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(y.z * inv, y.w * inv);
-  *reinterpret_cast<uint2*>(a.out + ((int64_t)(cut.start + t) * a.heads + cut.kvh * r + in % r) * D +
-                            c) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                            *reinterpret_cast<const uint32_t*>(&hi));
+  uint16_t* dst = a.out + ((int64_t)(cut.start + t) * a.heads + cut.kvh * r + in % r) * D + c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(y[i].x * inv, y[i].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(y[i].z * inv, y[i].w * inv);
+    *reinterpret_cast<uint2*>(dst + i * (D / 4)) = make_uint2(
+        *reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 }
 
 template <int D, bool View, bool Split>
@@ -1288,7 +1298,7 @@ cudaError_t launch_kernel(const AttnArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_join(const AttnArgs& a, cudaStream_t st) {
-  return launch_pdl(combine_kernel<D>, dim3(kGrid, Cfg<D>::kRows * D / 2048), dim3(512), 0, st, a);
+  return launch_pdl(combine_kernel<D>, dim3(kGrid, Cfg<D>::kRows * D / (16 * 512)), dim3(512), 0, st, a);
 }
 
 template <int D, bool View>
