@@ -22,8 +22,8 @@ namespace kv {
 
 constexpr int kTile = 16;  // tokens of a tile
 constexpr int kGrid = 152; // CTAs of the attention kernels: one per SM
-// Rows of up to this many queries per kv head (new tokens x query heads on it)
-// go through the decode kernel, longer ones through the prompt kernel
+// Causal rows of up to this many queries per kv head (new tokens x query heads on
+// it) go through the decode kernel, longer ones through the prompt kernel
 // (microseconds, decode | prompt, 8 query heads on a kv head; 1 and 16 rows of
 // 2000 to 4000 keys, 4 of 30000 to 60000):
 //   head_dim 256, 32 queries  13 | 24   32 | 33    84 |  76

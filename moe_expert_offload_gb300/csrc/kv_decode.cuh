@@ -35,15 +35,20 @@
 // against 1.6e-3 for bf16 rounding alone): every 16 tiles each group's mean is
 // moved from them into a rounded fp32 sum of its own.
 //
+// View: windows and trees.  A row's walk goes over the key tiles of the sinks and of the window of
+// its tokens, without the gap between them; in stages that hold a hidden key each score is tested
+// by bounds or by its token's bits.
+//
 // Measured: 64 rows of 150 to 8191 keys, 32 query heads on 8 of 128 (330 MB): 76.8 us,
 // 4.3 TB/s; 8 rows of 130000 keys, 16 heads on 2 of 256 (598 MB): 111.5 us, 5.4 TB/s.
+// Through a window of 1024 the first take 35.5 us, through one of 32768 the second 44 us.
 // The stream alone takes 54.7 and 88 us.  A tile takes 321 and 409 instructions: 80
 // and 160 unpack codes (four masks per product of them, and shifts), 18 and 34 are
 // MMAs, the rest is what a stage and a tile cost besides (the copies' bookkeeping,
 // the scan over the values' scales, the growth test, scales and biases).  Neither
 // the issue slots (57 and 43%) nor the ALU pipe (53 and 46%) are full: every warp is
-// one serial chain, and 16 (8) of them on an SM do not cover it.  Spilled: 20, 44 and
-// 56 bytes a thread at head_dim 64, 128 and 256.  Few keys are latency: 1000 keys of
+// one serial chain, and 16 (8) of them on an SM do not cover it.  Spilled: 28, 44 and
+// 60 bytes a thread at head_dim 64, 128 and 256 (View: 76, 164, 52).  Few keys are latency: 1000 keys of
 // one row 11.6 us, about 2 of them the scan over the rows and 2.5 the combine kernel.
 #pragma once
 #include <cstddef>

@@ -8,6 +8,13 @@
 // long row, a causal triangle and ragged batches keep all SMs equally busy;
 // units cut by a share's end are merged afterwards in a fixed order.
 //
+// View: windows and trees.  A unit's blocks are the key tiles of the sinks and of the window of
+// its tokens, without the gap between them; what a token does not see of a block at either end
+// is taken out of its scores, by bounds or by a tree's bits.  Split (View, head_dim 64 and 128):
+// where no row has more queries than one tile, the two tiles take a unit's key blocks in turn,
+// with the same queries, and join their results in the end (32 trees of 32 tokens, 4 heads on one
+// of 8: 106 us, 164 with the second tile empty).
+//
 // One CTA per SM, warp-specialised, blocks handed over with mbarriers:
 //   warps 0-7   softmax: thread = query row.  Scores come from TMEM, weights go
 //               back to TMEM in fp16 over the scores they came from, as the A
@@ -18,9 +25,14 @@
 //   warps 16-23 values alike.  Codes come by 16-byte loads one block ahead, one
 //               LOP3 per pair (1024 + c or 64 + c), the offset taken off exactly,
 //               one fma.  Both land in the 128-byte swizzled layout, the keys read
-//               K-major and the values MN-major by the MMAs.
+//               K-major and the values MN-major by the MMAs.  The values' warps
+//               also bring the next unit's queries, while the softmax is still at
+//               this one's last block and results.
 //   warp 24     issues the MMAs (M = 128, fp32 accumulators in TMEM): the next
 //               block's scores run while the softmax works on this one's.
+//   warp 25     walks over the share and hands out its units, up to four ahead (each
+//               role walking for itself, its code cold: 8192 tokens through a window of
+//               1024 took 235 us, with everything around it, now 205).
 // Registers move from the dequantising warps and the MMA warp's group to the
 // softmax (the CTA starts with 72 a thread; what they add up to is checked below).
 // The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
@@ -34,18 +46,28 @@
 // fp16's range (a score 2^3 to 2^9 above it), so the accumulator in TMEM is rarely
 // rescaled.
 //
-// Measured: 8192 tokens, 16 query heads on 2 of 256: 499 us, 1102 TFLOP/s (57% of a
-// large bf16 matrix product); 2048 tokens on 30000, 32 heads on 4 of 128: 787 us,
-// 1321 TFLOP/s (68%).  The compiler spills 400 to 430 bytes a thread
-// (stack 72 to 120).  Bound by the chain of a block: at head_dim 64 and 128 scores,
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 493 us, 1115 TFLOP/s (57% of a
+// large bf16 matrix product), through a window of 1024 205 us; 2048 tokens on 30000, 32
+// heads on 4 of 128: 783 us, 1328 TFLOP/s (68%), through a window of 4096 144 us, 957
+// TFLOP/s; 32 trees of up to 64 tokens on 150 to 8191 keys, 32 heads on 8 of 128: 166 us.
+// The compiler spills 20 to 120 bytes a thread, 64 to 168 with View.  Bound by the
+// chain of a block: at head_dim 64 and 128 scores,
 // TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
 // takes all the shared memory there is, values freed, dequantised (1400 cycles),
 // fenced (570), seen by the issuer (350) and multiplied (1500).  The tensor pipe is
-// busy 57% (128) and 49% (256) of the time, the issue slots 57 and 59%.  Measured and
+// busy 57% (128) and 49% (256) of the time, the issue slots 57 and 59%; through windows
+// 44 and 32%, 51 and 49%: a unit's ends (queries in 4000 cycles where they are not hidden, results
+// out 4500, a share's first unit 14000, blocks with hidden keys 3000 more than others)
+// weigh on the 9 (33) blocks that it has there, its code for them not in the SM's
+// instruction cache.  Measured and
 // dropped: two tiles with the next scores in halves of 64 keys, the first before
 // the product (975 us then against 876), a warp of its own that issues for each
 // tile (1046); one tile with keys and values handed over by halves of the columns
-// (575 against 516), with a second issuing warp for the products (556).
+// (575 against 516), with a second issuing warp for the products (556); split units among
+// others in one kernel (the flags alone: 861 us for 2048 tokens on 30000 instead of 786);
+// queries by two warps of their own (260 us for the window of 1024), by both dequantising
+// groups (228 instead of 225), with a block's tiles brought to L2 ahead (225 instead of 221 us for
+// 32 trees).
 #pragma once
 #include <climits>
 #include <type_traits>
@@ -63,7 +85,7 @@ using sc::su32;
 
 constexpr int kKeys = 128;  // keys of a block
 constexpr int kSoftWarps = 8, kSideWarps = 8, kMmaWarp = 24;
-constexpr int kThreads = 28 * 32;  // seven warp groups; three warps of the last one idle
+constexpr int kThreads = 28 * 32;  // seven warp groups; two warps of the last one idle
 constexpr int kStartRegs = 72;
 constexpr float kNone = -1e30f;  // below every raw score (q and k in fp16's range: 2^38 at most)
 // Scores this far from zero (in log2) have their reference taken off before they are scaled: the
@@ -104,7 +126,7 @@ struct Row {
   int start, n, len, tiles;  // tiles 0: nothing here
 };
 
-// Whether the row's tokens see each other by a tree's bits.
+// Whether the row's tokens see each other by a tree's bits (longer rows are chains).
 template <bool View>
 __device__ __forceinline__ bool by_tree(const AttnArgs& a, const Row& i) {
   return View && a.tree && i.n <= a.tree_max;

@@ -14,7 +14,10 @@
 // Children find their parents side by side (a minimum in shared memory), the path is then a walk
 // of a few steps.
 //
-// All three are bound by latency: a CTA per row (and layer), a chain of dependent loads.
+// All three are bound by latency: a CTA per row (and layer), a chain of dependent loads.  Measured:
+// the plan of 4 trees of 16 tokens 1.6 us, of 256 trees of up to 256 through a window 4.6 us (33
+// thousand tokens: eight rounds over their bits in shared memory); a path chosen and moved in 8 layers
+// 3.9 us, 64 paths in 40 layers 5.7 us (two kernels each).
 #include <climits>
 
 #include "kv_common.cuh"
