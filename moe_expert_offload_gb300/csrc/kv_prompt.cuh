@@ -1055,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           if (!kValues && half == 0) {
             const uint32_t gone = __ballot_sync(~0u, lost_now);
             if (lane == 0)
-              reinterpret_cast<uint8_t*>(&s_miss[n & 3u])[key >> 5] = (uint8_t)((gone & 1u) | (gone >> 15 & 2u));
+              reinterpret_cast<uint8_t*>(&s_miss[n & 3u])[key >> 5] = (uint8_t)((gone & 0xFFFFu ? 1 : 0) | (gone >> 16 ? 2 : 0));
           }
           fence_async();
           __syncwarp();

@@ -661,6 +661,35 @@ def test_views_leave_out_bad_blocks_and_rows(news, heavy, D):
         _check(c, out, rows=[0])  # (its work may be shared out in another way without row 1's)
 
 
+@pytest.mark.parametrize("heavy", [0, 14])
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 16), (128, 64), (256, 32)])
+@pytest.mark.parametrize("window,sinks,kinds", [(37, 2, None), (200, 20, ["any"]), (150, 0, ["line"])])
+def test_views_without_a_block(heavy, D, P, window, sinks, kinds):
+    """Blocks outside the pool where a row's window begins (within a tile), in its middle, at its end
+    and under its sinks: their keys alone are left out."""
+    lens, news = [900, 523, 333], [5, 90, 30]
+    c = _case(P, 2, D, 4, lens, news, window, sinks, kinds, 256, seed=47, heavy=heavy)
+    for b, (L, n) in enumerate(zip(lens, news)):
+        base = L - n
+        spots = [[max(0, base - window + 1) // P], [(base - 1) // P], [(L - 1) // P, 0]][b]
+        for i in spots:
+            c["kv"].block_table[b, i] = [-1, c["kv"].pool.shape[0], 2 ** 31 - 1][b]
+            c["see"][b][:, i * P:(i + 1) * P] = False
+    out = _run(c)
+    assert int(c["batch"].err[0]) == m.MOE_DERR_KV_INDEX
+    start, pool = 0, _np(c["kv"].pool)
+    for b, (L, n) in enumerate(zip(lens, news)):
+        j = np.arange(L)
+        k, v = ref.read_slots(pool, c["table"][b, j // P] * P + j % P, 2, P, D)
+        q, got, see = _f64(c["q"])[start:start + n], _f64(out)[start:start + n], c["see"][b]
+        left = see.any(1)  # a token that is left without a key is 0
+        assert not got[~left].any()
+        want = tree_ref.attention(q[left], k, v, c["scale"], see[left])
+        tol = ref.attention_bound(q[left], k, v, c["scale"], want)
+        assert np.all(np.abs(got[left] - want) <= tol), b
+        start += n
+
+
 def test_views_on_two_streams_and_in_graphs():
     """Calls side by side on two streams, and two captured calls that share a workspace."""
     a = _case(64, 2, 256, 8, [4000, 900], [1, 9], 500, 4, ["any"], 16, seed=19, heavy=14)
