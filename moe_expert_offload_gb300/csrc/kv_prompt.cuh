@@ -32,7 +32,7 @@
 //               block's scores run while the softmax works on this one's.
 //   warp 25     walks over the share and hands out its units, up to four ahead (each
 //               role walking for itself, its code cold: 8192 tokens through a window of
-//               1024 took 235 us, with everything around it, now 205).
+//               1024 took 235 us, with everything around it, now 196).
 // Registers move from the dequantising warps and the MMA warp's group to the
 // softmax (the CTA starts with 72 a thread; what they add up to is checked below).
 // The columns of a head run in the order 0,4,1,5,2,6,3,7 within every 8 (the
@@ -46,9 +46,9 @@
 // fp16's range (a score 2^3 to 2^9 above it), so the accumulator in TMEM is rarely
 // rescaled.
 //
-// Measured: 8192 tokens, 16 query heads on 2 of 256: 493 us, 1115 TFLOP/s (57% of a
-// large bf16 matrix product), through a window of 1024 205 us; 2048 tokens on 30000, 32
-// heads on 4 of 128: 783 us, 1328 TFLOP/s (68%), through a window of 4096 144 us, 957
+// Measured: 8192 tokens, 16 query heads on 2 of 256: 487 us, 1129 TFLOP/s (58% of a
+// large bf16 matrix product), through a window of 1024 196 us; 2048 tokens on 30000, 32
+// heads on 4 of 128: 780 us, 1333 TFLOP/s (68%), through a window of 4096 144 us, 957
 // TFLOP/s; 32 trees of up to 64 tokens on 150 to 8191 keys, 32 heads on 8 of 128: 166 us.
 // The compiler spills 20 to 120 bytes a thread, 64 to 168 with View.  Bound by the
 // chain of a block: at head_dim 64 and 128 scores,
@@ -110,7 +110,10 @@ struct Cfg {
                                       ((128u >> 4) << 24);  // bit 16: B is MN-major
   static constexpr int kO = D == 256 ? 256 : 128;   // TMEM columns between the tiles' results
   static constexpr int kS = 256;                    // scores: two slots of 128 columns
-  static constexpr int kSoftRegs = D == 256 ? 112 : 136, kSideRegs = D == 256 ? 56 : 48;
+  // (8192 tokens, head_dim 256, through a window of 1024 and causal, us: 96, 64, 48 registers 196 and
+  // 487; 112, 56, 48 200 and 496; 80, 72, 48 201 and 478.  2048 on 30000, 128, through 4096 and
+  // causal: 136, 48, 40 147 and 772; 120, 56, 40 148 and 773; 112, 56, 56 160 and 792)
+  static constexpr int kSoftRegs = D == 256 ? 96 : 136, kSideRegs = D == 256 ? 64 : 48;
   static constexpr int kMmaRegs = D == 256 ? 48 : 40;
   static_assert(kSoftRegs * 256 + kSideRegs * 512 + kMmaRegs * 128 <= kStartRegs * kThreads,
                 "the registers given out are there");
