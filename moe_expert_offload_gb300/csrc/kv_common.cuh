@@ -104,8 +104,10 @@ struct AttnArgs {
   // below `sinks`; the visibility of trees of up to tree_max tokens, `words` of a token
   int window, sinks, tree_max, words;
   const uint32_t* tree;
-  int prompts;  // 0: all rows are the decode kernel's
-  int* mode;  // which kernel takes which rows (RowsMode): the decode kernel finds it, the prompt kernel reads it
+  // View: 0 if all rows are the decode kernel's; which kernel takes which rows (RowsMode), which the
+  // decode kernel finds and the prompt kernel reads
+  int prompts;
+  int* mode;
 };
 
 // What a row's new tokens see of its keys, in whole tiles: the first sink_tiles tiles, then those
@@ -146,20 +148,20 @@ __device__ __forceinline__ RowBounds row_bounds(const AttnArgs& a, int b) {
 // With windows and trees, which kernel takes which rows goes by the whole batch: all rows through
 // the decode kernel, all through the prompt kernel, or those of up to view_cols columns and the
 // others, by what takes least time.  Times are modelled (10 ps a key tile of a unit, a fixed part),
-// with the numbers that choose best among the measured shapes (microseconds, decode | prompt; trees
-// without a window, rows x keys; 224 shapes: 0.5% above the faster one on average, 17% at most):
+// with numbers fitted to measured shapes (microseconds, decode | prompt; trees without a window, rows
+// x keys; over 215 shapes the choice is 1% above the faster kernel on average, 34% at most):
 //   head_dim 256, 8 heads on one of 2    16 columns   24        64        256
-//     1 x 2000                          14 | 22   14 | 23    15 | 25   22 | 28
-//     16 x 1000                         17 | 26   19 | 26    32 | 28  100 | 37
-//     64 x 4000                         66 | 89   90 | 89   205 | 93  743 | 162
+//     1 x 2000                          14 | 22   14 | 22    15 | 25   21 | 27
+//     16 x 1000                         17 | 24   19 | 25    33 | 27  101 | 32
+//     64 x 4000                         64 | 82   90 | 82   200 | 84  727 | 148
 //   head_dim 128, 8 on one of 4
-//     1 x 2000                          16 | 20   16 | 20    17 | 23   22 | 29
-//     16 x 1000                         19 | 28   20 | 28    33 | 29   88 | 40
-//     64 x 4000                         70 | 113  96 | 112  222 | 116 794 | 148
+//     1 x 2000                          17 | 20   17 | 20    17 | 22   24 | 29
+//     16 x 1000                         20 | 26   21 | 27    34 | 28   88 | 38
+//     64 x 4000                         71 | 102  98 | 100  224 | 103 791 | 138
 //   head_dim 64, 8 on one of 8
-//     1 x 2000                          14 | 20   15 | 20    15 | 21   24 | 26
-//     16 x 1000                         19 | 28   23 | 27    39 | 29  105 | 39
-//     64 x 4000                         79 | 139 108 | 138  246 | 141 883 | 203
+//     1 x 2000                          14 | 21   15 | 21    15 | 21   24 | 28
+//     16 x 1000                         19 | 28   22 | 28    39 | 29  105 | 38
+//     64 x 4000                         78 | 140 106 | 140  243 | 142 860 | 210
 __host__ __device__ constexpr int view_cols(int D) { return D == 256 ? 16 : D == 128 ? 24 : 32; }
 __host__ __device__ constexpr long long decode_tile_cost(int D) { return D == 256 ? 55 : D == 128 ? 35 : 30; }
 constexpr long long kPromptTileCost = 90;
