@@ -67,7 +67,9 @@
 // others in one kernel (the flags alone: 861 us for 2048 tokens on 30000 instead of 786);
 // queries by two warps of their own (260 us for the window of 1024), by both dequantising
 // groups (228 instead of 225), with a block's tiles brought to L2 ahead (225 instead of 221 us for
-// 32 trees).
+// 32 trees); warps without a query that leave their rows out (167 instead of 165 us for 32 trees, 150
+// instead of 146 through the window of 4096); split units for rows of up to two tiles (186 instead of
+// 165 us for 32 trees of up to 64 tokens).
 #pragma once
 #include <climits>
 #include <type_traits>
