@@ -690,6 +690,36 @@ def test_views_without_a_block(heavy, D, P, window, sinks, kinds):
         start += n
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("heavy", [0, 14])
+@pytest.mark.parametrize("D,news", [(64, [20, 9, 30]), (128, [20, 9, 30]), (128, [90, 1, 70]), (256, [20, 9, 30])])
+def test_broken_values_and_queries_stay_where_they_are(D, news, heavy, bad):
+    """A value's scale that is NaN or infinite spoils the row that sees it and no other, one outside the
+    window no row; a broken query spoils its own result and no other."""
+    c = _case(16, 2, D, 4, [250, 300, 120], news, 60, 2, ["any"], 200, seed=53, heavy=heavy)
+    good = _run(c)
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16)  # [tile][part][...]
+    G, base = D // 64, 250 - news[0]
+    for at, seen in ((base - 62, False), (base - 5, True)):
+        tile = int(c["table"][0, at // 16]) * 2 + 1  # row 0, kv head 1
+        meta[tile, 2 * 16 * G + at % 16] = bad  # V scale of group 0
+        out = _run(c)
+        assert int(c["batch"].err[0]) == 0
+        _check(c, out, rows=[1, 2])
+        row = out[:news[0]].float()
+        assert torch.isfinite(row[:, :4]).all()
+        assert torch.isfinite(row[:, 4:, :64]).all() != seen
+        if not seen:
+            assert torch.equal(out, good)
+    c = _case(16, 2, D, 4, [250, 300, 120], news, 60, 2, ["any"], 200, seed=53, heavy=heavy)
+    q = c["q"].clone()
+    q[3, 1, 7], q[sum(news) - 1, 5, 0] = bad, bad
+    out = _run(c, q=q)
+    touched = torch.zeros(c["T"], c["H"], dtype=torch.bool, device=DEV)
+    touched[3, 1] = touched[sum(news) - 1, 5] = True
+    assert torch.equal(out[~touched], good[~touched])
+
+
 def test_views_on_two_streams_and_in_graphs():
     """Calls side by side on two streams, and two captured calls that share a workspace."""
     a = _case(64, 2, 256, 8, [4000, 900], [1, 9], 500, 4, ["any"], 16, seed=19, heavy=14)
