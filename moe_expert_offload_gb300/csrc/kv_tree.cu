@@ -15,7 +15,7 @@
 // of a few steps.
 //
 // All three are bound by latency: a CTA per row (and layer), a chain of dependent loads.  Measured:
-// the plan of 4 trees of 16 tokens 1.6 us, of 256 trees of up to 256 through a window 4.6 us (33
+// the plan of 4 trees of 16 tokens 1.6 us, of 256 trees of up to 256 through a window 4.2 us (33
 // thousand tokens: eight rounds over their bits in shared memory); a path chosen and moved in 8 layers
 // 3.9 us, 64 paths in 40 layers 5.7 us (two kernels each).
 #include <climits>
@@ -89,7 +89,6 @@ __global__ void __launch_bounds__(MOE_KV_MAX_TREE) tree_plan_kernel(TreePlanArgs
     }
     buf ^= 1;
   }
-  if (i >= n) return;
   if (left) far = -1;  // further than anybody's first ancestor
   if (far >= 0) {
     // of the tokens out of the window, those at positions below the sinks' end stay
@@ -105,13 +104,30 @@ __global__ void __launch_bounds__(MOE_KV_MAX_TREE) tree_plan_kernel(TreePlanArgs
       bits[w] &= ~out;
     }
   }
-  const int t = r.start + i;
-  a.batch.pos[t] = r.base + depth;
-  uint32_t* to = a.seen + (size_t)t * a.words;
-  to[0] = (uint32_t)depth;
+  if (i < n) a.batch.pos[r.start + i] = r.base + depth;
+  const int words = a.words;
+  if constexpr (W <= 2) {
+    if (i >= n) return;
+    uint32_t* to = a.seen + (size_t)(r.start + i) * words;
+    to[0] = (uint32_t)depth;
 #pragma unroll
-  for (int w = 0; w < W; ++w)
-    if (w + 1 < a.words) to[w + 1] = bits[w];
+    for (int w = 0; w < W; ++w)
+      if (w + 1 < words) to[w + 1] = bits[w];
+  } else {
+    // many words go out in order, a warp's 32 tokens at a time, by way of the other buffer (whose
+    // bits nobody reads any more): 256 trees of up to 256 tokens 4.2 us, 4.6 a token per thread
+    const int lane = i & 31, first_token = i & ~31;
+    uint32_t* out = &s_bits[buf ^ 1][0][0] + first_token * W;
+#pragma unroll
+    for (int w = 0; w < W; ++w) out[lane * W + (w + lane) % W] = bits[w];
+    __syncwarp();
+    uint32_t* to = a.seen + (size_t)(r.start + first_token) * words;
+    const int inv = (65536 + words - 1) / words;  // x * inv >> 16 = x / words for x < 288
+    for (int k = lane; k < min(32, n - first_token) * words; k += 32) {
+      const int j = k * inv >> 16, w = k - j * words;
+      to[k] = w ? out[j * W + (w - 1 + j) % W] : (uint32_t)s_depth[buf][first_token + j];
+    }
+  }
 }
 
 // One CTA per row.
