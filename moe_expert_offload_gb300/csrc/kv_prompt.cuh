@@ -468,9 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   // it replaces, which are never more than one phase of that barrier ago.
   __shared__ __align__(8) uint64_t k_full[S], v_full[S], p_full[NT][2];
   __shared__ __align__(8) uint64_t s_full[NT][2], o_done[NT][2], drained;
-  // a unit's queries are there; by the unit's parity: those of the next one may come before the
-  // softmax has looked for these
-  __shared__ __align__(8) uint64_t q_full[2];
+  // a unit's queries are there; by the job's place, as the factors: those of the next units may come
+  // before a softmax warp has looked for these (of a split unit of one block the second tile's
+  // warps hold nobody up), and a place is filled again only after every warp has given its job back
+  __shared__ __align__(8) uint64_t q_full[kJobs];
   __shared__ __align__(8) uint64_t k_free[S], v_free[S], q_free;  // nothing reads the buffer any more
   __shared__ __align__(8) uint64_t job_full[kJobs], job_free[kJobs];
   __shared__ Job s_job[kJobs];
@@ -478,8 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
   __shared__ long long s_scan[kThreads / 32], s_at;
   __shared__ int s_row;
   __shared__ volatile int s_stop;  // a wait ran out
-  // factors of the rows' scores, of this unit and the next
-  __shared__ float s_fac[2][C::kRows], s_max[2][128], s_sum[2][128];
+  // factors of the rows' scores, by the job's place
+  __shared__ float s_fac[kJobs][C::kRows], s_max[2][128], s_sum[2][128];
   // key tiles of a block that are missing (a block id outside the pool): two bits of each byte, of
   // the last four blocks (the softmax reads a block's before the keys' side writes the fourth
   // behind it, which waits for scores that come after this block's weights)
@@ -514,11 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       bar_init(su32(&p_full[0][0] + i), kSoftWarps / NT);
     }
     for (int i = 0; i < kJobs; ++i) {
+      bar_init(su32(&q_full[i]), kSoftWarps);
       bar_init(su32(&job_full[i]), 1);
       bar_init(su32(&job_free[i]), kTakers);
     }
-    bar_init(su32(&q_full[0]), kSoftWarps);
-    bar_init(su32(&q_full[1]), kSoftWarps);
     bar_init(su32(&q_free), 1);
     bar_init(su32(&drained), 1);
     s_row = -1;
@@ -641,12 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
                           pack_h2(x[3], x[7])));
         // score = fac * accumulated, in units of log2
         if (col8 == 0)
-          s_fac[n_u & 1u][qr] = score_factor(a.scale, 8.8054160e-05f, e);  // log2(e) 2^-14 2^e
+          s_fac[n_u % kJobs][qr] = score_factor(a.scale, 8.8054160e-05f, e);  // log2(e) 2^-14 2^e
       }
     }
     fence_async();
     __syncwarp();
-    if (lane == 0) sc::bar_arrive(su32(&q_full[n_u & 1u]));
+    if (lane == 0) sc::bar_arrive(su32(&q_full[n_u % kJobs]));
   };
 
   if (wid < kSoftWarps) {
@@ -676,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
     for (; !any_of_256(!have); ++n_u) {
       const Job& u = s_job[n_u % kJobs];
       const int q_tile = Split ? 0 : tile;  // the tile of the queries
-      wait_all(&q_full[n_u & 1u], n_u >> 1, s_stop);
-      const float fac = s_fac[n_u & 1u][q_tile * 128 + row];
+      wait_all(&q_full[n_u % kJobs], n_u / kJobs, s_stop);
+      const float fac = s_fac[n_u % kJobs][q_tile * 128 + row];
       // Blocks of which every row of the tile sees every key.
       const int base0 = u.len - u.n, open = is_tree(u) ? base0 : base0 + u.tok0 + q_tile * per_tile + 1;
       int free0 = 0, free1 = open / kKeys;
@@ -1141,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       for (uint32_t n_u = 0; take(n_u); ++n_u) {
         const Job& u = s_job[n_u % kJobs];
         const int nb = u.blk1 - u.blk0;
-        wait_all(&q_full[n_u & 1u], n_u >> 1, s_stop);
+        wait_all(&q_full[n_u % kJobs], n_u / kJobs, s_stop);
         if constexpr (NT == 1) {
           for (int i = 0; i <= nb && !stopped(); ++i) {
             if (i < nb) scores(T0{}, 0, true, true, i + 1 == nb);

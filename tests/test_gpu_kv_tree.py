@@ -616,6 +616,23 @@ def test_views_of_row_counts(B, D, window):
     _check(c, out)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kinds,idle", [(None, 0), (["any", "chain", "bushy"], 100)])
+def test_views_of_many_units_of_one_block(D, kinds, idle):
+    """Hundreds of rows of up to 128 queries per kv head in a short window: their units are one block of
+    keys each, several on a CTA, of which (head_dim 64 and 128) the second query tile has none."""
+    rng = np.random.default_rng(D)
+    news = rng.integers(28, 33, 400).tolist()
+    lens = [n + int(x) for n, x in zip(news, rng.integers(0, 500, 400))]
+    c = _case(16, 2, D, 4, lens, news, 60, 4, kinds, 32, seed=90 + D, idle=idle)
+    out = _run(c)
+    assert int(c["batch"].err[0]) == 0
+    _check(c, out)
+    for _ in range(20):
+        again = _run(c)
+        assert int(c["batch"].err[0]) == 0 and torch.equal(again, out)
+
+
 @pytest.mark.parametrize("size", [1e2, 1e4, 1e9, 1e30])
 @pytest.mark.parametrize("D,news", [(D, n) for D in (64, 128, 256) for n in ([130, 60, 33], [1, 4, 2])])
 @pytest.mark.parametrize("heavy", [0, 14])
