@@ -715,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
             const int tree0 = tree ? base : INT_MAX, lim = tree ? u.len - 1 : base + t;
             const int open = tree ? base : base + u.tok0 + q_tile * per_tile + 1, shut = last_low(u);
             const uint32_t* bits = a.tree + (size_t)(u.start + t) * a.words + 1;
-            const int low = a.window > 0 ? base + (tree ? (int)bits[-1] : t) - a.window + 1 : 0;
+            // (not below 0: with a key taken off it stays within 32 bits, however large the window)
+            const int low = a.window > 0 ? max(base + (tree ? (int)bits[-1] : t) - a.window + 1, 0) : 0;
             uint32_t see[2] = {~0u, ~0u};
 #pragma unroll(D == 64 ? 4 : 1)
             for (int q = 0; q < 4; ++q) {

@@ -487,6 +487,21 @@ def test_trees(i, heavy, idle, poison):
     _check(c, out, rows=range(len(lens) + min(heavy, 1)))
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 2000])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("r,news", [(4, [32, 31, 17, 32]), (4, [60, 40, 256, 200]), (8, [130, 1, 100, 256])])
+@pytest.mark.parametrize("heavy,idle", [(0, 0), (14, 0), (14, 40)])
+def test_trees_under_windows_past_every_position(window, D, r, news, heavy, idle):
+    """Windows up to the largest there is leave everything in a tree's sight: bushy trees and stars, whose late
+    tokens stand far behind their position."""
+    lens = [n + x for n, x in zip(news, (0, 700, 30, 333))]
+    c = _case(16, 2, D, r, lens, news, window, 0, ["star", "bushy", "star", "forest"], 256, seed=61,
+              heavy=heavy, idle=idle)
+    out = _run(c)
+    assert int(c["batch"].err[0]) == 0
+    _check(c, out)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("news", [[1, 2, 1], [90, 3, 70]])
 @pytest.mark.parametrize("heavy", [0, 14])
