@@ -236,12 +236,12 @@ __device__ __forceinline__ bool next_unit(Walk& w, const AttnArgs& a, int r, int
     u.len = w.row.len;
     u.kvh = w.kvh;
     u.tok0 = w.j * tok;
-    u.blocks = (seen + kKeys - 1) / kKeys;
+    u.blocks = (seen - 1) / kKeys + 1;  // (seen + kKeys may pass 2^31 - 1)
     u.low = u.gap = 0;
     if constexpr (View) {
       u.low = first_seen<View>(a, w.row, u.tok0);
       u.gap = sight_of(a, u.low).gap;
-      u.blocks = (seen - u.gap * kTile + kKeys - 1) / kKeys;
+      u.blocks = (seen - u.gap * kTile - 1) / kKeys + 1;
     }
     // both ends of a share fall on the same block for the CTAs on either side
     auto block_at = [&](long long x) {
@@ -678,14 +678,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       const int q_tile = Split ? 0 : tile;  // the tile of the queries
       wait_all(&q_full[n_u % kJobs], n_u / kJobs, s_stop);
       const float fac = s_fac[n_u % kJobs][q_tile * 128 + row];
-      // Blocks of which every row of the tile sees every key.
-      const int base0 = u.len - u.n, open = is_tree(u) ? base0 : base0 + u.tok0 + q_tile * per_tile + 1;
-      int free0 = 0, free1 = open / kKeys;
+      // Blocks of which every row of the tile sees every key.  (A block's end, and that of a tile without
+      // queries, may lie behind 2^31 - 1: unsigned.)
+      const int base0 = u.len - u.n;
+      const uint32_t open = is_tree(u) ? base0 : (uint32_t)base0 + u.tok0 + q_tile * per_tile + 1;
+      int free0 = 0, free1 = (int)(open / kKeys);
       if constexpr (View) {
         constexpr int kTiles = kKeys / kTile;
         // (both ends lie behind the gap)
         free0 = (max(0, (max(last_low(u), 0) + kTile - 1) / kTile - u.gap) + kTiles - 1) / kTiles;
-        free1 = (open / kTile - u.gap) / kTiles;
+        free1 = ((int)(open / kTile) - u.gap) / kTiles;
       }
       // The row's reference, a raw score; a score x weighs 2^(x fac + off), off = 7 - top fac.
       // Where that is far from zero every visible score shall weigh too much (an infinite query's
@@ -713,19 +715,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
           if constexpr (View) {
             const bool tree = is_tree(u);
             const int tree0 = tree ? base : INT_MAX, lim = tree ? u.len - 1 : base + t;
-            const int open = tree ? base : base + u.tok0 + q_tile * per_tile + 1, shut = last_low(u);
+            const uint32_t open = tree ? base : (uint32_t)base + u.tok0 + q_tile * per_tile + 1;
+            const int shut = last_low(u);
             const uint32_t* bits = a.tree + (size_t)(u.start + t) * a.words + 1;
             // (not below 0: with a key taken off it stays within 32 bits, however large the window)
             const int low = a.window > 0 ? max(base + (tree ? (int)bits[-1] : t) - a.window + 1, 0) : 0;
             uint32_t see[2] = {~0u, ~0u};
 #pragma unroll(D == 64 ? 4 : 1)
             for (int q = 0; q < 4; ++q) {
-              const int key = tile_of(u, i * (kKeys / kTile) + c0 + q) * kTile;
-              if (key + kTile <= open && !is_missing(c0 + q) &&
-                  (key >= shut || key + kTile <= a.sinks))
+              // (tiles behind the last position that there can be count as that one's, which no token sees)
+              const int key = min(tile_of(u, i * (kKeys / kTile) + c0 + q), INT_MAX / kTile) * kTile;
+              if ((uint32_t)key + kTile <= open && !is_missing(c0 + q) &&
+                  (key >= shut || key <= a.sinks - kTile))
                 continue;
               uint32_t x = below16(lim - key + 1);
-              if (key + kTile > tree0) {
+              if (tree && key > tree0 - kTile) {
                 const int at = key - tree0;  // -15 and on: the first -at keys are cached ones
                 const int w = max(at, 0) >> 5, words = a.words - 1;
                 const uint32_t lo = w < words ? bits[w] : 0u, hi = w + 1 < words ? bits[w + 1] : 0u;
@@ -993,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
       for (uint32_t n_u = 0; take(n_u); ++n_u) {
         const Job& u = s_job[n_u % kJobs];
         const int len = u.len, blk0 = u.blk0, blk1 = u.blk1, low = u.low;
-        [[maybe_unused]] int sink_keys = 0, gap_keys = 0;
+        [[maybe_unused]] uint32_t sink_keys = 0, gap_keys = 0;
         if constexpr (View) {
           sink_keys = u.gap ? sight_of(a, 0).sink_tiles * kTile : 0;
           gap_keys = u.gap * kTile;
@@ -1005,12 +1009,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(AttnArgs a) {
         bool lost = false;  // what tile_at found last: the tile's block id lies outside the pool
         auto tile_at = [&](int i) -> const uint8_t* {  // the key's tile; null: it is not there
           lost = false;
-          int j = i * kKeys + key;
+          uint32_t j = (uint32_t)i * kKeys + key;  // (may pass 2^31 - 1 behind the row's end)
           if constexpr (View)
             if (j >= sink_keys) j += gap_keys;
-          if (i >= blk1 || j >= len) return nullptr;
+          if (i >= blk1 || j >= (uint32_t)len) return nullptr;
           // (the window's begin within a tile, and behind the sinks: nothing is read there)
-          if (View && j < low && j >= a.sinks) return nullptr;
+          if (View && (int)j < low && (int)j >= a.sinks) return nullptr;
           const int block = table[j >> p_shift];
           if ((unsigned)block >= (unsigned)a.kv.num_blocks) {
             if (!kValues) atomicOr(a.batch.err, MOE_DERR_KV_INDEX);

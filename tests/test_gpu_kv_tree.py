@@ -615,6 +615,51 @@ def test_views_of_long_contexts(P, K, D, r, B, least, most, n, window, sinks, cy
     assert torch.equal(_run(c), out)
 
 
+def _longest(c, cycle):
+    """The case's one row on a table as wide as there can be, over `cycle` blocks of 16 tokens."""
+    kv, width = c["kv"], (2 ** 31 - 1) // 16
+    c["table"] = np.resize(c["table"][0, :cycle].astype(np.int32), (1, width))
+    kv.block_table = torch.tensor(c["table"], device=DEV)
+    kv.c.block_table, kv.c.max_blocks = kv.block_table.data_ptr(), width
+
+
+@pytest.mark.parametrize("D,r,n,window,sinks,kinds", [
+    (64, 16, 1000, 1000, 20, None), (128, 16, 1000, 1000, 20, None), (256, 16, 1000, 1000, 0, None),
+    (128, 32, 256, 500, 4, ["bushy"]), (64, 32, 256, 500, 4, ["star"]), (256, 32, 256, 500, 0, ["forest"]),
+    (128, 8, 1, 1000, 20, None), (256, 4, 5, 300, 0, ["any"]),
+])
+def test_views_up_to_the_last_position(D, r, n, window, sinks, kinds):
+    """Rows that end at the last positions that there can be: what lies behind them passes 2^31 - 1."""
+    cycle = 40
+    c = _wide_case(16, 1, D, r, [n + 900], [n], window, sinks, cycle, 7, kinds)
+    _longest(c, cycle)
+    for less in (0, 1, 16, 47, 84, 112, 128, 300):
+        L = 2 ** 31 - 16 - less
+        c["lens"], c["batch"] = [L], _batch([L], [n], c["T"])
+        if kinds:
+            m.moe_kv_tree_plan(c["batch"].c, c["view"], 1, c["T"])
+        out = _run(c)
+        assert int(c["batch"].err[0]) == 0
+        _check_wide(c, out, window, sinks)
+
+
+def test_a_whole_context_of_the_last_position():
+    """A causal row that sees 2^31 - 16 keys, whose values are all 1.5: so are its results, but for the sums'
+    roundings.  A CTA adds up 2^24 / 152 = 110400 blocks of 128 keys: the weights' sum to the nearest (2^-24
+    each, 0.7%), the products in eight steps that may lose a whole one of 2^-23 (10.5%), and bf16's 2^-8."""
+    D, n, cycle = 64, 8, 40
+    c = _wide_case(16, 1, D, 16, [n + 900], [n], 0, 0, cycle, 7)
+    meta = c["kv"].pool.view(-1, 18 * D)[:, 16 * D:].view(torch.float16)  # scales and biases of K, of V
+    meta[:, 32:48], meta[:, 48:] = 0.0, 1.5
+    _longest(c, cycle)
+    L = 2 ** 31 - 16
+    c["lens"], c["batch"] = [L], _batch([L], [n], c["T"])
+    out = _run(c)
+    assert int(c["batch"].err[0]) == 0
+    assert float((out[:n].float() / 1.5 - 1).abs().max()) <= 0.12
+    assert torch.all(out[n:] == 5.0)
+
+
 @pytest.mark.parametrize("B", [31, 32, 33, 600, 1000])
 @pytest.mark.parametrize("D,window", [(64, 20), (256, 0), (128, 50)])
 def test_views_of_row_counts(B, D, window):
