@@ -198,3 +198,31 @@ def test_the_restatement_on_worked_trees():
     assert tree_ref.accept(parents, [7, 1, 1, 1, 2, 3, 4, 5], [6, 3, 9, 9, 9, 4, 8, 9]) == ([0], 6)
     assert tree_ref.accept(chain, [1, 2, 3], [4, 5, 6]) == ([0, 1, 2], 6)
     assert tree_ref.accept([], [], []) == ([], -1)
+
+
+def test_layers_are_a_list():
+    """A cache's layers join, slice and change like any list, and moe_kv_tree_keep takes them as they are then."""
+    pytest.importorskip("torch")
+    a, b = (m.DeviceKv(2, 4, 6, 16, 1, 64, device="cpu", layers=3) for _ in range(2))
+    assert isinstance(a.layers, list) and a.c is a.layers[0]
+    a.c.max_blocks = 3
+    assert a.layers[0].max_blocks == a.layers.array[0].max_blocks == 3
+    both = a.layers + b.layers
+    assert [x.pool for x in both] == [p.data_ptr() for p in a.pools + b.pools]
+    for x in both:
+        x.pool = PTR  # (128-byte aligned)
+
+    def keep(layers):
+        return _keep(layers, rows=1, T=0)  # launches nothing
+
+    for layers in (a.layers, both, a.layers[1:], tuple(a.layers), a.layers.array):
+        assert keep(layers) == m.MOE_OK
+    b.layers[1].kv_heads = 2  # in place
+    _refused(m.MOE_EINVAL, lambda: keep(b.layers), "layer 1")
+    a.layers[2] = _kv(head_dim=128)  # another struct
+    _refused(m.MOE_EINVAL, lambda: keep(a.layers), "layer 2")
+    a.layers.pop()
+    assert keep(a.layers) == m.MOE_OK
+    a.layers.append(_kv(head_dim=128))
+    a.layers.append(a.layers[0])
+    _refused(m.MOE_EINVAL, lambda: keep(a.layers), "layer 2")
