@@ -149,7 +149,11 @@ __device__ __forceinline__ RowBounds row_bounds(const AttnArgs& a, int b) {
 // the decode kernel, all through the prompt kernel, or those of up to view_cols columns and the
 // others, by what takes least time.  Times are modelled (10 ps a key tile of a unit, a fixed part),
 // with numbers fitted to measured shapes (microseconds, decode | prompt; trees without a window, rows
-// x keys; over 215 shapes the choice is 1% above the faster kernel on average, 34% at most):
+// x keys; over 215 shapes the choice is 1% above the faster kernel on average).  It loses most where both
+// take about as long and the other kernel's idle launch (6 us) comes on top: 34% with one row of 30000 keys and
+// 64 columns (head_dim 256, 8 heads on one of 2: 50, 37 through the decode kernel alone), 30% with 64 rows of 1000
+// keys and 24 columns (the same heads: 47, 36 through the prompt kernel), 25% with 16 rows of 1000 keys and 32
+// columns (head_dim 128, 4 heads on one of 8: 40, 32 through the prompt kernel):
 //   head_dim 256, 8 heads on one of 2    16 columns   24        64        256
 //     1 x 2000                          14 | 22   14 | 22    15 | 25   21 | 27
 //     16 x 1000                         17 | 24   19 | 25    33 | 27  101 | 32
@@ -169,7 +173,9 @@ __host__ __device__ constexpr int prompt_unit_tiles(int D) { return D == 128 ? 4
 constexpr long long kDecodeFixed = 1950000;
 // The host, which knows the rows' number and bounds but not their lengths, leaves the prompt kernel
 // out where the decode kernel's part of such rows is at most this: an idle launch of the prompt
-// kernel costs 6 to 8 us, rows that it would have taken sooner at most about 3.
+// kernel costs 6 to 8 us (12 with cold caches), rows that it would have taken sooner at most about 3.
+// Without a window rows are as long as the block table is wide (a tree of 16 tokens on 1000 keys, 16 heads on 2 of
+// 256: 14 us with a table of up to 10800 tokens, 20.6 with a wider one).
 constexpr long long kDecodeAlone = 1200000;
 constexpr long long kPromptFixed = 2200000, kBothFixed = 900000;
 enum RowsMode { kByColumns, kAllDecode, kAllPrompt };

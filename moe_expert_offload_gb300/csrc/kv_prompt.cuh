@@ -47,11 +47,11 @@
 // rescaled.
 //
 // Measured: 8192 tokens, 16 query heads on 2 of 256: 487 us, 1129 TFLOP/s (58% of a
-// large bf16 matrix product), through a window of 1024 196 us; 2048 tokens on 30000, 32
-// heads on 4 of 128: 780 us, 1333 TFLOP/s (68%), through a window of 4096 144 us, 957
-// TFLOP/s; 32 trees of up to 64 tokens on 150 to 8191 keys, 32 heads on 8 of 128: 166 us.
-// The compiler spills 104 and 120 bytes a thread at head_dim 64 and 128, none at 256 (View: 168,
-// 168 and 20).  Bound by the
+// large bf16 matrix product), through a window of 1024 195 to 202 us; 2048 tokens on 30000, 32
+// heads on 4 of 128: 780 us, 1333 TFLOP/s (68%), through a window of 4096 145 us, 950
+// TFLOP/s; 32 trees of up to 64 tokens on 150 to 8191 keys, 32 heads on 8 of 128: 165 us.
+// The compiler spills 72 and 120 bytes a thread at head_dim 64 and 128, none at 256 (View: 168,
+// 172 and 20; its split form 136 and 136).  Bound by the
 // chain of a block: at head_dim 64 and 128 scores,
 // TMEM load, exponentials, TMEM store, product; at 256, whose one block of values
 // takes all the shared memory there is, values freed, dequantised (1400 cycles),
